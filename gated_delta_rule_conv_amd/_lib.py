@@ -22,11 +22,14 @@ GDN_F32, GDN_BF16 = 0, 1
 GDN_ACT_NONE, GDN_ACT_SILU = 0, 1
 GDN_MMA_AUTO, GDN_MMA_FP32, GDN_MMA_BF16X3 = 0, 1, 2
 GDN_PREFILL_AUTO, GDN_PREFILL_WHOLE, GDN_PREFILL_SEGMENTS = 0, 1, 2
+GDN_PACK_INT8, GDN_PACK_E4M3 = 0, 1
+GDN_TREE_MAX_NODES = 64
 
 EXPORTED = ("gdn_dims_init", "gdn_conv_update", "gdn_prefill_workspace_size", "gdn_prefill_chunked",
             "gdn_prefill_fused_workspace_size", "gdn_prefill_fused", "gdn_prefill_fused_static", "gdn_decode_batched",
             "gdn_decode_fused",
-            "gdn_slot_copy", "gdn_slot_pointers", "gdn_last_error", "gdn_abi_version", "gdn_hbm_probe")
+            "gdn_slot_copy", "gdn_slot_pointers", "gdn_tree_verify", "gdn_tree_accept", "gdn_slot_packed_size",
+            "gdn_slot_pack", "gdn_slot_unpack", "gdn_group_norm", "gdn_last_error", "gdn_abi_version", "gdn_hbm_probe")
 
 
 class gdn_dims(ctypes.Structure):
@@ -55,6 +58,33 @@ def make_dims(num_k_heads: int, num_v_heads: int, head_dim: int, conv_width: int
     """gdn_dims with struct_size set; ``qk_l2norm=False`` sets the struct's qk_l2norm_off."""
     return gdn_dims(ctypes.sizeof(gdn_dims), num_k_heads, num_v_heads, head_dim, conv_width, chunk_size,
                     activation, in_dtype, mma, l2_eps, scale, prefill_form, out_dtype, 0 if qk_l2norm else 1)
+
+
+class gdn_norm_dims(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_int32),
+        ("groups", ctypes.c_int32),
+        ("group_size", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32),
+        ("gate_dtype", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("centered", ctypes.c_int32),
+        ("gate_first", ctypes.c_int32),
+        ("shared_params", ctypes.c_int32),
+        ("eps", ctypes.c_float),
+    ]
+
+
+def make_norm_dims(groups: int, group_size: int, in_dtype: int = GDN_F32, gate_dtype: int = GDN_BF16,
+                   param_dtype: int = GDN_BF16, out_dtype: int = GDN_BF16, activation: int = GDN_ACT_SILU,
+                   centered: bool = False, gate_first: bool = False, shared_params: bool = True,
+                   eps: float = 1e-6) -> gdn_norm_dims:
+    """gdn_norm_dims with struct_size set; the defaults are the layer's output norm (fp32 o,
+    bf16 gate, weight and result, SiLU gate after a root-mean-square norm per v-head)."""
+    return gdn_norm_dims(ctypes.sizeof(gdn_norm_dims), groups, group_size, in_dtype, gate_dtype, param_dtype,
+                         out_dtype, activation, int(centered), int(gate_first), int(shared_params), eps)
 
 
 class GDNError(RuntimeError):
@@ -100,9 +130,16 @@ def _load() -> ctypes.CDLL:
     lib.gdn_decode_fused.argtypes = [D, P, I64, P, P, P, P, P, P, P, P, I32, P]
     lib.gdn_slot_copy.argtypes = [D, P, P, P, P, I32, P]
     lib.gdn_slot_pointers.argtypes = [U64, I64, I32, P, I32, P, P]
+    lib.gdn_tree_verify.argtypes = [D, P, I64, P, P, P, P, P, P, P, I32, I32, I32, P, P, P, P, P, P]
+    lib.gdn_tree_accept.argtypes = [D, P, I64, P, P, P, P, P, P, I32, I32, I32, P, P, P]
+    lib.gdn_slot_packed_size.argtypes = [D, I32, ctypes.POINTER(SZ)]
+    lib.gdn_slot_pack.argtypes = [D, I32, P, P, P, I32, P]
+    lib.gdn_slot_unpack.argtypes = [D, I32, P, P, P, I32, P]
+    lib.gdn_group_norm.argtypes = [ctypes.POINTER(gdn_norm_dims), P, I64, P, I64, P, P, P, I64, I32, P]
     for fn in ("gdn_dims_init", "gdn_conv_update", "gdn_prefill_workspace_size", "gdn_prefill_chunked",
                "gdn_prefill_fused_workspace_size", "gdn_prefill_fused", "gdn_prefill_fused_static", "gdn_decode_batched",
-               "gdn_decode_fused", "gdn_slot_copy", "gdn_slot_pointers"):
+               "gdn_decode_fused", "gdn_slot_copy", "gdn_slot_pointers", "gdn_tree_verify", "gdn_tree_accept",
+               "gdn_slot_packed_size", "gdn_slot_pack", "gdn_slot_unpack", "gdn_group_norm"):
         getattr(lib, fn).restype = ctypes.c_int
     lib.gdn_hbm_probe.argtypes = [P, SZ, ctypes.c_uint32, P]
     lib.gdn_hbm_probe.restype = ctypes.c_int
@@ -248,3 +285,46 @@ def gdn_slot_pointers(pool_base: int, slot_bytes: int, pool_slots: int, slot_idx
     st = _LIB.gdn_slot_pointers(ctypes.c_uint64(pool_base), slot_bytes, pool_slots, _ptr(slot_idx), m,
                                 _ptr(out_ptrs), _stream(stream, slot_idx, out_ptrs))
     _check("gdn_slot_pointers", st)
+
+
+def gdn_tree_verify(dims: gdn_dims, x, x_stride: int, conv_w, conv_b, g, beta, o, parents, cu_nodes, m: int,
+                    total_nodes: int, max_nodes: int, state_ptrs, conv_state_ptrs, k_rec, u_rec, gamma_rec,
+                    stream=None) -> None:
+    st = _LIB.gdn_tree_verify(ctypes.byref(dims), _ptr(x), x_stride, _ptr(conv_w), _ptr(conv_b), _ptr(g), _ptr(beta),
+                              _ptr(o), _ptr(parents), _ptr(cu_nodes), m, total_nodes, max_nodes, _ptr(state_ptrs),
+                              _ptr(conv_state_ptrs), _ptr(k_rec), _ptr(u_rec), _ptr(gamma_rec),
+                              _stream(stream, x, o, state_ptrs))
+    _check("gdn_tree_verify", st)
+
+
+def gdn_tree_accept(dims: gdn_dims, x, x_stride: int, k_rec, u_rec, gamma_rec, parents, cu_nodes, accepted, m: int,
+                    total_nodes: int, max_nodes: int, state_ptrs, conv_state_ptrs, stream=None) -> None:
+    st = _LIB.gdn_tree_accept(ctypes.byref(dims), _ptr(x), x_stride, _ptr(k_rec), _ptr(u_rec), _ptr(gamma_rec),
+                              _ptr(parents), _ptr(cu_nodes), _ptr(accepted), m, total_nodes, max_nodes,
+                              _ptr(state_ptrs), _ptr(conv_state_ptrs), _stream(stream, x, k_rec, state_ptrs))
+    _check("gdn_tree_accept", st)
+
+
+def gdn_slot_packed_size(dims: gdn_dims, fmt: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("gdn_slot_packed_size", _LIB.gdn_slot_packed_size(ctypes.byref(dims), fmt, ctypes.byref(out)))
+    return int(out.value)
+
+
+def gdn_slot_pack(dims: gdn_dims, fmt: int, state_ptrs, conv_state_ptrs, packed_ptrs, n: int, stream=None) -> None:
+    st = _LIB.gdn_slot_pack(ctypes.byref(dims), fmt, _ptr(state_ptrs), _ptr(conv_state_ptrs), _ptr(packed_ptrs), n,
+                            _stream(stream, state_ptrs, packed_ptrs))
+    _check("gdn_slot_pack", st)
+
+
+def gdn_slot_unpack(dims: gdn_dims, fmt: int, packed_ptrs, state_ptrs, conv_state_ptrs, n: int, stream=None) -> None:
+    st = _LIB.gdn_slot_unpack(ctypes.byref(dims), fmt, _ptr(packed_ptrs), _ptr(state_ptrs), _ptr(conv_state_ptrs), n,
+                              _stream(stream, state_ptrs, packed_ptrs))
+    _check("gdn_slot_unpack", st)
+
+
+def gdn_group_norm(dims: gdn_norm_dims, x, x_stride: int, gate, gate_stride: int, weight, bias, y, y_stride: int,
+                   rows: int, stream=None) -> None:
+    st = _LIB.gdn_group_norm(ctypes.byref(dims), _ptr(x), x_stride, _ptr(gate), gate_stride, _ptr(weight), _ptr(bias),
+                             _ptr(y), y_stride, rows, _stream(stream, x, y))
+    _check("gdn_group_norm", st)

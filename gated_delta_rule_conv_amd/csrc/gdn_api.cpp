@@ -218,6 +218,57 @@ gdn_status static_scratch(hipStream_t stream, const char* fn, void** out) {
   return GDN_OK;
 }
 
+// The arguments that gdn_tree_verify and gdn_tree_accept share.
+gdn_status check_tree(const gdn_dims* d, const char* fn, const void* x, int64_t x_stride, const int32_t* cu_nodes,
+                      int32_t m, int32_t total_nodes, int32_t max_nodes, const uint64_t* state_ptrs,
+                      const uint64_t* conv_state_ptrs) {
+  if (max_nodes < 1) return fail(GDN_ERR_SHAPE, "%s: max_nodes must be >= 1 (got %d)", fn, max_nodes);
+  if (max_nodes > GDN_TREE_MAX_NODES)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: trees of %d nodes not built (at most %d)", fn, max_nodes,
+                GDN_TREE_MAX_NODES);
+  if (m > 65535) return fail(GDN_ERR_SHAPE, "%s: m = %d above the grid limit 65535", fn, m);
+  if (!x || !cu_nodes || !state_ptrs || !conv_state_ptrs)
+    return fail(GDN_ERR_NULL, "%s: x, cu_nodes, state_ptrs and conv_state_ptrs are required", fn);
+  const int64_t C = channels(d);
+  const int64_t esz = d->in_dtype == GDN_BF16 ? 2 : 4;
+  if (x_stride < 0 || (total_nodes > 1 && x_stride < C))
+    return fail(GDN_ERR_SHAPE, "%s: x row stride %lld below channel count %lld", fn, static_cast<long long>(x_stride),
+                static_cast<long long>(C));
+  if (!aligned16(x) || (x_stride * esz) % 16)
+    return fail(GDN_ERR_ALIGN, "%s: x must be 16-byte aligned and x_stride a multiple of 16 bytes", fn);
+  return GDN_OK;
+}
+
+// Checks of gdn_slot_packed_size, gdn_slot_pack and gdn_slot_unpack, and their sizes.
+gdn_status check_pack(const gdn_dims* d, int32_t format, const char* fn, gdn::PackArgs* a) {
+  if (gdn_status st = check_dims(d, fn)) return st;
+  if (format != GDN_PACK_INT8 && format != GDN_PACK_E4M3)
+    return fail(GDN_ERR_DTYPE, "%s: unknown pack format %d", fn, format);
+  *a = gdn::PackArgs{};
+  a->rows = d->num_v_heads * d->head_dim;  // (at most the channel count, below 2^24)
+  a->d = d->head_dim;
+  a->e4m3 = format == GDN_PACK_E4M3;
+  a->conv_bytes = (d->conv_width - 1) * channels(d) * (d->in_dtype == GDN_BF16 ? 2 : 4);
+  return GDN_OK;
+}
+
+gdn_status pack_impl(const char* fn, const gdn_dims* dims, int32_t format, const uint64_t* state_ptrs,
+                     const uint64_t* conv_state_ptrs, const uint64_t* packed_ptrs, int32_t n, void* stream,
+                     bool unpack) {
+  gdn::PackArgs a;
+  if (gdn_status st = check_pack(dims, format, fn, &a)) return st;
+  if (n < 0) return fail(GDN_ERR_SHAPE, "%s: negative n", fn);
+  if (n == 0) return GDN_OK;
+  if (n > 65535) return fail(GDN_ERR_SHAPE, "%s: n = %d above the grid limit 65535", fn, n);
+  if (!state_ptrs || !packed_ptrs) return fail(GDN_ERR_NULL, "%s: state_ptrs and packed_ptrs are required", fn);
+  a.state_ptrs = state_ptrs;
+  a.conv_ptrs = conv_state_ptrs;
+  a.packed_ptrs = packed_ptrs;
+  if (!conv_state_ptrs) a.conv_bytes = 0;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  return hip_status(unpack ? gdn::launch_slot_unpack(a, n, s) : gdn::launch_slot_pack(a, n, s), fn);
+}
+
 }  // namespace
 
 extern "C" {
@@ -470,6 +521,165 @@ gdn_status gdn_slot_pointers(uint64_t pool_base, int64_t slot_bytes, int32_t poo
   return hip_status(
       gdn::launch_slot_pointers(pool_base, slot_bytes, pool_slots, slot_idx, m, out_ptrs, static_cast<hipStream_t>(stream)),
       fn);
+}
+
+gdn_status gdn_tree_verify(const gdn_dims* dims, const void* x, int64_t x_stride, const void* conv_w,
+                           const void* conv_b, const float* g, const float* beta, void* o, const int32_t* parents,
+                           const int32_t* cu_nodes, int32_t m, int32_t total_nodes, int32_t max_nodes,
+                           const uint64_t* state_ptrs, const uint64_t* conv_state_ptrs, float* k_rec, float* u_rec,
+                           float* gamma_rec, void* stream) {
+  const char* fn = "gdn_tree_verify";
+  if (gdn_status st = check_dims(dims, fn)) return st;
+  if (m < 0 || total_nodes < 0) return fail(GDN_ERR_SHAPE, "%s: negative m or total_nodes", fn);
+  if (m == 0 && total_nodes != 0) return fail(GDN_ERR_SHAPE, "%s: nodes without slots", fn);
+  if (total_nodes == 0) return GDN_OK;
+  if (gdn_status st = check_tree(dims, fn, x, x_stride, cu_nodes, m, total_nodes, max_nodes, state_ptrs,
+                                 conv_state_ptrs))
+    return st;
+  if (!conv_w || !g || !beta || !o) return fail(GDN_ERR_NULL, "%s: conv_w, g, beta and o are required", fn);
+  const int recs = (k_rec != nullptr) + (u_rec != nullptr) + (gamma_rec != nullptr);
+  if (recs != 0 && recs != 3)
+    return fail(GDN_ERR_NULL, "%s: k_rec, u_rec and gamma_rec come together (all or none)", fn);
+  if (!aligned16(conv_w) || (conv_b && !aligned16(conv_b)) || !aligned16(k_rec) || !aligned16(u_rec))
+    return fail(GDN_ERR_ALIGN, "%s: conv_w, conv_b, k_rec and u_rec must be 16-byte aligned", fn);
+  gdn::TreeArgs a{};
+  a.r = gdn::RecurArgs{nullptr, 0, nullptr, 0, nullptr, 0, g, beta, o, state_ptrs, dims->num_k_heads,
+                       dims->num_v_heads, dims->head_dim, dims->l2_eps, dims->scale,
+                       dims->out_dtype == GDN_BF16, dims->qk_l2norm_off == 0,
+                       dims->num_v_heads / dims->num_k_heads};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.w = conv_w;
+  a.b = conv_b;
+  a.conv_ptrs = conv_state_ptrs;
+  a.parents = parents;
+  a.cu_nodes = cu_nodes;
+  a.k_rec = k_rec;
+  a.u_rec = u_rec;
+  a.gamma_rec = gamma_rec;
+  a.total_nodes = total_nodes;
+  a.max_nodes = max_nodes;
+  a.channels = static_cast<int32_t>(channels(dims));
+  a.width = dims->conv_width;
+  a.silu = dims->activation == GDN_ACT_SILU;
+  a.bf16 = dims->in_dtype == GDN_BF16;
+  return hip_status(gdn::launch_tree_verify(a, m, static_cast<hipStream_t>(stream)), fn);
+}
+
+gdn_status gdn_tree_accept(const gdn_dims* dims, const void* x, int64_t x_stride, const float* k_rec,
+                           const float* u_rec, const float* gamma_rec, const int32_t* parents,
+                           const int32_t* cu_nodes, const int32_t* accepted, int32_t m, int32_t total_nodes,
+                           int32_t max_nodes, const uint64_t* state_ptrs, const uint64_t* conv_state_ptrs,
+                           void* stream) {
+  const char* fn = "gdn_tree_accept";
+  if (gdn_status st = check_dims(dims, fn)) return st;
+  if (m < 0 || total_nodes < 0) return fail(GDN_ERR_SHAPE, "%s: negative m or total_nodes", fn);
+  if (m == 0 && total_nodes != 0) return fail(GDN_ERR_SHAPE, "%s: nodes without slots", fn);
+  if (total_nodes == 0) return GDN_OK;
+  if (gdn_status st = check_tree(dims, fn, x, x_stride, cu_nodes, m, total_nodes, max_nodes, state_ptrs,
+                                 conv_state_ptrs))
+    return st;
+  if (!k_rec || !u_rec || !gamma_rec || !accepted)
+    return fail(GDN_ERR_NULL, "%s: k_rec, u_rec, gamma_rec and accepted are required", fn);
+  if (!aligned16(k_rec) || !aligned16(u_rec))
+    return fail(GDN_ERR_ALIGN, "%s: k_rec and u_rec must be 16-byte aligned", fn);
+  gdn::AcceptArgs a{};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.k_rec = k_rec;
+  a.u_rec = u_rec;
+  a.gamma_rec = gamma_rec;
+  a.parents = parents;
+  a.cu_nodes = cu_nodes;
+  a.accepted = accepted;
+  a.state_ptrs = state_ptrs;
+  a.conv_ptrs = conv_state_ptrs;
+  a.total_nodes = total_nodes;
+  a.max_nodes = max_nodes;
+  a.hk = dims->num_k_heads;
+  a.hv = dims->num_v_heads;
+  a.d = dims->head_dim;
+  a.channels = static_cast<int32_t>(channels(dims));
+  a.width = dims->conv_width;
+  a.bf16 = dims->in_dtype == GDN_BF16;
+  return hip_status(gdn::launch_tree_accept(a, m, static_cast<hipStream_t>(stream)), fn);
+}
+
+gdn_status gdn_slot_packed_size(const gdn_dims* dims, int32_t format, size_t* bytes) {
+  const char* fn = "gdn_slot_packed_size";
+  gdn::PackArgs a;
+  if (gdn_status st = check_pack(dims, format, fn, &a)) return st;
+  if (!bytes) return fail(GDN_ERR_NULL, "%s: bytes is NULL", fn);
+  *bytes = static_cast<size_t>(a.rows) * (a.d + 4) + static_cast<size_t>(a.conv_bytes);
+  return GDN_OK;
+}
+
+gdn_status gdn_slot_pack(const gdn_dims* dims, int32_t format, const uint64_t* state_ptrs,
+                         const uint64_t* conv_state_ptrs, const uint64_t* packed_ptrs, int32_t n, void* stream) {
+  return pack_impl("gdn_slot_pack", dims, format, state_ptrs, conv_state_ptrs, packed_ptrs, n, stream, false);
+}
+
+gdn_status gdn_slot_unpack(const gdn_dims* dims, int32_t format, const uint64_t* packed_ptrs,
+                           const uint64_t* state_ptrs, const uint64_t* conv_state_ptrs, int32_t n, void* stream) {
+  return pack_impl("gdn_slot_unpack", dims, format, state_ptrs, conv_state_ptrs, packed_ptrs, n, stream, true);
+}
+
+gdn_status gdn_group_norm(const gdn_norm_dims* dims, const void* x, int64_t x_stride, const void* gate,
+                          int64_t gate_stride, const void* weight, const void* bias, void* y, int64_t y_stride,
+                          int32_t rows, void* stream) {
+  const char* fn = "gdn_group_norm";
+  if (!dims) return fail(GDN_ERR_NULL, "%s: dims is NULL", fn);
+  if (dims->struct_size != static_cast<int32_t>(sizeof(gdn_norm_dims)))
+    return fail(GDN_ERR_SHAPE, "%s: dims->struct_size is %d, expected %d", fn, dims->struct_size,
+                static_cast<int>(sizeof(gdn_norm_dims)));
+  if (dims->groups < 1 || dims->group_size < 1)
+    return fail(GDN_ERR_SHAPE, "%s: groups and group_size must be >= 1 (%d, %d)", fn, dims->groups, dims->group_size);
+  const int64_t width = static_cast<int64_t>(dims->groups) * dims->group_size;
+  if (width > (1 << 24)) return fail(GDN_ERR_SHAPE, "%s: %lld channels too many", fn, static_cast<long long>(width));
+  for (int32_t t : {dims->in_dtype, dims->gate_dtype, dims->param_dtype, dims->out_dtype})
+    if (t != GDN_F32 && t != GDN_BF16) return fail(GDN_ERR_DTYPE, "%s: unknown dtype %d", fn, t);
+  if (dims->activation != GDN_ACT_NONE && dims->activation != GDN_ACT_SILU)
+    return fail(GDN_ERR_DTYPE, "%s: unknown activation %d", fn, dims->activation);
+  for (int32_t f : {dims->centered, dims->gate_first, dims->shared_params})
+    if (f != 0 && f != 1) return fail(GDN_ERR_DTYPE, "%s: a switch must be 0 or 1 (got %d)", fn, f);
+  if (!(dims->eps >= 0.0f) || !(dims->eps < 1e30f)) return fail(GDN_ERR_SHAPE, "%s: eps must be finite and >= 0", fn);
+  if (rows < 0) return fail(GDN_ERR_SHAPE, "%s: negative rows", fn);
+  if (rows == 0) return GDN_OK;
+  if (!x || !y) return fail(GDN_ERR_NULL, "%s: x and y are required", fn);
+  if (dims->gate_first && !gate) return fail(GDN_ERR_NULL, "%s: gate_first needs a gate", fn);
+  if (x_stride < 0 || y_stride < 0 || (gate && gate_stride < 0)) return fail(GDN_ERR_SHAPE, "%s: negative stride", fn);
+  if (rows > 1 && (x_stride < width || y_stride < width || (gate && gate_stride < width)))
+    return fail(GDN_ERR_SHAPE, "%s: row strides (x %lld, gate %lld, y %lld) below the row width %lld", fn,
+                static_cast<long long>(x_stride), static_cast<long long>(gate_stride),
+                static_cast<long long>(y_stride), static_cast<long long>(width));
+  const auto misaligned = [](const void* p, int32_t dtype) {
+    return (reinterpret_cast<uintptr_t>(p) & (dtype == GDN_BF16 ? 1u : 3u)) != 0;
+  };
+  if (misaligned(x, dims->in_dtype) || misaligned(gate, dims->gate_dtype) || misaligned(weight, dims->param_dtype) ||
+      misaligned(bias, dims->param_dtype) || misaligned(y, dims->out_dtype))
+    return fail(GDN_ERR_ALIGN, "%s: a pointer is not aligned to its type", fn);
+  gdn::NormArgs a{};
+  a.x = x;
+  a.x_stride = x_stride;
+  a.gate = gate;
+  a.gate_stride = gate_stride;
+  a.weight = weight;
+  a.bias = bias;
+  a.y = y;
+  a.y_stride = y_stride;
+  a.rows = rows;
+  a.groups = dims->groups;
+  a.size = dims->group_size;
+  a.x_bf16 = dims->in_dtype == GDN_BF16;
+  a.gate_bf16 = dims->gate_dtype == GDN_BF16;
+  a.param_bf16 = dims->param_dtype == GDN_BF16;
+  a.y_bf16 = dims->out_dtype == GDN_BF16;
+  a.silu = dims->activation == GDN_ACT_SILU;
+  a.centered = dims->centered;
+  a.gate_first = dims->gate_first;
+  a.shared = dims->shared_params;
+  a.eps = dims->eps;
+  return hip_status(gdn::launch_group_norm(a, static_cast<hipStream_t>(stream)), fn);
 }
 
 }  // extern "C"

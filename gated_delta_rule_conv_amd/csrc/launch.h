@@ -114,4 +114,89 @@ hipError_t launch_slot_copy(const uint64_t* src, const uint64_t* dst, int64_t by
 hipError_t launch_slot_pointers(uint64_t base, int64_t slot_bytes, int32_t pool_slots, const int32_t* idx,
                                 int32_t m, uint64_t* out, hipStream_t s);
 
+// A tree of drafted tokens per slot (gdn_tree_verify).
+struct TreeArgs {
+  RecurArgs r;  // g, beta, o, state_ptrs and the layer's sizes (q, k, v unused)
+  const void* x;
+  int64_t x_stride;
+  const void* w;
+  const void* b;  // nullable
+  const uint64_t* conv_ptrs;
+  const int32_t* parents;  // nullable (chains)
+  const int32_t* cu_nodes;
+  float* k_rec;      // nullable, all three or none
+  float* u_rec;
+  float* gamma_rec;
+  int32_t total_nodes;
+  int32_t max_nodes;
+  int32_t channels;
+  int32_t width;
+  int32_t silu;
+  int32_t bf16;
+};
+
+hipError_t launch_tree_verify(const TreeArgs& a, int32_t m, hipStream_t s);
+
+struct AcceptArgs {
+  const void* x;
+  int64_t x_stride;
+  const float* k_rec;
+  const float* u_rec;
+  const float* gamma_rec;
+  const int32_t* parents;  // nullable (chains)
+  const int32_t* cu_nodes;
+  const int32_t* accepted;
+  const uint64_t* state_ptrs;
+  const uint64_t* conv_ptrs;
+  int32_t total_nodes;
+  int32_t max_nodes;
+  int32_t hk;
+  int32_t hv;
+  int32_t d;
+  int32_t channels;
+  int32_t width;
+  int32_t bf16;
+};
+
+hipError_t launch_tree_accept(const AcceptArgs& a, int32_t m, hipStream_t s);
+
+// 8-bit snapshots: a block is codes (hv d d bytes), scales (hv d fp32), conv state (conv_bytes).
+struct PackArgs {
+  const uint64_t* state_ptrs;
+  const uint64_t* conv_ptrs;  // nullable
+  const uint64_t* packed_ptrs;
+  int32_t rows;  // hv * d state rows of d values
+  int32_t d;
+  int32_t e4m3;
+  int64_t conv_bytes;  // 0 when conv_ptrs is null
+};
+
+hipError_t launch_slot_pack(const PackArgs& a, int32_t n, hipStream_t s);
+hipError_t launch_slot_unpack(const PackArgs& a, int32_t n, hipStream_t s);
+
+struct NormArgs {
+  const void* x;
+  int64_t x_stride;
+  const void* gate;  // nullable
+  int64_t gate_stride;
+  const void* weight;  // nullable
+  const void* bias;    // nullable
+  void* y;
+  int64_t y_stride;
+  int32_t rows;
+  int32_t groups;
+  int32_t size;
+  int32_t x_bf16;
+  int32_t gate_bf16;
+  int32_t param_bf16;
+  int32_t y_bf16;
+  int32_t silu;
+  int32_t centered;
+  int32_t gate_first;
+  int32_t shared;
+  float eps;
+};
+
+hipError_t launch_group_norm(const NormArgs& a, hipStream_t s);
+
 }  // namespace gdn

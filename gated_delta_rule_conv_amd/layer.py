@@ -7,8 +7,9 @@ device arrays of 64-bit block addresses that gdn_slot_pointers builds on the dev
 and conv state in such a pool of slots; aprender #5279, "Phase plan", phase P5, puts
 the slot index on the launch grid and hands the kernels one address per slot.)
 
-``conv_update``, ``prefill``, ``decode`` and ``decode_fused`` derive pointers, strides and views from
-torch tensors and call the library; all arithmetic happens in the HIP kernels.
+``conv_update``, ``prefill``, ``decode``, ``decode_fused``, ``tree_verify``, ``tree_accept``,
+``slot_pack``, ``slot_unpack`` and ``group_norm`` derive pointers, strides and views from torch
+tensors and call the library; all arithmetic happens in the HIP kernels.
 """
 
 from __future__ import annotations
@@ -75,6 +76,39 @@ class SlotPool:
                            dc if conv_state else None, n, stream)
 
 
+    def pack_slots(self, slot_idx: torch.Tensor, packed: torch.Tensor, fmt: int, conv_state: bool = True,
+                   stream=None) -> None:
+        """8-bit snapshots: slot slot_idx[i] into row i of packed (from packed_slots())."""
+        sp, cp = self.pointers(slot_idx)
+        slot_pack(self.dims, fmt, sp, cp if conv_state else None, _block_pointers(packed, slot_idx), stream)
+
+    def unpack_slots(self, packed: torch.Tensor, block_idx: torch.Tensor, slot_idx: torch.Tensor, fmt: int,
+                     conv_state: bool = True, stream=None) -> None:
+        """Slot slot_idx[i] filled from row block_idx[i] of packed (int32 device index tensors;
+        one block may fill several slots)."""
+        assert block_idx.numel() == slot_idx.numel()
+        sp, cp = self.pointers(slot_idx)
+        slot_unpack(self.dims, fmt, _block_pointers(packed, slot_idx, block_idx), sp, cp if conv_state else None,
+                    stream)
+
+
+def packed_slots(dims: gdn_dims, n: int, fmt: int, device="cuda") -> torch.Tensor:
+    """Room for n 8-bit snapshots: uint8 [n, gdn_slot_packed_size]."""
+    return torch.zeros((n, _lib.gdn_slot_packed_size(dims, fmt)), dtype=torch.uint8, device=device)
+
+
+def _block_pointers(packed: torch.Tensor, slot_idx: torch.Tensor, block_idx=None) -> torch.Tensor:
+    """Device addresses of packed's rows block_idx (default: 0, 1, ..), 0 outside it."""
+    assert packed.dtype == torch.uint8 and packed.dim() == 2 and packed.is_contiguous()
+    n = slot_idx.numel()
+    if block_idx is None:
+        block_idx = torch.arange(n, dtype=torch.int32, device=slot_idx.device)
+    assert block_idx.dtype == torch.int32 and block_idx.is_cuda
+    out = torch.empty(n, dtype=torch.int64, device=slot_idx.device)
+    _lib.gdn_slot_pointers(packed.data_ptr(), packed.shape[1], packed.shape[0], block_idx, n, out)
+    return out
+
+
 def qkv_views(dims: gdn_dims, y: torch.Tensor):
     """q, k, v views of the conv output y [T, C] (channels [q | k | v])."""
     hk = dims.num_k_heads * dims.head_dim
@@ -129,6 +163,63 @@ def decode_fused(dims: gdn_dims, x: torch.Tensor, conv_w: torch.Tensor, conv_b, 
                           conv_state_out_ptrs, state_ptrs.numel(), stream)
 
 
+def tree_record(dims: gdn_dims, total_nodes: int, device="cuda"):
+    """What tree_verify leaves for tree_accept: fp32 (k [T, Hk, d], u [T, Hv, d], gamma [T, Hv])."""
+    Hk, Hv, d = dims.num_k_heads, dims.num_v_heads, dims.head_dim
+    return (torch.empty((total_nodes, Hk, d), dtype=torch.float32, device=device),
+            torch.empty((total_nodes, Hv, d), dtype=torch.float32, device=device),
+            torch.empty((total_nodes, Hv), dtype=torch.float32, device=device))
+
+
+def _check_tree(x, parents, cu_nodes, state_ptrs) -> None:
+    assert x.stride(-1) == 1 and cu_nodes.dtype == torch.int32 and cu_nodes.numel() == state_ptrs.numel() + 1
+    assert parents is None or (parents.dtype == torch.int32 and parents.numel() == x.shape[0])
+
+
+def tree_verify(dims: gdn_dims, x: torch.Tensor, conv_w: torch.Tensor, conv_b, g: torch.Tensor, beta: torch.Tensor,
+                o: torch.Tensor, parents, cu_nodes: torch.Tensor, max_nodes: int, state_ptrs: torch.Tensor,
+                conv_state_ptrs: torch.Tensor, record=None, stream=None) -> None:
+    """The drafted trees of m slots answered against their states, which stay as they are;
+    parents None: chains. record (from tree_record()) is needed to accept nodes afterwards."""
+    _check_tree(x, parents, cu_nodes, state_ptrs)
+    assert g.is_contiguous() and beta.is_contiguous() and o.is_contiguous()
+    assert g.shape[0] == beta.shape[0] == o.shape[0] == x.shape[0]
+    k, u, gamma = record if record is not None else (None, None, None)
+    _lib.gdn_tree_verify(dims, x, x.stride(0), conv_w, conv_b, g, beta, o, parents, cu_nodes, state_ptrs.numel(),
+                         x.shape[0], max_nodes, state_ptrs, conv_state_ptrs, k, u, gamma, stream)
+
+
+def tree_accept(dims: gdn_dims, x: torch.Tensor, record, parents, cu_nodes: torch.Tensor, max_nodes: int,
+                accepted: torch.Tensor, state_ptrs: torch.Tensor, conv_state_ptrs: torch.Tensor, stream=None) -> None:
+    """Slot i's state and conv state moved along the root path of node accepted[i] (-1: none)."""
+    _check_tree(x, parents, cu_nodes, state_ptrs)
+    assert accepted.dtype == torch.int32 and accepted.numel() == state_ptrs.numel()
+    k, u, gamma = record
+    _lib.gdn_tree_accept(dims, x, x.stride(0), k, u, gamma, parents, cu_nodes, accepted, state_ptrs.numel(),
+                         x.shape[0], max_nodes, state_ptrs, conv_state_ptrs, stream)
+
+
+def slot_pack(dims: gdn_dims, fmt: int, state_ptrs: torch.Tensor, conv_state_ptrs, packed_ptrs: torch.Tensor,
+              stream=None) -> None:
+    _lib.gdn_slot_pack(dims, fmt, state_ptrs, conv_state_ptrs, packed_ptrs, state_ptrs.numel(), stream)
+
+
+def slot_unpack(dims: gdn_dims, fmt: int, packed_ptrs: torch.Tensor, state_ptrs: torch.Tensor, conv_state_ptrs,
+                stream=None) -> None:
+    _lib.gdn_slot_unpack(dims, fmt, packed_ptrs, state_ptrs, conv_state_ptrs, state_ptrs.numel(), stream)
+
+
+def group_norm(dims, x: torch.Tensor, weight, y: torch.Tensor, gate=None, bias=None, stream=None) -> None:
+    """y = the norm of every group of every row of x, times weight, plus bias, gated (dims from
+    make_norm_dims()). Rows are the first axis; the other axes of x, gate and y are contiguous."""
+    width = dims.groups * dims.group_size
+    for t in (x, y, gate):
+        assert t is None or (t.numel() == x.shape[0] * width and t.stride(-1) == 1 and
+                             (t.dim() == 2 or (t.dim() == 3 and t.stride(1) == t.shape[2])))
+    _lib.gdn_group_norm(dims, x, x.stride(0), gate, 0 if gate is None else gate.stride(0), weight, bias, y,
+                        y.stride(0), x.shape[0], stream)
+
+
 def prefill_workspace(dims: gdn_dims, num_seqs: int, total_tokens: int, device="cuda") -> torch.Tensor:
     nbytes = _lib.gdn_prefill_workspace_size(dims, num_seqs, total_tokens)
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
@@ -139,6 +230,7 @@ def prefill_fused_workspace(dims: gdn_dims, num_seqs: int, total_tokens: int, de
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
-__all__ = ["SlotPool", "channels", "conv_update", "decode", "decode_fused", "prefill", "prefill_fused",
-           "prefill_fused_static", "prefill_fused_workspace", "prefill_workspace", "qkv_views", "torch_in_dtype",
+__all__ = ["SlotPool", "channels", "conv_update", "decode", "decode_fused", "group_norm", "packed_slots", "prefill",
+           "prefill_fused", "prefill_fused_static", "prefill_fused_workspace", "prefill_workspace", "qkv_views",
+           "slot_pack", "slot_unpack", "torch_in_dtype", "tree_accept", "tree_record", "tree_verify",
            "GDN_F32", "GDN_BF16"]

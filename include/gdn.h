@@ -52,7 +52,7 @@ typedef enum gdn_status {
                               precision policy, prefill form, or a 0/1 switch) */
   GDN_ERR_ALIGN = 4,       /* a pointer or stride breaks the 16-byte alignment rule */
   GDN_ERR_WORKSPACE = 5,   /* workspace NULL or smaller than gdn_prefill_workspace_size */
-  GDN_ERR_UNSUPPORTED = 6, /* valid but not built: head dim, chunk size or conv width */
+  GDN_ERR_UNSUPPORTED = 6, /* valid but not built: head dim, chunk size, conv width or tree size */
   GDN_ERR_HIP = 7          /* the HIP runtime failed the launch */
 } gdn_status;
 
@@ -339,6 +339,133 @@ gdn_status gdn_slot_pointers(uint64_t pool_base, int64_t slot_bytes, int32_t poo
  */
 gdn_status gdn_slot_copy(const gdn_dims* dims, const uint64_t* src_state_ptrs, const uint64_t* dst_state_ptrs,
                          const uint64_t* src_conv_ptrs, const uint64_t* dst_conv_ptrs, int32_t n, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * gdn_tree_verify -- speculative decoding: one forward pass of the layer over a tree of
+ * drafted tokens per slot, read against the slot's state and conv state, which stay as they
+ * are. Node i of a slot's tree is answered as if its root path (its ancestors, then itself)
+ * were the next tokens of the sequence:
+ *   y_i  the conv of gdn_conv_update over [conv state, x of the root path], at its end;
+ *   S_i = exp(g_i) S_p(i) (I - beta_i k_i k_i^T) + beta_i v_i k_i^T,  o_i = S_i q_i,
+ * with p(i) its parent and S of "no parent" the slot's state. Siblings do not see each other.
+ * Computed without forming any S_i: with G_i the sum of g over the root path,
+ *   u_i = beta_i (v_i - e^G_i S k_i) - beta_i sum_{j above i} e^(G_i - G_j) (k_i . k_j) u_j
+ *   o_i = e^G_i S q_i + sum_{j above or at i} e^(G_i - G_j) (q_i . k_j) u_j.
+ *
+ *  x          [total_nodes][C] in_dtype, row stride x_stride; conv_w, conv_b as gdn_conv_update.
+ *  g, beta    [total_nodes][Hv] fp32.   o: [total_nodes][Hv][d] in dims->out_dtype.
+ *  parents    device int32 [total_nodes]: the parent's number inside its own tree, or -1 for a
+ *             node that continues the slot itself (there may be several). Parents come before
+ *             their children; an entry outside [-1, own number) is read as -1.
+ *             NULL: every tree is a chain (node i's parent is i - 1).
+ *  cu_nodes   device int32 [m+1]; slot i owns rows [cu_nodes[i], cu_nodes[i+1]), possibly none.
+ *  max_nodes  the largest tree of the call, 1 .. 64 (GDN_TREE_MAX_NODES). Rows of a tree beyond
+ *             its first max_nodes, and rows outside [0, total_nodes), are not touched.
+ *  state_ptrs, conv_state_ptrs  device u64 [m], read only; an entry of 0 in either marks an
+ *             inactive slot (nothing read or written for it). Two slots may share a state here.
+ *  k_rec, u_rec, gamma_rec  the record gdn_tree_accept needs, all three or none: fp32
+ *             [total_nodes][Hk][d] (normalised k), [total_nodes][Hv][d] (u) and
+ *             [total_nodes][Hv] (G).
+ * Each slot's result is the same bits whatever else is in the call. The products with the state
+ * and between the tokens are as exact as fp32 ones whatever dims->mma is.
+ *  Alignment: x, conv_w, conv_b, k_rec, u_rec 16-byte aligned, x_stride a multiple of 16 bytes.
+ *  Errors: GDN_ERR_UNSUPPORTED for max_nodes above GDN_TREE_MAX_NODES; else as gdn_decode_fused.
+ */
+#define GDN_TREE_MAX_NODES 64
+gdn_status gdn_tree_verify(const gdn_dims* dims, const void* x, int64_t x_stride, const void* conv_w,
+                           const void* conv_b, const float* g, const float* beta, void* o, const int32_t* parents,
+                           const int32_t* cu_nodes, int32_t m, int32_t total_nodes, int32_t max_nodes,
+                           const uint64_t* state_ptrs, const uint64_t* conv_state_ptrs, float* k_rec, float* u_rec,
+                           float* gamma_rec, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * gdn_tree_accept -- the step after gdn_tree_verify: moves each slot to its accepted node a,
+ *   S <- e^G_a S + sum_{j above or at a} e^(G_a - G_j) u_j k_j^T,
+ * and its conv state to the last K-1 rows of [conv state, x of a's root path], both in place:
+ * the state and conv state that decoding the path token by token would leave (to rounding; the
+ * conv state bit for bit).
+ *
+ *  x, parents, cu_nodes, m, total_nodes, max_nodes  as given to gdn_tree_verify.
+ *  k_rec, u_rec, gamma_rec  its record (read only).
+ *  accepted   device int32 [m]: the last accepted node's number inside its tree; -1, or any
+ *             number the tree does not have, accepts nothing: the slot keeps its bits.
+ *  state_ptrs, conv_state_ptrs  device u64 [m], distinct slots; an entry of 0 in either marks an
+ *             inactive slot.
+ *  Alignment and errors as gdn_tree_verify.
+ */
+gdn_status gdn_tree_accept(const gdn_dims* dims, const void* x, int64_t x_stride, const float* k_rec,
+                           const float* u_rec, const float* gamma_rec, const int32_t* parents,
+                           const int32_t* cu_nodes, const int32_t* accepted, int32_t m, int32_t total_nodes,
+                           int32_t max_nodes, const uint64_t* state_ptrs, const uint64_t* conv_state_ptrs,
+                           void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * 8-bit snapshots: gdn_slot_copy with the snapshot held in a quarter of the state's bytes
+ * (0.57 MiB instead of 2.05 MiB for a 16/32-head, d = 128 bf16 layer).
+ *
+ * A snapshot is one block of gdn_slot_packed_size bytes, 16-byte aligned:
+ *   codes  [Hv][d][d] of one byte, scales [Hv][d] fp32 (one per state row), conv state
+ *   [K-1][C] in_dtype, one after the other.
+ * With a = the largest magnitude of a state row and M = 127 (INT8) or 448 (E4M3):
+ *   scale = a / M,   code = round(x * (M * (1 / a))) to the nearest integer (INT8: two's
+ *   complement) or to the nearest OCP e4m3 value (E4M3), ties to even, every operation rounded to
+ *   fp32 once;  read back: x = scale * code.
+ * Rows with a < 2^-100 are held as zeros (scale 0). A row with a NaN or an infinity in it gets a NaN
+ * scale and zero codes, so all of it reads back as NaN. The conv state is kept bit for bit.
+ */
+typedef enum gdn_pack_format { GDN_PACK_INT8 = 0, GDN_PACK_E4M3 = 1 } gdn_pack_format;
+
+/* gdn_slot_packed_size -- bytes of one snapshot block (a multiple of 16), written to *bytes. */
+gdn_status gdn_slot_packed_size(const gdn_dims* dims, int32_t format, size_t* bytes);
+
+/* ---------------------------------------------------------------------------------
+ * gdn_slot_pack -- for i < n, write slot i's state and conv state into the block at
+ * packed_ptrs[i].   gdn_slot_unpack -- the reverse: fill slot i from the block at packed_ptrs[i].
+ *
+ *  state_ptrs, packed_ptrs  device u64 [n].
+ *  conv_state_ptrs          device u64 [n], or NULL: the conv part of the blocks is neither
+ *             read nor written.
+ *  Entry i is skipped as a whole when any of its pointers is 0. All addresses 16-byte aligned.
+ *  Unchecked precondition: destinations are distinct from one another and overlap no source (one
+ *  block may fill several slots).
+ */
+gdn_status gdn_slot_pack(const gdn_dims* dims, int32_t format, const uint64_t* state_ptrs,
+                         const uint64_t* conv_state_ptrs, const uint64_t* packed_ptrs, int32_t n, void* stream);
+gdn_status gdn_slot_unpack(const gdn_dims* dims, int32_t format, const uint64_t* packed_ptrs,
+                           const uint64_t* state_ptrs, const uint64_t* conv_state_ptrs, int32_t n, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * gdn_group_norm -- the norm over each group of channels of each token, with the activation and
+ * the gate: what follows o in the layer, where a group is a v-head (groups = Hv,
+ * group_size = d) and the gate the z projection. For the group_size values x of a group:
+ *   n = x / sqrt(mean(x^2) + eps),  or, centered:  n = (x - mean(x)) / sqrt(var(x) + eps)
+ *   y = (n * weight + bias) * act(gate)        with a gate
+ *   y = act(n * weight + bias)                 without
+ *   y = n' * weight + bias, n' the norm of x * act(gate)      gate_first
+ * No statistic crosses tokens, so prefill and decode rows give the same bits.
+ */
+typedef struct gdn_norm_dims {
+  int32_t struct_size;   /* sizeof(gdn_norm_dims) as compiled by the caller */
+  int32_t groups;        /* >= 1 */
+  int32_t group_size;    /* >= 1, groups * group_size <= 2^24 */
+  int32_t in_dtype;      /* gdn_dtype of x */
+  int32_t gate_dtype;    /* gdn_dtype of gate */
+  int32_t param_dtype;   /* gdn_dtype of weight and bias */
+  int32_t out_dtype;     /* gdn_dtype of y (bf16: rounded to nearest even) */
+  int32_t activation;    /* gdn_activation */
+  int32_t centered;      /* 0: root mean square; 1: mean taken off first */
+  int32_t gate_first;    /* 0: gate after the norm; 1: before it (needs a gate) */
+  int32_t shared_params; /* 0: weight and bias [groups * group_size]; 1: [group_size] for all groups */
+  float eps;             /* finite, >= 0 */
+} gdn_norm_dims;
+
+/*  x, gate, y  [rows][groups * group_size] with row strides (elements), any alignment of their
+ *              type; gate NULL for none. y overlaps no input.
+ *  weight      see shared_params; NULL: 1.   bias: same shape; NULL: 0.
+ */
+gdn_status gdn_group_norm(const gdn_norm_dims* dims, const void* x, int64_t x_stride, const void* gate,
+                          int64_t gate_stride, const void* weight, const void* bias, void* y, int64_t y_stride,
+                          int32_t rows, void* stream);
 
 /* Thread-local text describing the last non-OK status returned on this thread. */
 const char* gdn_last_error(void);
