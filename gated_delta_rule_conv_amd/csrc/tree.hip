@@ -50,39 +50,106 @@ __device__ __forceinline__ int xcd_head() {
   return (n % 8 == 0) ? (b % 8) * (n / 8) + b / 8 : b;
 }
 
+// fp16 operands that carry an fp32 value in two halves: hi = fp16(x), lo = fp16(x - hi), about 22
+// significant bits. A product is hi hi' + hi lo' + lo hi' on v_mfma_f32_16x16x32_f16 with fp32
+// accumulation; what is left out is 2^-22 of it at most, typically 2^-24, as an fp32 product's own
+// rounding. fp16 has little range, so every row is first multiplied by a power of two (exact) that
+// puts its norm (or largest value) at 2^11 .. 2^13, and the result by its inverse: parts below fp16's
+// normal range are then under 2^-25 of the row.
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
+
+struct Half2 {
+  f16x8 hi, lo;
+};
+
+__device__ __forceinline__ void mma_f16x3(f32x4& acc, const Half2& a, const Half2& b) {
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.lo, b.hi, acc, 0, 0, 0);
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.lo, acc, 0, 0, 0);
+  acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.hi, acc, 0, 0, 0);
+}
+
+// The exponent that takes a magnitude below 2^e to below 2^13 (kept where its inverse is finite too).
+__device__ __forceinline__ int f16_shift(int e) { return e < -97 ? 110 : 13 - e; }
+
+// x * mul (mul a power of two, or a factor whose product with x is wanted to 22 bits) in two halves,
+// one instruction a half: fp16(x mul + 0) and fp16(x mul - hi).
+__device__ __forceinline__ _Float16 half_hi(float x, float mul) { return static_cast<_Float16>(fmaf(x, mul, 0.0f)); }
+__device__ __forceinline__ _Float16 half_lo(float x, float mul, _Float16 hi) {
+  return static_cast<_Float16>(fmaf(x, mul, -static_cast<float>(hi)));
+}
+
+__device__ __forceinline__ void barrier_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
 // One workgroup per (slot, v-head), one wave per 16 state rows; NB = blocks of 16 nodes.
 //
 // The rows of the state do not mix, so with K, Q [N][d] the normalised tokens and S the wave's 16
-// rows everything is small matrix products, on 16x16 fp32 MFMA tiles whose contraction index runs
-// as 4 (l / 16) + r: the tile of a result (lane l: rows 4 (l / 16) + r of column l % 16) is then the
-// right operand of the next product as it stands.
+// rows everything is small matrix products on 16x16 tiles:
 //   M = K S^T, W = Q S^T               [N][16]
 //   A_ij = -beta_i e^(G_i - G_j) k_i.k_j for j above i, else 0;   P_ij = e^(G_i - G_j) q_i.k_j, j above or at i
 //   U = (I - A)^-1 (beta (V - e^G M)), O = e^G W + P U
 // (I - A) is unit lower triangular (parents come first): its 16x16 diagonal blocks are inverted by
-// substitution, the rest is block substitution on MFMA.
+// substitution, the rest is block substitution. The products with d terms (M, W, A, P) run on fp16
+// pairs, the others on fp32 MFMA with the contraction index dealt as 4 (l / 16) + r, so that a result
+// tile (lane l: rows 4 (l / 16) + r of column l % 16) is the right operand of the next product as it stands.
+//
+// Everything a workgroup reads from memory is loaded before anything is computed: its state rows
+// (registers), the x rows of its nodes and the conv-state rows before them (LDS, as they came; the conv
+// then gathers each node's window there), parents, g and beta. The barriers order LDS only, so the state
+// rows stay in flight across them.
 //
 // A zero of A or P times an infinity or a NaN would carry a broken token into branches that do not
 // see it. So such values never enter the products: a k that is not finite marks its node, a right
 // side beta (v - e^G M) that is not finite marks its node for that state row, zeros go in their
 // place, and the results of the marked nodes and their descendants are set to NaN at the end.
+template <typename T, int K, int D, int NB>
+struct VerifyLds {
+  static constexpr int N = 16 * NB;
+  static constexpr int KS = D + 16;  // fp16 values of a row of K and Q (conflict-free fragment reads)
+  static constexpr int PS = N + 4;   // floats of a row of A and P
+  static constexpr int XS = 2 * D + 16 / sizeof(T);  // values of a row of x's q and k channels of the head
+  static constexpr int VS = D + 16 / sizeof(T);      // ... and of its v channels
+  struct Products {
+    float a[N][PS];       // A
+    float p[N][PS];       // P
+    float t[NB][16][20];  // inverses of the diagonal blocks
+  };
+  // rows of x: the conv-state rows, oldest first, then the nodes'
+  union {
+    T x[K - 1 + N][XS];
+    Products m;  // (written once the conv is done with x)
+  };
+  union {
+    T xv[K - 1 + N][VS];
+    _Float16 qk[2][2][N][KS];  // q, k; hi, lo; inside a row see place() (written once v is convolved)
+  };
+  float inv[2][N];           // inverse of the row's power of two, q and k
+  float gam[N], eg[N], beta[N];
+  uint32_t anc[N][2];         // ancestors (bit j: node j), not itself
+  uint32_t kbad[2], qbad[2];  // nodes whose k (q) is not finite
+};
+
+// Where value k of a row of q or k lies in LDS: a lane's 8 values of a 32-wide MFMA step are adjacent. The
+// step's contraction index is dealt to the lane group c = l / 16 as {4 c + 0..3, 16 + 4 c + 0..3}, the
+// columns that two 16-byte state loads bring.
+__device__ __forceinline__ constexpr int place(int k) {
+  return (k / 32) * 32 + ((k % 16) / 4) * 8 + ((k % 32) / 16) * 4 + k % 4;
+}
+
 template <typename T, int K, int D, int NB, bool SILU>
-__global__ __launch_bounds__(D * 4) void tree_verify_kernel(TreeArgs a) {
+__global__ __launch_bounds__(D * 4, (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_verify_kernel(TreeArgs a) {
+  using Lds = VerifyLds<T, K, D, NB>;
   constexpr int W = D / 16;          // waves
   constexpr int NT = W * kWave;      // threads (4 D)
   constexpr int N = 16 * NB;
-  constexpr int KS = D + 4;          // floats of an LDS row of K and Q
-  constexpr int PS = N + 4;          // floats of an LDS row of A and P
-  constexpr int CH = 2 * D / 8;      // 8-channel pieces of a node's k-head channels (q, then k)
-  __shared__ __attribute__((aligned(16))) float qk_l[2][N][KS];  // q^, k^
-  __shared__ __attribute__((aligned(16))) float a_l[N][PS];      // A
-  __shared__ __attribute__((aligned(16))) float p_l[N][PS];      // P
-  __shared__ __attribute__((aligned(16))) float t_l[NB][16][20]; // inverses of the diagonal blocks
-  __shared__ float gam_l[N], eg_l[N], beta_l[N];
-  __shared__ uint32_t anc_l[N][2];                               // ancestors (bit j: node j), not itself
-  __shared__ uint32_t kbad_l[2], qbad_l[2];                      // nodes whose k (q) is not finite
-  __shared__ int par_l[N];
-  __shared__ int win_l[N][3];  // the rows before node i, newest first: a node, or -1 - r for conv-state row r
+  constexpr int CH = 2 * D / 4;      // 4-channel pieces of a node's q and k channels
+  using Raw = typename Vec8<T>::Raw;
+  using V4 = Vec4<T>;
+  __shared__ __attribute__((aligned(16))) Lds lds;
 
   const RecurArgs& r = a.r;
   const int i = blockIdx.y;
@@ -99,37 +166,59 @@ __global__ __launch_bounds__(D * 4) void tree_verify_kernel(TreeArgs a) {
   const int h = j / r.group;
   const int C = a.channels;
 
+  // every wave: lane t's parent (the root for lanes past the tree)
+  const int par = lane < n ? parent_of(a.parents, first, lane) : -1;
+  const float gval = w == 0 && lane < n ? r.g[static_cast<int64_t>(first + lane) * r.hv + j] : 0.f;
+  const float bval = w == 0 && lane < n ? r.beta[static_cast<int64_t>(first + lane) * r.hv + j] : 0.f;
+  // x and conv-state rows, on their way to LDS
+  const T* x = static_cast<const T*>(a.x) + static_cast<int64_t>(first) * a.x_stride;
+  const T* cs = reinterpret_cast<const T*>(cp);
+  constexpr int LX = D / 2;                // lanes on one row (3 D / 8 of them with a piece)
+  constexpr int RW = W * kWave / LX;       // rows a pass
+  constexpr int IT = (K - 1 + N + RW - 1) / RW;
+  const int px = (lane % LX) * 8;          // the lane's channels within the head's q | k | v
+  const int rx = w * (kWave / LX) + (kWave == LX ? 0 : lane / LX);
+  const int chx = px < D ? h * D + px : px < 2 * D ? (r.hk - 1 + h) * D + px : (2 * r.hk - 2 + j) * D + px;
+  Raw raw[IT];
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int row = it * RW + rx;
+    if (row < K - 1 + n && px < 3 * D)
+      raw[it] = Vec8<T>::load_raw((row < K - 1 ? cs + static_cast<int64_t>(row) * C : x + (row - (K - 1)) * a.x_stride) + chx);
+  }
+  // taps of the lane's v channel, and of the thread's 4 q or k channels
+  const int vch = (2 * r.hk + j) * D + w * 16 + l16;
+  T vtap[K], vbias;
+#pragma unroll
+  for (int t = 0; t < K; ++t) vtap[t] = static_cast<const T*>(a.w)[static_cast<int64_t>(vch) * K + t];
+  vbias = static_cast<const T*>(a.b ? a.b : a.w)[vch];  // (taps stand in when there is no bias)
+  const int piece = tid % CH;
+  const bool is_k = piece * 4 >= D;
+  const int d0 = (piece * 4) % D;
+  const int ch0 = (is_k ? r.hk * D : 0) + h * D + d0;
+  typename V4::Raw tap[K], bias;
+#pragma unroll
+  for (int t = 0; t < K; ++t) tap[t] = V4::load_raw(static_cast<const T*>(a.w) + static_cast<int64_t>(ch0) * K + 4 * t);
+  bias = V4::load_raw(static_cast<const T*>(a.b ? a.b : a.w) + ch0);
   // the wave's state rows: lane (c4, l16) holds columns 16 e + 4 c4 .. + 3 of row l16
   const gf32x4* S = (const gf32x4*)(reinterpret_cast<const float*>(sp) +
                                     (static_cast<int64_t>(j) * D + w * 16 + l16) * D);
   f32x4 s[D / 16];
 #pragma unroll
   for (int e = 0; e < D / 16; ++e) s[e] = __builtin_nontemporal_load(S + 4 * e + c4);
-
-  if (tid < N) {
-    const bool live = tid < n;
-    par_l[tid] = live ? parent_of(a.parents, first, tid) : -1;
-    const int64_t gi = static_cast<int64_t>(first + tid) * r.hv + j;
-    gam_l[tid] = live ? r.g[gi] : 0.f;
-    beta_l[tid] = live ? r.beta[gi] : 0.f;
-  }
-  if (tid < 2) kbad_l[tid] = qbad_l[tid] = 0;
-  __syncthreads();
-  if (tid < N) {
-    // walk K-1 rows back: nodes up to the root, then conv-state rows, newest (K-2) first
-    int at = par_l[tid], row = K - 2;
+  __builtin_amdgcn_sched_barrier(0);  // every load above is issued before the first wait
+  if (tid < 2) lds.kbad[tid] = lds.qbad[tid] = 0;
 #pragma unroll
-    for (int t = 0; t < K - 1; ++t) {
-      win_l[tid][t] = at >= 0 ? at : -1 - row;
-      if (at >= 0) at = par_l[at];
-      else --row;
-    }
+  for (int it = 0; it < IT; ++it) {
+    const int row = it * RW + rx;
+    if (row < K - 1 + n && px < 3 * D) *reinterpret_cast<Raw*>(px < 2 * D ? &lds.x[row][px] : &lds.xv[row][px - 2 * D]) = raw[it];
   }
+
   if (w == 0) {
     // ancestors and sums of g along the root path by doubling: after round s they cover 2^s levels
-    const bool live = lane < N;
-    int up = live ? par_l[lane] : -1;
-    float gam = live ? gam_l[lane] : 0.f;
+    const int64_t gi = static_cast<int64_t>(first + lane) * r.hv + j;
+    int up = par;
+    float gam = gval;
     uint32_t lo = up >= 0 && up < 32 ? 1u << up : 0u, hi = up >= 32 ? 1u << (up - 32) : 0u;
 #pragma unroll
     for (int s2 = 1; s2 < N; s2 *= 2) {
@@ -144,174 +233,197 @@ __global__ __launch_bounds__(D * 4) void tree_verify_kernel(TreeArgs a) {
         up = up2;
       }
     }
-    if (live) {
-      anc_l[lane][0] = lo;
-      anc_l[lane][1] = hi;
-      gam_l[lane] = gam;
-      eg_l[lane] = expf(gam);
-      if (lane < n && a.gamma_rec) a.gamma_rec[static_cast<int64_t>(first + lane) * r.hv + j] = gam;
+    if (lane < N) {
+      lds.anc[lane][0] = lo;
+      lds.anc[lane][1] = hi;
+      lds.gam[lane] = gam;
+      lds.eg[lane] = expf(gam);
+      lds.beta[lane] = bval;
+      if (lane < n && a.gamma_rec) a.gamma_rec[gi] = gam;
     }
   }
-  __syncthreads();
+  barrier_lds();
 
-  const T* x = static_cast<const T*>(a.x) + static_cast<int64_t>(first) * a.x_stride;
-  const T* cs = reinterpret_cast<const T*>(cp);
-  // q and k of every node: a thread convolves 8 channels (always the same ones) of one node a
-  // pass, 2 D / 8 threads a node
+  // lane t: the LDS rows of the K-1 rows before node t, 8 bits each, the nearest one lowest
+  int back = 0;
   {
-    const int piece = tid % CH;
-    const bool is_k = piece * 8 >= D;
-    const int d0 = (piece * 8) % D;
-    const int ch0 = (is_k ? r.hk * D : 0) + h * D + d0;
-    ConvTaps<T, K> taps;
-    taps.load(static_cast<const T*>(a.w), static_cast<const T*>(a.b), ch0);
+    int at = lane + K - 1;
 #pragma unroll
-    for (int pass = 0; pass < N / (NT / CH); ++pass) {
-      const int t = pass * (NT / CH) + tid / CH;
-      float y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-      if (t < n) {
-        float win[K - 1][8], cur[8];
-#pragma unroll
-        for (int q = 0; q < K - 1; ++q) {
-          const int at = win_l[t][K - 2 - q];
-          Vec8<T>::load(at >= 0 ? x + at * a.x_stride + ch0 : cs + static_cast<int64_t>(-1 - at) * C + ch0, win[q]);
-        }
-        Vec8<T>::load(x + t * a.x_stride + ch0, cur);
-        taps.apply(win, cur, SILU, y);
-      }
-      float ss = 0.f;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) ss = fmaf(y[e], y[e], ss);
-      ss = group_sum<D / 8>(ss);
-      float f = r.qk_norm && t < n ? 1.0f / sqrtf(ss + r.eps) : 1.0f;
-      if (!is_k) f *= r.scale;
-#pragma unroll
-      for (int e = 0; e < 8; ++e) y[e] *= f;
-      if (t < n && is_k && a.k_rec && j % r.group == 0)
-        Vec8<float>::store(a.k_rec + (static_cast<int64_t>(first + t) * r.hk + h) * D + d0, y);
-      if (!(ss < __builtin_inff())) {  // (the node's threads agree on ss)
-        float bad = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) bad += y[e] * 0.f;
-        if (group_sum<D / 8>(bad) != 0.f) {
-          atomicOr(&(is_k ? kbad_l : qbad_l)[t >> 5], 1u << (t & 31));
-#pragma unroll
-          for (int e = 0; e < 8; ++e) y[e] = 0.f;
-        }
-      }
-      float* dst = &qk_l[is_k ? 1 : 0][t][d0];
-      *reinterpret_cast<float4*>(dst) = make_float4(y[0], y[1], y[2], y[3]);
-      *reinterpret_cast<float4*>(dst + 4) = make_float4(y[4], y[5], y[6], y[7]);
+    for (int t = 0; t < K - 1; ++t) {
+      const int up = __shfl(par, at >= K - 1 ? at - (K - 1) : 0);
+      at = at >= K - 1 ? K - 1 + up : at - 1;  // (parent -1 is row K-2, the newest conv-state row)
+      back |= at << (8 * t);
     }
   }
   // v of the lane's nodes (4 c4 + 0..3 of every block) at its state row
   float v[NB][4];
-  {
-    const int ch = (2 * r.hk + j) * D + w * 16 + l16;
-    float tap[K];
 #pragma unroll
-    for (int t = 0; t < K; ++t) tap[t] = elem_f32<T>(static_cast<const T*>(a.w)[static_cast<int64_t>(ch) * K + t]);
-    const float bias = a.b ? elem_f32<T>(static_cast<const T*>(a.b)[ch]) : 0.f;
+  for (int b = 0; b < NB; ++b)
 #pragma unroll
-    for (int b = 0; b < NB; ++b)
+    for (int e = 0; e < 4; ++e) {
+      const int t = 16 * b + 4 * c4 + e;
+      const int rows = __shfl(back, t);
+      const int off = w * 16 + l16;
+      float acc = a.b ? elem_f32<T>(vbias) : 0.f;
 #pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        const int t = 16 * b + 4 * c4 + e;
-        v[b][e] = 0.f;
-        if (t < n) {
-          float acc = bias;
+      for (int q = 0; q < K - 1; ++q)
+        acc = fmaf(elem_f32<T>(vtap[q]), elem_f32<T>(lds.xv[(rows >> (8 * (K - 2 - q))) & 255][off]), acc);
+      acc = fmaf(elem_f32<T>(vtap[K - 1]), elem_f32<T>(lds.xv[K - 1 + t][off]), acc);
+      v[b][e] = t < n ? (SILU ? silu(acc) : acc) : 0.f;
+    }
+  barrier_lds();
+  // q and k: a thread convolves 4 channels (always the same ones) of one node a pass, 8 nodes a pass
 #pragma unroll
-          for (int q = 0; q < K - 1; ++q) {
-            const int at = win_l[t][K - 2 - q];
-            acc = fmaf(tap[q], elem_f32<T>(at >= 0 ? x[at * a.x_stride + ch] : cs[static_cast<int64_t>(-1 - at) * C + ch]),
-                       acc);
-          }
-          acc = fmaf(tap[K - 1], elem_f32<T>(x[t * a.x_stride + ch]), acc);
-          v[b][e] = SILU ? silu(acc) : acc;
-        }
+  for (int pass = 0; pass < N / (NT / CH); ++pass) {
+    const int t = pass * (NT / CH) + tid / CH;
+    const int rows = __shfl(back, t);
+    float y[4] = {0.f, 0.f, 0.f, 0.f};
+    if (t < n) {
+      const int off = (is_k ? D : 0) + d0;
+      typename V4::Raw win[K - 1];
+#pragma unroll
+      for (int q = 0; q < K - 1; ++q) win[q] = V4::load_raw(&lds.x[(rows >> (8 * (K - 2 - q))) & 255][off]);
+      conv4_raw<T, K>(tap, bias, a.b != nullptr, win, V4::load_raw(&lds.x[K - 1 + t][off]), SILU, y);
+    }
+    const auto row_sum = [](float z) {  // over the D / 4 lanes of a row
+      z = group_sum<(D / 4 < 16 ? D / 4 : 16)>(z);
+      if constexpr (D / 4 > 16) z += __shfl_xor(z, 16);
+      return z;
+    };
+    float ss = 0.f;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) ss = fmaf(y[e], y[e], ss);
+    ss = row_sum(ss);
+    float f = r.qk_norm && t < n ? __builtin_amdgcn_rsqf(ss + r.eps) : 1.0f;
+    if (!is_k) f *= r.scale;
+    if (t < n && is_k && a.k_rec && j % r.group == 0)
+      *reinterpret_cast<f32x4*>(a.k_rec + (static_cast<int64_t>(first + t) * r.hk + h) * D + d0) =
+          f32x4{y[0] * f, y[1] * f, y[2] * f, y[3] * f};
+    if (!(ss < __builtin_inff())) {  // (the row's threads agree on ss)
+      if (row_sum((y[0] * 0.f + y[1] * 0.f) + (y[2] * 0.f + y[3] * 0.f)) != 0.f) {
+        atomicOr(&(is_k ? lds.kbad : lds.qbad)[t >> 5], 1u << (t & 31));
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = 0.f;
+        f = 0.f;
       }
+    }
+    const int sh = f16_shift((__builtin_amdgcn_frexp_expf(ss * f * f) + 1) >> 1);  // (|row| < 2^((e + 1) / 2))
+    if (d0 == 0) lds.inv[is_k][t] = ldexpf(1.0f, -sh);
+    const float mul = ldexpf(f, sh);
+    f16x4 hi, lo;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      hi[e] = half_hi(y[e], mul);
+      lo[e] = half_lo(y[e], mul, hi[e]);
+    }
+    *reinterpret_cast<f16x4*>(&lds.qk[is_k][0][t][place(d0)]) = hi;
+    *reinterpret_cast<f16x4*>(&lds.qk[is_k][1][t][place(d0)]) = lo;
   }
-  __syncthreads();
+  barrier_lds();
 
-  // A and P: the lower blocks of k k^T and q k^T, dealt to the waves
+  const auto frag = [&](int which, int b, int step) {
+    const int at = step * 32 + c4 * 8;
+    return Half2{*reinterpret_cast<const f16x8*>(&lds.qk[which][0][16 * b + l16][at]),
+                 *reinterpret_cast<const f16x8*>(&lds.qk[which][1][16 * b + l16][at])};
+  };
+  // A and P: the lower blocks of k k^T and q k^T, dealt to the waves, A's diagonal blocks first;
+  // the wave that has one inverts it (lane c < 16 forms column c)
   {
     constexpr int NL = NB * (NB + 1) / 2;
     for (int task = w; task < 2 * NL; task += W) {
       const bool is_p = task >= NL;
-      int bi = 0, rest = is_p ? task - NL : task;
-      while (rest > bi) rest -= ++bi;  // block row bi, block column rest
-      const int bj = rest;
+      int bi, bj;
+      if (task < NB) {
+        bi = bj = task;
+      } else {  // the other blocks of A by rows, then P's
+        int rest = is_p ? task - NL : task - NB;
+        bi = is_p ? 0 : 1;
+        while (rest >= (is_p ? bi + 1 : bi)) rest -= is_p ? ++bi : bi++;
+        bj = rest;
+      }
       f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-      for (int e = 0; e < D / 16; ++e) {
-        const f32x4 left = *reinterpret_cast<const f32x4*>(&qk_l[is_p ? 0 : 1][16 * bi + l16][16 * e + 4 * c4]);
-        const f32x4 right = *reinterpret_cast<const f32x4*>(&qk_l[1][16 * bj + l16][16 * e + 4 * c4]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(left[q], right[q], acc, 0, 0, 0);
-      }
+      for (int e = 0; e < D / 32; ++e) mma_f16x3(acc, frag(is_p ? 0 : 1, bi, e), frag(1, bj, e));
       const int col = 16 * bj + l16;
-      const float gcol = gam_l[col];
+      const float gcol = lds.gam[col], icol = lds.inv[1][col];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int row = 16 * bi + 4 * c4 + q;
-        const bool above = (anc_l[row][col >> 5] >> (col & 31)) & 1u;
+        const bool above = (lds.anc[row][col >> 5] >> (col & 31)) & 1u;
         const bool use = above || (is_p && row == col);
-        const float f = use ? expf(gam_l[row] - gcol) * (is_p ? 1.0f : -beta_l[row]) : 0.f;
-        (is_p ? p_l : a_l)[row][col] = use ? f * acc[q] : 0.f;
+        const float f = use ? expf(lds.gam[row] - gcol) * (is_p ? 1.0f : -lds.beta[row]) : 0.f;
+        (is_p ? lds.m.p : lds.m.a)[row][col] = use ? f * (acc[q] * lds.inv[is_p ? 0 : 1][row] * icol) : 0.f;
+      }
+      if (task < NB) {
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+        __builtin_amdgcn_wave_barrier();
+        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+        if (lane < 16) {
+          float cl[16];
+#pragma unroll
+          for (int q = 0; q < 16; ++q) {
+            float x2 = q == lane ? 1.0f : 0.0f;
+#pragma unroll
+            for (int t = 0; t < q; ++t) x2 = fmaf(lds.m.a[16 * bi + q][16 * bi + t], cl[t], x2);
+            cl[q] = x2;
+            lds.m.t[bi][q][lane] = x2;
+          }
+        }
       }
     }
   }
-  __syncthreads();
-  // inverses of the diagonal blocks: lane 16 b + c of the first wave forms column c of block b
-  if (w == 0 && lane < N) {
-    const int b = lane / 16;
-    float col[16];
-#pragma unroll
-    for (int q = 0; q < 16; ++q) {
-      float acc = q == l16 ? 1.0f : 0.0f;
-#pragma unroll
-      for (int t = 0; t < q; ++t) acc = fmaf(a_l[16 * b + q][16 * b + t], col[t], acc);
-      col[q] = acc;
-      t_l[b][q][l16] = acc;
-    }
-  }
-  // M and W
+  // the state rows as fp16 pairs, then M and W
   f32x4 m[NB], o[NB];
 #pragma unroll
   for (int b = 0; b < NB; ++b) m[b] = o[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+  float top = 0.f;
 #pragma unroll
   for (int e = 0; e < D / 16; ++e)
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      const f32x4 qf = *reinterpret_cast<const f32x4*>(&qk_l[0][16 * b + l16][16 * e + 4 * c4]);
-      const f32x4 kf = *reinterpret_cast<const f32x4*>(&qk_l[1][16 * b + l16][16 * e + 4 * c4]);
+    for (int q = 0; q < 4; ++q) top = fmaxf(top, fabsf(s[e][q]));
+  top = fmaxf(top, __shfl_xor(top, 16));
+  top = fmaxf(top, __shfl_xor(top, 32));
+  const int sh = f16_shift(__builtin_amdgcn_frexp_expf(top));
+  const float sinv = ldexpf(1.0f, -sh), smul = ldexpf(1.0f, sh);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        m[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(kf[q], s[e][q], m[b], 0, 0, 0);
-        o[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(qf[q], s[e][q], o[b], 0, 0, 0);
-      }
+  for (int e = 0; e < D / 32; ++e) {
+    Half2 sf;
+#pragma unroll
+    for (int q = 0; q < 8; ++q) {
+      sf.hi[q] = half_hi(s[2 * e + q / 4][q % 4], smul);
+      sf.lo[q] = half_lo(s[2 * e + q / 4][q % 4], smul, sf.hi[q]);
     }
-  __syncthreads();
+#pragma unroll
+    for (int b = 0; b < NB; ++b) {
+      mma_f16x3(m[b], frag(1, b, e), sf);
+      mma_f16x3(o[b], frag(0, b, e), sf);
+    }
+  }
+  barrier_lds();
   // block substitution; u of block b replaces m[b]
-  const int64_t base = (static_cast<int64_t>(first) * r.hv + j) * D + w * 16 + l16;
-  uint32_t bad[2] = {kbad_l[0], kbad_l[1]};  // marked nodes of the lane's state row
-  const uint32_t qbad[2] = {qbad_l[0], qbad_l[1]};
+  const int64_t step = static_cast<int64_t>(r.hv) * D;  // values from a node's o (or u) to the next one's
+  const int64_t base = static_cast<int64_t>(first + 4 * c4) * step + j * D + w * 16 + l16;
+  uint16_t* o16 = static_cast<uint16_t*>(r.o) + base;
+  float* o32 = static_cast<float*>(r.o) + base;
+  float* u32 = a.u_rec ? a.u_rec + base : nullptr;
+  uint32_t bad[2] = {lds.kbad[0], lds.kbad[1]};  // marked nodes of the lane's state row
+  const uint32_t qbad[2] = {lds.qbad[0], lds.qbad[1]};
   bool dirty = (bad[0] | bad[1] | qbad[0] | qbad[1]) != 0;
 #pragma unroll
   for (int b = 0; b < NB; ++b) {
-    f32x4 rhs, eg;
+    f32x4 rhs;
 #pragma unroll
     for (int q = 0; q < 4; ++q) {
       const int t = 16 * b + 4 * c4 + q;
-      eg[q] = eg_l[t];
-      rhs[q] = beta_l[t] * (v[b][q] - eg[q] * m[b][q]);
-      o[b][q] *= eg[q];
+      const float eg = lds.eg[t] * sinv;
+      rhs[q] = lds.beta[t] * (v[b][q] - m[b][q] * (eg * lds.inv[1][t]));
+      o[b][q] *= eg * lds.inv[0][t];
     }
+    if (__any(!((fabsf(rhs[0]) + fabsf(rhs[1])) + (fabsf(rhs[2]) + fabsf(rhs[3])) < __builtin_inff()))) {
+      dirty = true;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const uint64_t off = __ballot(!(fabsf(rhs[q]) < __builtin_inff()));
-      if (off) {
-        dirty = true;
+      for (int q = 0; q < 4; ++q) {
+        const uint64_t off = __ballot(!(fabsf(rhs[q]) < __builtin_inff()));
 #pragma unroll
         for (int g = 0; g < 4; ++g)
           if ((off >> (16 * g + l16)) & 1u) bad[b / 2] |= 1u << (16 * (b % 2) + 4 * g + q);
@@ -320,18 +432,18 @@ __global__ __launch_bounds__(D * 4) void tree_verify_kernel(TreeArgs a) {
     }
 #pragma unroll
     for (int b2 = 0; b2 < b; ++b2) {
-      const f32x4 left = *reinterpret_cast<const f32x4*>(&a_l[16 * b + l16][16 * b2 + 4 * c4]);
+      const f32x4 left = *reinterpret_cast<const f32x4*>(&lds.m.a[16 * b + l16][16 * b2 + 4 * c4]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) rhs = __builtin_amdgcn_mfma_f32_16x16x4f32(left[q], m[b2][q], rhs, 0, 0, 0);
     }
-    const f32x4 inv = *reinterpret_cast<const f32x4*>(&t_l[b][l16][4 * c4]);
+    const f32x4 inv = *reinterpret_cast<const f32x4*>(&lds.m.t[b][l16][4 * c4]);
     f32x4 u = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int q = 0; q < 4; ++q) u = __builtin_amdgcn_mfma_f32_16x16x4f32(inv[q], rhs[q], u, 0, 0, 0);
     m[b] = u;
 #pragma unroll
     for (int b2 = 0; b2 <= b; ++b2) {
-      const f32x4 left = *reinterpret_cast<const f32x4*>(&p_l[16 * b + l16][16 * b2 + 4 * c4]);
+      const f32x4 left = *reinterpret_cast<const f32x4*>(&lds.m.p[16 * b + l16][16 * b2 + 4 * c4]);
 #pragma unroll
       for (int q = 0; q < 4; ++q) o[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(left[q], m[b2][q], o[b], 0, 0, 0);
     }
@@ -340,17 +452,17 @@ __global__ __launch_bounds__(D * 4) void tree_verify_kernel(TreeArgs a) {
       const int t = 16 * b + 4 * c4 + q;
       if (dirty) {
         const uint32_t self = 1u << (t & 31);
-        const bool hit = (((anc_l[t][0] | (t < 32 ? self : 0u)) & bad[0]) | ((anc_l[t][1] | (t < 32 ? 0u : self)) & bad[1])) != 0;
+        const bool hit =
+            (((lds.anc[t][0] | (t < 32 ? self : 0u)) & bad[0]) | ((lds.anc[t][1] | (t < 32 ? 0u : self)) & bad[1])) != 0;
         if (hit) u[q] = __builtin_nanf("");
         if (hit || (qbad[t >> 5] & self)) o[b][q] = __builtin_nanf("");
       }
       if (t < n) {
-        const int64_t at = base + static_cast<int64_t>(t) * r.hv * D;
         if (r.o_bf16)
-          static_cast<uint16_t*>(r.o)[at] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[b][q]));
+          o16[(16 * b + q) * step] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[b][q]));
         else
-          static_cast<float*>(r.o)[at] = o[b][q];
-        if (a.u_rec) a.u_rec[at] = u[q];
+          o32[(16 * b + q) * step] = o[b][q];
+        if (u32) u32[(16 * b + q) * step] = u[q];
       }
     }
   }
