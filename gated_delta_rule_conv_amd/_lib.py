@@ -166,15 +166,46 @@ def _ptr(t) -> int | None:
     return t.data_ptr()
 
 
+def _torch_calls():
+    """torch's current stream of a device as a handle, and its current device: the calls below
+    torch.cuda's, which build a Stream object and check for initialisation (2 us a launch), where
+    this torch has them."""
+    import torch
+
+    def slow_stream(device):
+        return torch.cuda.current_stream(device).cuda_stream
+
+    return (getattr(torch._C, "_cuda_getCurrentRawStream", slow_stream),
+            getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device), torch.cuda.device)
+
+
+_raw_stream, _current_device, _device_guard = _torch_calls()
+
+
 def _stream(stream, *tensors) -> int | None:
     if stream is not None:
         return stream if isinstance(stream, int) else stream.cuda_stream
-    import torch
-
     for t in tensors:
         if t is not None and not isinstance(t, int) and t.is_cuda:
-            return torch.cuda.current_stream(t.device).cuda_stream
+            return _raw_stream(t.get_device())
     return None
+
+
+def _launch(name: str, fn, stream, t, *args) -> None:
+    """fn(*args, stream) on the device of tensor t (an int address: the current device), on the
+    given stream or torch's current one there."""
+    device = -1 if t is None or isinstance(t, int) or not t.is_cuda else t.get_device()
+    if stream is not None:
+        stream = stream if isinstance(stream, int) else stream.cuda_stream
+    elif device >= 0:
+        stream = _raw_stream(device)
+    if device >= 0 and device != _current_device():
+        with _device_guard(device):
+            st = fn(*args, stream)
+    else:
+        st = fn(*args, stream)
+    if st != GDN_OK:
+        raise GDNError(name, st, (_LIB.gdn_last_error() or b"").decode())
 
 
 def _check(fn: str, status: int) -> None:
@@ -290,19 +321,16 @@ def gdn_slot_pointers(pool_base: int, slot_bytes: int, pool_slots: int, slot_idx
 def gdn_tree_verify(dims: gdn_dims, x, x_stride: int, conv_w, conv_b, g, beta, o, parents, cu_nodes, m: int,
                     total_nodes: int, max_nodes: int, state_ptrs, conv_state_ptrs, k_rec, u_rec, gamma_rec,
                     stream=None) -> None:
-    st = _LIB.gdn_tree_verify(ctypes.byref(dims), _ptr(x), x_stride, _ptr(conv_w), _ptr(conv_b), _ptr(g), _ptr(beta),
-                              _ptr(o), _ptr(parents), _ptr(cu_nodes), m, total_nodes, max_nodes, _ptr(state_ptrs),
-                              _ptr(conv_state_ptrs), _ptr(k_rec), _ptr(u_rec), _ptr(gamma_rec),
-                              _stream(stream, x, o, state_ptrs))
-    _check("gdn_tree_verify", st)
+    _launch("gdn_tree_verify", _LIB.gdn_tree_verify, stream, x, ctypes.byref(dims), _ptr(x), x_stride, _ptr(conv_w),
+            _ptr(conv_b), _ptr(g), _ptr(beta), _ptr(o), _ptr(parents), _ptr(cu_nodes), m, total_nodes, max_nodes,
+            _ptr(state_ptrs), _ptr(conv_state_ptrs), _ptr(k_rec), _ptr(u_rec), _ptr(gamma_rec))
 
 
 def gdn_tree_accept(dims: gdn_dims, x, x_stride: int, k_rec, u_rec, gamma_rec, parents, cu_nodes, accepted, m: int,
                     total_nodes: int, max_nodes: int, state_ptrs, conv_state_ptrs, stream=None) -> None:
-    st = _LIB.gdn_tree_accept(ctypes.byref(dims), _ptr(x), x_stride, _ptr(k_rec), _ptr(u_rec), _ptr(gamma_rec),
-                              _ptr(parents), _ptr(cu_nodes), _ptr(accepted), m, total_nodes, max_nodes,
-                              _ptr(state_ptrs), _ptr(conv_state_ptrs), _stream(stream, x, k_rec, state_ptrs))
-    _check("gdn_tree_accept", st)
+    _launch("gdn_tree_accept", _LIB.gdn_tree_accept, stream, x, ctypes.byref(dims), _ptr(x), x_stride, _ptr(k_rec),
+            _ptr(u_rec), _ptr(gamma_rec), _ptr(parents), _ptr(cu_nodes), _ptr(accepted), m, total_nodes, max_nodes,
+            _ptr(state_ptrs), _ptr(conv_state_ptrs))
 
 
 def gdn_slot_packed_size(dims: gdn_dims, fmt: int) -> int:
@@ -312,19 +340,16 @@ def gdn_slot_packed_size(dims: gdn_dims, fmt: int) -> int:
 
 
 def gdn_slot_pack(dims: gdn_dims, fmt: int, state_ptrs, conv_state_ptrs, packed_ptrs, n: int, stream=None) -> None:
-    st = _LIB.gdn_slot_pack(ctypes.byref(dims), fmt, _ptr(state_ptrs), _ptr(conv_state_ptrs), _ptr(packed_ptrs), n,
-                            _stream(stream, state_ptrs, packed_ptrs))
-    _check("gdn_slot_pack", st)
+    _launch("gdn_slot_pack", _LIB.gdn_slot_pack, stream, state_ptrs, ctypes.byref(dims), fmt, _ptr(state_ptrs),
+            _ptr(conv_state_ptrs), _ptr(packed_ptrs), n)
 
 
 def gdn_slot_unpack(dims: gdn_dims, fmt: int, packed_ptrs, state_ptrs, conv_state_ptrs, n: int, stream=None) -> None:
-    st = _LIB.gdn_slot_unpack(ctypes.byref(dims), fmt, _ptr(packed_ptrs), _ptr(state_ptrs), _ptr(conv_state_ptrs), n,
-                              _stream(stream, state_ptrs, packed_ptrs))
-    _check("gdn_slot_unpack", st)
+    _launch("gdn_slot_unpack", _LIB.gdn_slot_unpack, stream, state_ptrs, ctypes.byref(dims), fmt, _ptr(packed_ptrs),
+            _ptr(state_ptrs), _ptr(conv_state_ptrs), n)
 
 
 def gdn_group_norm(dims: gdn_norm_dims, x, x_stride: int, gate, gate_stride: int, weight, bias, y, y_stride: int,
                    rows: int, stream=None) -> None:
-    st = _LIB.gdn_group_norm(ctypes.byref(dims), _ptr(x), x_stride, _ptr(gate), gate_stride, _ptr(weight), _ptr(bias),
-                             _ptr(y), y_stride, rows, _stream(stream, x, y))
-    _check("gdn_group_norm", st)
+    _launch("gdn_group_norm", _LIB.gdn_group_norm, stream, x, ctypes.byref(dims), _ptr(x), x_stride, _ptr(gate),
+            gate_stride, _ptr(weight), _ptr(bias), _ptr(y), y_stride, rows)

@@ -85,7 +85,9 @@ __device__ __forceinline__ void barrier_lds() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
-// One workgroup per (slot, v-head), one wave per 16 state rows; NB = blocks of 16 nodes.
+// One workgroup per slot and up to HP v-heads of one k-head, so that they share its q and k; one wave
+// per 16 state rows of a head. PAR heads run side by side on waves of their own, the others after them
+// on the same waves (their state rows are loaded while the head before finishes). NB = blocks of 16 nodes.
 //
 // The rows of the state do not mix, so with K, Q [N][d] the normalised tokens and S the wave's 16
 // rows everything is small matrix products on 16x16 tiles:
@@ -106,13 +108,13 @@ __device__ __forceinline__ void barrier_lds() {
 // see it. So such values never enter the products: a k that is not finite marks its node, a right
 // side beta (v - e^G M) that is not finite marks its node for that state row, zeros go in their
 // place, and the results of the marked nodes and their descendants are set to NaN at the end.
-template <typename T, int K, int D, int NB>
+template <typename T, int K, int D, int NB, int HP>
 struct VerifyLds {
   static constexpr int N = 16 * NB;
   static constexpr int KS = D + 16;  // fp16 values of a row of K and Q (conflict-free fragment reads)
   static constexpr int PS = N + 4;   // floats of a row of A and P
-  static constexpr int XS = 2 * D + 16 / sizeof(T);  // values of a row of x's q and k channels of the head
-  static constexpr int VS = D + 16 / sizeof(T);      // ... and of its v channels
+  static constexpr int XS = 2 * D + 16 / sizeof(T);  // values of a row of x's q and k channels
+  static constexpr int VS = HP * D + 16 / sizeof(T);  // ... and of the heads' v channels
   struct Products {
     float a[N][PS];       // A
     float p[N][PS];       // P
@@ -121,14 +123,14 @@ struct VerifyLds {
   // rows of x: the conv-state rows, oldest first, then the nodes'
   union {
     T x[K - 1 + N][XS];
-    Products m;  // (written once the conv is done with x)
+    Products m[HP];  // (written once the conv is done with x)
   };
   union {
     T xv[K - 1 + N][VS];
     _Float16 qk[2][2][N][KS];  // q, k; hi, lo; inside a row see place() (written once v is convolved)
   };
   float inv[2][N];           // inverse of the row's power of two, q and k
-  float gam[N], eg[N], beta[N];
+  float gam[HP][N], eg[HP][N], beta[HP][N];
   uint32_t anc[N][2];         // ancestors (bit j: node j), not itself
   uint32_t kbad[2], qbad[2];  // nodes whose k (q) is not finite
 };
@@ -140,11 +142,18 @@ __device__ __forceinline__ constexpr int place(int k) {
   return (k / 32) * 32 + ((k % 16) / 4) * 8 + ((k % 32) / 16) * 4 + k % 4;
 }
 
+// Heads of a workgroup, and how many of them side by side, by the blocks of nodes.
+constexpr int kVerifyHeads = 2;
+constexpr int verify_par(int nb) { return nb > 2 ? 2 : 1; }
+
 template <typename T, int K, int D, int NB, bool SILU>
-__global__ __launch_bounds__(D * 4, (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_verify_kernel(TreeArgs a) {
-  using Lds = VerifyLds<T, K, D, NB>;
-  constexpr int W = D / 16;          // waves
-  constexpr int NT = W * kWave;      // threads (4 D)
+__global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tree_verify_kernel(TreeArgs a,
+                                                                                               int32_t heads) {
+  constexpr int HP = kVerifyHeads, PAR = verify_par(NB), SEQ = HP / PAR;
+  using Lds = VerifyLds<T, K, D, NB, HP>;
+  constexpr int WH = D / 16;         // waves of a head
+  constexpr int W = WH * PAR;        // waves
+  constexpr int NT = W * kWave;      // threads
   constexpr int N = 16 * NB;
   constexpr int CH = 2 * D / 4;      // 4-channel pieces of a node's q and k channels
   using Raw = typename Vec8<T>::Raw;
@@ -153,45 +162,60 @@ __global__ __launch_bounds__(D * 4, (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_v
 
   const RecurArgs& r = a.r;
   const int i = blockIdx.y;
-  const int j = xcd_head();
   int first, n;
   tree_span(a.cu_nodes, i, a.total_nodes, a.max_nodes, first, n);
   const uint64_t sp = ((cu64*)r.state_ptrs)[i];
   const uint64_t cp = ((cu64*)a.conv_ptrs)[i];
   if (n == 0 || sp == 0 || cp == 0) return;  // (the whole workgroup)
+  // the workgroup's v-heads: j0 .. j0 + nh - 1 of k-head h
+  const int chunks = (r.group + heads - 1) / heads;
+  const int bx = xcd_head();
+  const int h = bx / chunks;
+  const int g0 = (bx - h * chunks) * heads;
+  const int j0 = h * r.group + g0;
+  const int nh = heads < r.group - g0 ? heads : r.group - g0;
   const int tid = threadIdx.x;
   const int lane = tid & (kWave - 1);
   const int w = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int hw = PAR == 1 ? 0 : w / WH;   // the wave's first head (of the workgroup's)
+  const int row_w = (w % WH) * 16;        // and its state rows
   const int c4 = lane / 16, l16 = lane % 16;
-  const int h = j / r.group;
   const int C = a.channels;
 
   // every wave: lane t's parent (the root for lanes past the tree)
   const int par = lane < n ? parent_of(a.parents, first, lane) : -1;
-  const float gval = w == 0 && lane < n ? r.g[static_cast<int64_t>(first + lane) * r.hv + j] : 0.f;
-  const float bval = w == 0 && lane < n ? r.beta[static_cast<int64_t>(first + lane) * r.hv + j] : 0.f;
+  // wave t < nh: g and beta of head t
+  const bool tree_wave = w < nh;
+  const int64_t gi = static_cast<int64_t>(first + lane) * r.hv + j0 + w;
+  const float gval = tree_wave && lane < n ? r.g[gi] : 0.f;
+  const float bval = tree_wave && lane < n ? r.beta[gi] : 0.f;
   // x and conv-state rows, on their way to LDS
   const T* x = static_cast<const T*>(a.x) + static_cast<int64_t>(first) * a.x_stride;
   const T* cs = reinterpret_cast<const T*>(cp);
-  constexpr int LX = D / 2;                // lanes on one row (3 D / 8 of them with a piece)
+  constexpr int LX = (2 + HP) * D / 8;     // lanes on one row
   constexpr int RW = W * kWave / LX;       // rows a pass
   constexpr int IT = (K - 1 + N + RW - 1) / RW;
-  const int px = (lane % LX) * 8;          // the lane's channels within the head's q | k | v
+  const int px = (lane % LX) * 8;          // the lane's channels within q | k | the heads' v
+  const int pn = (2 + nh) * D;
   const int rx = w * (kWave / LX) + (kWave == LX ? 0 : lane / LX);
-  const int chx = px < D ? h * D + px : px < 2 * D ? (r.hk - 1 + h) * D + px : (2 * r.hk - 2 + j) * D + px;
+  const int chx = px < D ? h * D + px : px < 2 * D ? (r.hk - 1 + h) * D + px : (2 * r.hk - 2 + j0) * D + px;
   Raw raw[IT];
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
     const int row = it * RW + rx;
-    if (row < K - 1 + n && px < 3 * D)
+    if (row < K - 1 + n && px < pn)
       raw[it] = Vec8<T>::load_raw((row < K - 1 ? cs + static_cast<int64_t>(row) * C : x + (row - (K - 1)) * a.x_stride) + chx);
   }
-  // taps of the lane's v channel, and of the thread's 4 q or k channels
-  const int vch = (2 * r.hk + j) * D + w * 16 + l16;
-  T vtap[K], vbias;
+  // taps of the lane's v channels (one a head), and of the thread's 4 q or k channels
+  T vtap[SEQ][K], vbias[SEQ];
 #pragma unroll
-  for (int t = 0; t < K; ++t) vtap[t] = static_cast<const T*>(a.w)[static_cast<int64_t>(vch) * K + t];
-  vbias = static_cast<const T*>(a.b ? a.b : a.w)[vch];  // (taps stand in when there is no bias)
+  for (int q = 0; q < SEQ; ++q) {
+    const int lh = q * PAR + hw < nh ? q * PAR + hw : 0;
+    const int vch = (2 * r.hk + j0 + lh) * D + row_w + l16;
+#pragma unroll
+    for (int t = 0; t < K; ++t) vtap[q][t] = static_cast<const T*>(a.w)[static_cast<int64_t>(vch) * K + t];
+    vbias[q] = static_cast<const T*>(a.b ? a.b : a.w)[vch];  // (taps stand in when there is no bias)
+  }
   const int piece = tid % CH;
   const bool is_k = piece * 4 >= D;
   const int d0 = (piece * 4) % D;
@@ -200,23 +224,25 @@ __global__ __launch_bounds__(D * 4, (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_v
 #pragma unroll
   for (int t = 0; t < K; ++t) tap[t] = V4::load_raw(static_cast<const T*>(a.w) + static_cast<int64_t>(ch0) * K + 4 * t);
   bias = V4::load_raw(static_cast<const T*>(a.b ? a.b : a.w) + ch0);
-  // the wave's state rows: lane (c4, l16) holds columns 16 e + 4 c4 .. + 3 of row l16
-  const gf32x4* S = (const gf32x4*)(reinterpret_cast<const float*>(sp) +
-                                    (static_cast<int64_t>(j) * D + w * 16 + l16) * D);
+  // the wave's state rows of its head lh: lane (c4, l16) holds columns 16 e + 4 c4 .. + 3 of row l16
   f32x4 s[D / 16];
+  const auto load_state = [&](int lh) {
+    const gf32x4* S = (const gf32x4*)(reinterpret_cast<const float*>(sp) +
+                                      (static_cast<int64_t>(j0 + lh) * D + row_w + l16) * D);
 #pragma unroll
-  for (int e = 0; e < D / 16; ++e) s[e] = __builtin_nontemporal_load(S + 4 * e + c4);
+    for (int e = 0; e < D / 16; ++e) s[e] = __builtin_nontemporal_load(S + 4 * e + c4);
+  };
+  if (hw < nh) load_state(hw);
   __builtin_amdgcn_sched_barrier(0);  // every load above is issued before the first wait
   if (tid < 2) lds.kbad[tid] = lds.qbad[tid] = 0;
 #pragma unroll
   for (int it = 0; it < IT; ++it) {
     const int row = it * RW + rx;
-    if (row < K - 1 + n && px < 3 * D) *reinterpret_cast<Raw*>(px < 2 * D ? &lds.x[row][px] : &lds.xv[row][px - 2 * D]) = raw[it];
+    if (row < K - 1 + n && px < pn) *reinterpret_cast<Raw*>(px < 2 * D ? &lds.x[row][px] : &lds.xv[row][px - 2 * D]) = raw[it];
   }
 
-  if (w == 0) {
+  if (tree_wave) {
     // ancestors and sums of g along the root path by doubling: after round s they cover 2^s levels
-    const int64_t gi = static_cast<int64_t>(first + lane) * r.hv + j;
     int up = par;
     float gam = gval;
     uint32_t lo = up >= 0 && up < 32 ? 1u << up : 0u, hi = up >= 32 ? 1u << (up - 32) : 0u;
@@ -234,11 +260,13 @@ __global__ __launch_bounds__(D * 4, (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_v
       }
     }
     if (lane < N) {
-      lds.anc[lane][0] = lo;
-      lds.anc[lane][1] = hi;
-      lds.gam[lane] = gam;
-      lds.eg[lane] = expf(gam);
-      lds.beta[lane] = bval;
+      if (w == 0) {
+        lds.anc[lane][0] = lo;
+        lds.anc[lane][1] = hi;
+      }
+      lds.gam[w][lane] = gam;
+      lds.eg[w][lane] = expf(gam);
+      lds.beta[w][lane] = bval;
       if (lane < n && a.gamma_rec) a.gamma_rec[gi] = gam;
     }
   }
@@ -255,24 +283,27 @@ __global__ __launch_bounds__(D * 4, (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_v
       back |= at << (8 * t);
     }
   }
-  // v of the lane's nodes (4 c4 + 0..3 of every block) at its state row
-  float v[NB][4];
+  // v of the lane's nodes (4 c4 + 0..3 of every block) at its state row, a head after the other
+  float v[SEQ][NB][4];
 #pragma unroll
   for (int b = 0; b < NB; ++b)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int t = 16 * b + 4 * c4 + e;
       const int rows = __shfl(back, t);
-      const int off = w * 16 + l16;
-      float acc = a.b ? elem_f32<T>(vbias) : 0.f;
 #pragma unroll
-      for (int q = 0; q < K - 1; ++q)
-        acc = fmaf(elem_f32<T>(vtap[q]), elem_f32<T>(lds.xv[(rows >> (8 * (K - 2 - q))) & 255][off]), acc);
-      acc = fmaf(elem_f32<T>(vtap[K - 1]), elem_f32<T>(lds.xv[K - 1 + t][off]), acc);
-      v[b][e] = t < n ? (SILU ? silu(acc) : acc) : 0.f;
+      for (int sq = 0; sq < SEQ; ++sq) {
+        const int off = (sq * PAR + hw) * D + row_w + l16;
+        float acc = a.b ? elem_f32<T>(vbias[sq]) : 0.f;
+#pragma unroll
+        for (int q = 0; q < K - 1; ++q)
+          acc = fmaf(elem_f32<T>(vtap[sq][q]), elem_f32<T>(lds.xv[(rows >> (8 * (K - 2 - q))) & 255][off]), acc);
+        acc = fmaf(elem_f32<T>(vtap[sq][K - 1]), elem_f32<T>(lds.xv[K - 1 + t][off]), acc);
+        v[sq][b][e] = t < n ? (SILU ? silu(acc) : acc) : 0.f;
+      }
     }
   barrier_lds();
-  // q and k: a thread convolves 4 channels (always the same ones) of one node a pass, 8 nodes a pass
+  // q and k: a thread convolves 4 channels (always the same ones) of one node a pass
 #pragma unroll
   for (int pass = 0; pass < N / (NT / CH); ++pass) {
     const int t = pass * (NT / CH) + tid / CH;
@@ -296,7 +327,7 @@ __global__ __launch_bounds__(D * 4, (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_v
     ss = row_sum(ss);
     float f = r.qk_norm && t < n ? __builtin_amdgcn_rsqf(ss + r.eps) : 1.0f;
     if (!is_k) f *= r.scale;
-    if (t < n && is_k && a.k_rec && j % r.group == 0)
+    if (t < n && is_k && a.k_rec && g0 == 0)
       *reinterpret_cast<f32x4*>(a.k_rec + (static_cast<int64_t>(first + t) * r.hk + h) * D + d0) =
           f32x4{y[0] * f, y[1] * f, y[2] * f, y[3] * f};
     if (!(ss < __builtin_inff())) {  // (the row's threads agree on ss)
@@ -326,8 +357,8 @@ __global__ __launch_bounds__(D * 4, (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_v
     return Half2{*reinterpret_cast<const f16x8*>(&lds.qk[which][0][16 * b + l16][at]),
                  *reinterpret_cast<const f16x8*>(&lds.qk[which][1][16 * b + l16][at])};
   };
-  // A and P: the lower blocks of k k^T and q k^T, dealt to the waves, A's diagonal blocks first;
-  // the wave that has one inverts it (lane c < 16 forms column c)
+  // A and P of all heads: the lower blocks of k k^T and q k^T, dealt to the waves, k k^T's diagonal
+  // blocks first; the wave that has one inverts I - A there (lane 16 t + c: column c for head t)
   {
     constexpr int NL = NB * (NB + 1) / 2;
     for (int task = w; task < 2 * NL; task += W) {
@@ -345,124 +376,144 @@ __global__ __launch_bounds__(D * 4, (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_v
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) mma_f16x3(acc, frag(is_p ? 0 : 1, bi, e), frag(1, bj, e));
       const int col = 16 * bj + l16;
-      const float gcol = lds.gam[col], icol = lds.inv[1][col];
+      const float icol = lds.inv[1][col];
+      bool use[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int row = 16 * bi + 4 * c4 + q;
-        const bool above = (lds.anc[row][col >> 5] >> (col & 31)) & 1u;
-        const bool use = above || (is_p && row == col);
-        const float f = use ? expf(lds.gam[row] - gcol) * (is_p ? 1.0f : -lds.beta[row]) : 0.f;
-        (is_p ? lds.m.p : lds.m.a)[row][col] = use ? f * (acc[q] * lds.inv[is_p ? 0 : 1][row] * icol) : 0.f;
+        use[q] = ((lds.anc[row][col >> 5] >> (col & 31)) & 1u) || (is_p && row == col);
+        acc[q] *= lds.inv[is_p ? 0 : 1][row] * icol;
+      }
+      for (int t = 0; t < nh; ++t) {
+        const float gcol = lds.gam[t][col];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int row = 16 * bi + 4 * c4 + q;
+          const float f = use[q] ? expf(lds.gam[t][row] - gcol) * (is_p ? 1.0f : -lds.beta[t][row]) : 0.f;
+          (is_p ? lds.m[t].p : lds.m[t].a)[row][col] = use[q] ? f * acc[q] : 0.f;
+        }
       }
       if (task < NB) {
         __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
         __builtin_amdgcn_wave_barrier();
         __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-        if (lane < 16) {
+        if (lane < 16 * nh) {
+          auto& mh = lds.m[lane / 16];
           float cl[16];
 #pragma unroll
           for (int q = 0; q < 16; ++q) {
-            float x2 = q == lane ? 1.0f : 0.0f;
+            float z = q == l16 ? 1.0f : 0.0f;
 #pragma unroll
-            for (int t = 0; t < q; ++t) x2 = fmaf(lds.m.a[16 * bi + q][16 * bi + t], cl[t], x2);
-            cl[q] = x2;
-            lds.m.t[bi][q][lane] = x2;
+            for (int t = 0; t < q; ++t) z = fmaf(mh.a[16 * bi + q][16 * bi + t], cl[t], z);
+            cl[q] = z;
+            mh.t[bi][q][l16] = z;
           }
         }
       }
     }
   }
-  // the state rows as fp16 pairs, then M and W
-  f32x4 m[NB], o[NB];
+  const int64_t step = static_cast<int64_t>(r.hv) * D;  // values from a node's o (or u) to the next one's
 #pragma unroll
-  for (int b = 0; b < NB; ++b) m[b] = o[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-  float top = 0.f;
+  for (int sq = 0; sq < SEQ; ++sq) {
+    const int lh = sq * PAR + hw;
+    // the state rows as fp16 pairs, then M and W
+    f32x4 m[NB], o[NB];
+    float sinv = 1.0f;
+    if (lh < nh) {
 #pragma unroll
-  for (int e = 0; e < D / 16; ++e)
+      for (int b = 0; b < NB; ++b) m[b] = o[b] = f32x4{0.f, 0.f, 0.f, 0.f};
+      float top = 0.f;
 #pragma unroll
-    for (int q = 0; q < 4; ++q) top = fmaxf(top, fabsf(s[e][q]));
-  top = fmaxf(top, __shfl_xor(top, 16));
-  top = fmaxf(top, __shfl_xor(top, 32));
-  const int sh = f16_shift(__builtin_amdgcn_frexp_expf(top));
-  const float sinv = ldexpf(1.0f, -sh), smul = ldexpf(1.0f, sh);
+      for (int e = 0; e < D / 16; ++e)
 #pragma unroll
-  for (int e = 0; e < D / 32; ++e) {
-    Half2 sf;
+        for (int q = 0; q < 4; ++q) top = fmaxf(top, fabsf(s[e][q]));
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      const int sh = f16_shift(__builtin_amdgcn_frexp_expf(top));
+      const float smul = ldexpf(1.0f, sh);
+      sinv = ldexpf(1.0f, -sh);
 #pragma unroll
-    for (int q = 0; q < 8; ++q) {
-      sf.hi[q] = half_hi(s[2 * e + q / 4][q % 4], smul);
-      sf.lo[q] = half_lo(s[2 * e + q / 4][q % 4], smul, sf.hi[q]);
+      for (int e = 0; e < D / 32; ++e) {
+        Half2 sf;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          sf.hi[q] = half_hi(s[2 * e + q / 4][q % 4], smul);
+          sf.lo[q] = half_lo(s[2 * e + q / 4][q % 4], smul, sf.hi[q]);
+        }
+#pragma unroll
+        for (int b = 0; b < NB; ++b) {
+          mma_f16x3(m[b], frag(1, b, e), sf);
+          mma_f16x3(o[b], frag(0, b, e), sf);
+        }
+      }
+      if (lh + PAR < nh) load_state(lh + PAR);
     }
+    if (sq == 0) barrier_lds();  // A, P and the inverses of every head
+    if (lh >= nh) break;
+    // block substitution; u of block b replaces m[b]
+    const auto& mh = lds.m[lh];
+    const int64_t base = static_cast<int64_t>(first + 4 * c4) * step + (j0 + lh) * D + row_w + l16;
+    uint16_t* o16 = static_cast<uint16_t*>(r.o) + base;
+    float* o32 = static_cast<float*>(r.o) + base;
+    float* u32 = a.u_rec ? a.u_rec + base : nullptr;
+    uint32_t bad[2] = {lds.kbad[0], lds.kbad[1]};  // marked nodes of the lane's state row
+    const uint32_t qbad[2] = {lds.qbad[0], lds.qbad[1]};
+    bool dirty = (bad[0] | bad[1] | qbad[0] | qbad[1]) != 0;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
-      mma_f16x3(m[b], frag(1, b, e), sf);
-      mma_f16x3(o[b], frag(0, b, e), sf);
-    }
-  }
-  barrier_lds();
-  // block substitution; u of block b replaces m[b]
-  const int64_t step = static_cast<int64_t>(r.hv) * D;  // values from a node's o (or u) to the next one's
-  const int64_t base = static_cast<int64_t>(first + 4 * c4) * step + j * D + w * 16 + l16;
-  uint16_t* o16 = static_cast<uint16_t*>(r.o) + base;
-  float* o32 = static_cast<float*>(r.o) + base;
-  float* u32 = a.u_rec ? a.u_rec + base : nullptr;
-  uint32_t bad[2] = {lds.kbad[0], lds.kbad[1]};  // marked nodes of the lane's state row
-  const uint32_t qbad[2] = {lds.qbad[0], lds.qbad[1]};
-  bool dirty = (bad[0] | bad[1] | qbad[0] | qbad[1]) != 0;
-#pragma unroll
-  for (int b = 0; b < NB; ++b) {
-    f32x4 rhs;
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int t = 16 * b + 4 * c4 + q;
-      const float eg = lds.eg[t] * sinv;
-      rhs[q] = lds.beta[t] * (v[b][q] - m[b][q] * (eg * lds.inv[1][t]));
-      o[b][q] *= eg * lds.inv[0][t];
-    }
-    if (__any(!((fabsf(rhs[0]) + fabsf(rhs[1])) + (fabsf(rhs[2]) + fabsf(rhs[3])) < __builtin_inff()))) {
-      dirty = true;
+      f32x4 rhs;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const uint64_t off = __ballot(!(fabsf(rhs[q]) < __builtin_inff()));
-#pragma unroll
-        for (int g = 0; g < 4; ++g)
-          if ((off >> (16 * g + l16)) & 1u) bad[b / 2] |= 1u << (16 * (b % 2) + 4 * g + q);
-        if ((off >> lane) & 1u) rhs[q] = 0.f;
+        const int t = 16 * b + 4 * c4 + q;
+        const float eg = lds.eg[lh][t] * sinv;
+        rhs[q] = lds.beta[lh][t] * (v[sq][b][q] - m[b][q] * (eg * lds.inv[1][t]));
+        o[b][q] *= eg * lds.inv[0][t];
       }
-    }
+      if (__any(!((fabsf(rhs[0]) + fabsf(rhs[1])) + (fabsf(rhs[2]) + fabsf(rhs[3])) < __builtin_inff()))) {
+        dirty = true;
 #pragma unroll
-    for (int b2 = 0; b2 < b; ++b2) {
-      const f32x4 left = *reinterpret_cast<const f32x4*>(&lds.m.a[16 * b + l16][16 * b2 + 4 * c4]);
+        for (int q = 0; q < 4; ++q) {
+          const uint64_t off = __ballot(!(fabsf(rhs[q]) < __builtin_inff()));
 #pragma unroll
-      for (int q = 0; q < 4; ++q) rhs = __builtin_amdgcn_mfma_f32_16x16x4f32(left[q], m[b2][q], rhs, 0, 0, 0);
-    }
-    const f32x4 inv = *reinterpret_cast<const f32x4*>(&lds.m.t[b][l16][4 * c4]);
-    f32x4 u = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-    for (int q = 0; q < 4; ++q) u = __builtin_amdgcn_mfma_f32_16x16x4f32(inv[q], rhs[q], u, 0, 0, 0);
-    m[b] = u;
-#pragma unroll
-    for (int b2 = 0; b2 <= b; ++b2) {
-      const f32x4 left = *reinterpret_cast<const f32x4*>(&lds.m.p[16 * b + l16][16 * b2 + 4 * c4]);
-#pragma unroll
-      for (int q = 0; q < 4; ++q) o[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(left[q], m[b2][q], o[b], 0, 0, 0);
-    }
-#pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int t = 16 * b + 4 * c4 + q;
-      if (dirty) {
-        const uint32_t self = 1u << (t & 31);
-        const bool hit =
-            (((lds.anc[t][0] | (t < 32 ? self : 0u)) & bad[0]) | ((lds.anc[t][1] | (t < 32 ? 0u : self)) & bad[1])) != 0;
-        if (hit) u[q] = __builtin_nanf("");
-        if (hit || (qbad[t >> 5] & self)) o[b][q] = __builtin_nanf("");
+          for (int g = 0; g < 4; ++g)
+            if ((off >> (16 * g + l16)) & 1u) bad[b / 2] |= 1u << (16 * (b % 2) + 4 * g + q);
+          if ((off >> lane) & 1u) rhs[q] = 0.f;
+        }
       }
-      if (t < n) {
-        if (r.o_bf16)
-          o16[(16 * b + q) * step] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[b][q]));
-        else
-          o32[(16 * b + q) * step] = o[b][q];
-        if (u32) u32[(16 * b + q) * step] = u[q];
+#pragma unroll
+      for (int b2 = 0; b2 < b; ++b2) {
+        const f32x4 left = *reinterpret_cast<const f32x4*>(&mh.a[16 * b + l16][16 * b2 + 4 * c4]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) rhs = __builtin_amdgcn_mfma_f32_16x16x4f32(left[q], m[b2][q], rhs, 0, 0, 0);
+      }
+      const f32x4 inv = *reinterpret_cast<const f32x4*>(&mh.t[b][l16][4 * c4]);
+      f32x4 u = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int q = 0; q < 4; ++q) u = __builtin_amdgcn_mfma_f32_16x16x4f32(inv[q], rhs[q], u, 0, 0, 0);
+      m[b] = u;
+#pragma unroll
+      for (int b2 = 0; b2 <= b; ++b2) {
+        const f32x4 left = *reinterpret_cast<const f32x4*>(&mh.p[16 * b + l16][16 * b2 + 4 * c4]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) o[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(left[q], m[b2][q], o[b], 0, 0, 0);
+      }
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        const int t = 16 * b + 4 * c4 + q;
+        if (dirty) {
+          const uint32_t self = 1u << (t & 31);
+          const bool hit = (((lds.anc[t][0] | (t < 32 ? self : 0u)) & bad[0]) |
+                            ((lds.anc[t][1] | (t < 32 ? 0u : self)) & bad[1])) != 0;
+          if (hit) u[q] = __builtin_nanf("");
+          if (hit || (qbad[t >> 5] & self)) o[b][q] = __builtin_nanf("");
+        }
+        if (t < n) {
+          if (r.o_bf16)
+            o16[(16 * b + q) * step] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[b][q]));
+          else
+            o32[(16 * b + q) * step] = o[b][q];
+          if (u32) u32[(16 * b + q) * step] = u[q];
+        }
       }
     }
   }
@@ -470,11 +521,15 @@ __global__ __launch_bounds__(D * 4, (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_v
 
 template <typename T, int K, int D, int NB>
 hipError_t verify_nb(const TreeArgs& a, int32_t m, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.r.hv), static_cast<unsigned>(m));
+  // both heads of a pair on one workgroup once that leaves a workgroup for every CU
+  const int32_t pairs = (a.r.group + kVerifyHeads - 1) / kVerifyHeads;
+  const int32_t heads = static_cast<int64_t>(m) * a.r.hk * pairs >= 256 ? kVerifyHeads : 1;
+  const dim3 grid(static_cast<unsigned>(a.r.hk * (heads == 1 ? a.r.group : pairs)), static_cast<unsigned>(m));
+  constexpr int threads = D * 4 * verify_par(NB);
   if (a.silu)
-    tree_verify_kernel<T, K, D, NB, true><<<grid, D * 4, 0, s>>>(a);
+    tree_verify_kernel<T, K, D, NB, true><<<grid, threads, 0, s>>>(a, heads);
   else
-    tree_verify_kernel<T, K, D, NB, false><<<grid, D * 4, 0, s>>>(a);
+    tree_verify_kernel<T, K, D, NB, false><<<grid, threads, 0, s>>>(a, heads);
   return hipGetLastError();
 }
 

@@ -212,12 +212,17 @@ def slot_unpack(dims: gdn_dims, fmt: int, packed_ptrs: torch.Tensor, state_ptrs:
 def group_norm(dims, x: torch.Tensor, weight, y: torch.Tensor, gate=None, bias=None, stream=None) -> None:
     """y = the norm of every group of every row of x, times weight, plus bias, gated (dims from
     make_norm_dims()). Rows are the first axis; the other axes of x, gate and y are contiguous."""
-    width = dims.groups * dims.group_size
-    for t in (x, y, gate):
-        assert t is None or (t.numel() == x.shape[0] * width and t.stride(-1) == 1 and
-                             (t.dim() == 2 or (t.dim() == 3 and t.stride(1) == t.shape[2])))
+    rows = x.shape[0]
+    n = rows * dims.groups * dims.group_size
+    assert _rows_whole(x, rows, n) and _rows_whole(y, rows, n) and (gate is None or _rows_whole(gate, rows, n))
     _lib.gdn_group_norm(dims, x, x.stride(0), gate, 0 if gate is None else gate.stride(0), weight, bias, y,
-                        y.stride(0), x.shape[0], stream)
+                        y.stride(0), rows, stream)
+
+
+def _rows_whole(t: torch.Tensor, rows: int, n: int) -> bool:
+    """Whether t holds n values in `rows` contiguous rows, [rows, width] or [rows, a, b]."""
+    s = t.stride()
+    return s[-1] == 1 and t.shape[0] == rows and t.numel() == n and (len(s) == 2 or (len(s) == 3 and s[1] == t.shape[2]))
 
 
 def prefill_workspace(dims: gdn_dims, num_seqs: int, total_tokens: int, device="cuda") -> torch.Tensor:
