@@ -28,11 +28,9 @@ __device__ __forceinline__ float elem_f32(T v) {
 // inside [0, total]).
 __device__ __forceinline__ void tree_span(const int32_t* cu, int i, int total, int max_nodes, int& first, int& n) {
   const int b = ((ci32*)cu)[i], e = ((ci32*)cu)[i + 1];
+  const int len = e - b < max_nodes ? e - b : max_nodes;
   first = b;
-  n = 0;
-  if (b < 0 || e <= b || b >= total) return;
-  n = e - b < max_nodes ? e - b : max_nodes;
-  n = n < total - b ? n : total - b;
+  n = b < 0 || e <= b || b >= total ? 0 : len < total - b ? len : total - b;
 }
 
 // Node t's parent inside its tree (-1: the slot itself).
@@ -43,7 +41,7 @@ __device__ __forceinline__ int parent_of(const int32_t* parents, int first, int 
   return p >= -1 && p < t ? p : -1;
 }
 
-// Renumbers grid.x so that consecutive v-heads, which read the same q and k channels, share an
+// Renumbers grid.x so that consecutive k-heads, which read and write neighbouring bytes, share an
 // XCD's L2 (see decode.hip).
 __device__ __forceinline__ int xcd_head() {
   const int n = gridDim.x, b = blockIdx.x;
@@ -77,6 +75,65 @@ __device__ __forceinline__ int f16_shift(int e) { return e < -97 ? 110 : 13 - e;
 __device__ __forceinline__ _Float16 half_hi(float x, float mul) { return static_cast<_Float16>(fmaf(x, mul, 0.0f)); }
 __device__ __forceinline__ _Float16 half_lo(float x, float mul, _Float16 hi) {
   return static_cast<_Float16>(fmaf(x, mul, -static_cast<float>(hi)));
+}
+
+// a * b of 32-wide steps on three independent chains (summed by total())
+__device__ __forceinline__ void mma_f16x3(f32x4 (&acc)[3], const Half2& a, const Half2& b) {
+  acc[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.hi, acc[0], 0, 0, 0);
+  acc[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.lo, b.hi, acc[1], 0, 0, 0);
+  acc[2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.lo, acc[2], 0, 0, 0);
+}
+
+// v of the lane 16 (or 32) away combined with the lane's own by op.
+template <typename F>
+__device__ __forceinline__ float across16(float v, F op) {
+  const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return op(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+template <typename F>
+__device__ __forceinline__ float across32(float v, F op) {
+  const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+  return op(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+
+// left * right + acc for 16x16 fp32 tiles: left given as MFMA's left operand (lane l: row l % 16, columns
+// 4 (l / 16) + q), right and acc as results (rows 4 (l / 16) + q of column l % 16). The left operand of
+// a matrix is the result layout of its transpose.
+__device__ __forceinline__ f32x4 mul16(const f32x4& left, const f32x4& right, f32x4 acc) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(left[q], right[q], acc, 0, 0, 0);
+  return acc;
+}
+
+// (I - A)^-1 of a strictly lower triangular 16x16 tile A (result layout in and out). With D the inverses
+// of I - A's 4x4 diagonal blocks, formed by substitution inside the four lanes that hold a block, L the
+// rest of A and X = D L (X^4 = 0):  (I - A)^-1 = (I + X^2)(D + X D).
+// Five products in three dependent steps; sixteen steps of substitution took two to three times as long.
+__device__ __forceinline__ f32x4 unit_lower_inverse(const f32x4& a, int lane) {
+  const int c4 = lane / 16, k = lane % 4;
+  const bool on_diagonal = (lane % 16) / 4 == c4;
+  // entries of the lane's 4x4 diagonal block: column c from lane c of the quad (quad_perm [c c c c])
+  const float a10 = dpp_f32<0x00>(a[1]), a20 = dpp_f32<0x00>(a[2]), a30 = dpp_f32<0x00>(a[3]);
+  const float a21 = dpp_f32<0x55>(a[2]), a31 = dpp_f32<0x55>(a[3]), a32 = dpp_f32<0xAA>(a[3]);
+  const float d20 = fmaf(a21, a10, a20), d31 = fmaf(a32, a21, a31);
+  const float d30 = fmaf(a32, d20, fmaf(a31, a10, a30));
+  const float z = 0.f, one = on_diagonal ? 1.f : 0.f;
+  const auto pick = [&](float v0, float v1, float v2, float v3) {
+    const float v = k == 0 ? v0 : k == 1 ? v1 : k == 2 ? v2 : v3;
+    return on_diagonal ? v : 0.f;
+  };
+  // D's column k (result layout) and row k (left operand)
+  const f32x4 d = {k == 0 ? one : z, pick(a10, 1.f, z, z), pick(d20, a21, 1.f, z), pick(d30, d31, a32, 1.f)};
+  const f32x4 dl = {pick(1.f, a10, d20, d30), pick(z, 1.f, a21, d31), pick(z, z, 1.f, a32), k == 3 ? one : z};
+  f32x4 rest;
+#pragma unroll
+  for (int q = 0; q < 4; ++q) rest[q] = on_diagonal ? 0.f : a[q];
+  const f32x4 zero = {0.f, 0.f, 0.f, 0.f};
+  const f32x4 x = mul16(dl, rest, zero);   // X = D L
+  const f32x4 xt = mul16(rest, dl, zero);  // X^T = L^T D^T (L's result layout is L^T's left operand, D^T's right is dl)
+  const f32x4 sqt = mul16(x, xt, zero);    // (X^2)^T = X^T X^T
+  const f32x4 y = mul16(xt, d, d);         // D + X D
+  return mul16(sqt, y, y);
 }
 
 __device__ __forceinline__ void barrier_lds() {
@@ -116,7 +173,7 @@ struct VerifyLds {
   static constexpr int XS = 2 * D + 16 / sizeof(T);  // values of a row of x's q and k channels
   static constexpr int VS = HP * D + 16 / sizeof(T);  // ... and of the heads' v channels
   struct Products {
-    float a[N][PS];       // A
+    float a[N][PS];       // A (its diagonal blocks stay in registers)
     float p[N][PS];       // P
     float t[NB][16][20];  // inverses of the diagonal blocks
   };
@@ -127,10 +184,13 @@ struct VerifyLds {
   };
   union {
     T xv[K - 1 + N][VS];
-    _Float16 qk[2][2][N][KS];  // q, k; hi, lo; inside a row see place() (written once v is convolved)
+    _Float16 qk_shared[NB > 1 ? 2 : 0][2][N][KS];  // (larger trees: written once v is convolved)
   };
-  float inv[2][N];           // inverse of the row's power of two, q and k
-  float gam[HP][N], eg[HP][N], beta[HP][N];
+  _Float16 qk_own[NB > 1 ? 0 : 2][2][N][KS];
+  // q, k; hi, lo; inside a row see place()
+  __device__ __forceinline__ _Float16 (*qk())[2][N][KS] { return NB > 1 ? qk_shared : qk_own; }
+  alignas(16) float inv[2][N];  // inverse of the row's power of two, q and k
+  alignas(16) float gam[HP][N], eg[HP][N], beta[HP][N];
   uint32_t anc[N][2];         // ancestors (bit j: node j), not itself
   uint32_t kbad[2], qbad[2];  // nodes whose k (q) is not finite
 };
@@ -147,8 +207,8 @@ constexpr int kVerifyHeads = 2;
 constexpr int verify_par(int nb) { return nb > 2 ? 2 : 1; }
 
 template <typename T, int K, int D, int NB, bool SILU>
-__global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tree_verify_kernel(TreeArgs a,
-                                                                                               int32_t heads) {
+__global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tree_verify_kernel(TreeArgs a, int32_t heads,
+                                                                                               int32_t chunks) {
   constexpr int HP = kVerifyHeads, PAR = verify_par(NB), SEQ = HP / PAR;
   using Lds = VerifyLds<T, K, D, NB, HP>;
   constexpr int WH = D / 16;         // waves of a head
@@ -162,15 +222,14 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
 
   const RecurArgs& r = a.r;
   const int i = blockIdx.y;
-  int first, n;
-  tree_span(a.cu_nodes, i, a.total_nodes, a.max_nodes, first, n);
   const uint64_t sp = ((cu64*)r.state_ptrs)[i];
   const uint64_t cp = ((cu64*)a.conv_ptrs)[i];
+  int first, n;
+  tree_span(a.cu_nodes, i, a.total_nodes, a.max_nodes, first, n);
   if (n == 0 || sp == 0 || cp == 0) return;  // (the whole workgroup)
   // the workgroup's v-heads: j0 .. j0 + nh - 1 of k-head h
-  const int chunks = (r.group + heads - 1) / heads;
   const int bx = xcd_head();
-  const int h = bx / chunks;
+  const int h = chunks == 1 ? bx : bx / chunks;
   const int g0 = (bx - h * chunks) * heads;
   const int j0 = h * r.group + g0;
   const int nh = heads < r.group - g0 ? heads : r.group - g0;
@@ -235,21 +294,26 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
   if (hw < nh) load_state(hw);
   __builtin_amdgcn_sched_barrier(0);  // every load above is issued before the first wait
   if (tid < 2) lds.kbad[tid] = lds.qbad[tid] = 0;
+  // lane t: the LDS rows of the K-1 rows before node t, 8 bits each, the nearest one lowest
+  int back = 0;
+  {
+    int at = lane + K - 1;
 #pragma unroll
-  for (int it = 0; it < IT; ++it) {
-    const int row = it * RW + rx;
-    if (row < K - 1 + n && px < pn) *reinterpret_cast<Raw*>(px < 2 * D ? &lds.x[row][px] : &lds.xv[row][px - 2 * D]) = raw[it];
+    for (int t = 0; t < K - 1; ++t) {
+      const int up = __shfl(par, at >= K - 1 ? at - (K - 1) : 0);
+      at = at >= K - 1 ? K - 1 + up : at - 1;  // (parent -1 is row K-2, the newest conv-state row)
+      back |= at << (8 * t);
+    }
   }
-
   if (tree_wave) {
     // ancestors and sums of g along the root path by doubling: after round s they cover 2^s levels
     int up = par;
     float gam = gval;
-    uint32_t lo = up >= 0 && up < 32 ? 1u << up : 0u, hi = up >= 32 ? 1u << (up - 32) : 0u;
-#pragma unroll
-    for (int s2 = 1; s2 < N; s2 *= 2) {
+    uint32_t lo = up >= 0 && up < 32 ? 1u << up : 0u, hi = 0u;
+    if constexpr (N > 32) hi = up >= 32 ? 1u << (up - 32) : 0u;
+    while (__any(up >= 0)) {
       const int from = up >= 0 ? up : lane;
-      const uint32_t lo2 = __shfl(lo, from), hi2 = __shfl(hi, from);
+      const uint32_t lo2 = __shfl(lo, from), hi2 = N > 32 ? __shfl(hi, from) : 0u;
       const float g2 = __shfl(gam, from);
       const int up2 = __shfl(up, from);
       if (up >= 0) {
@@ -270,23 +334,20 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
       if (lane < n && a.gamma_rec) a.gamma_rec[gi] = gam;
     }
   }
+#pragma unroll
+  for (int it = 0; it < IT; ++it) {
+    const int row = it * RW + rx;
+    if (row < K - 1 + n && px < pn) *reinterpret_cast<Raw*>(px < 2 * D ? &lds.x[row][px] : &lds.xv[row][px - 2 * D]) = raw[it];
+  }
+
   barrier_lds();
 
-  // lane t: the LDS rows of the K-1 rows before node t, 8 bits each, the nearest one lowest
-  int back = 0;
-  {
-    int at = lane + K - 1;
-#pragma unroll
-    for (int t = 0; t < K - 1; ++t) {
-      const int up = __shfl(par, at >= K - 1 ? at - (K - 1) : 0);
-      at = at >= K - 1 ? K - 1 + up : at - 1;  // (parent -1 is row K-2, the newest conv-state row)
-      back |= at << (8 * t);
-    }
-  }
   // v of the lane's nodes (4 c4 + 0..3 of every block) at its state row, a head after the other
   float v[SEQ][NB][4];
+  const auto conv_v = [&]() {
 #pragma unroll
   for (int b = 0; b < NB; ++b)
+    if (16 * b < n)
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
       const int t = 16 * b + 4 * c4 + e;
@@ -299,26 +360,31 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
         for (int q = 0; q < K - 1; ++q)
           acc = fmaf(elem_f32<T>(vtap[sq][q]), elem_f32<T>(lds.xv[(rows >> (8 * (K - 2 - q))) & 255][off]), acc);
         acc = fmaf(elem_f32<T>(vtap[sq][K - 1]), elem_f32<T>(lds.xv[K - 1 + t][off]), acc);
-        v[sq][b][e] = t < n ? (SILU ? silu(acc) : acc) : 0.f;
+        v[sq][b][e] = SILU ? silu(acc) : acc;  // (rows past the tree hold anything)
       }
     }
-  barrier_lds();
+  };
+  if constexpr (NB > 1) {
+    conv_v();
+    barrier_lds();
+  }
   // q and k: a thread convolves 4 channels (always the same ones) of one node a pass
 #pragma unroll
   for (int pass = 0; pass < N / (NT / CH); ++pass) {
+    if (pass * (NT / CH) >= n) break;
     const int t = pass * (NT / CH) + tid / CH;
     const int rows = __shfl(back, t);
-    float y[4] = {0.f, 0.f, 0.f, 0.f};
-    if (t < n) {
-      const int off = (is_k ? D : 0) + d0;
-      typename V4::Raw win[K - 1];
+    const int off = (is_k ? D : 0) + d0;
+    typename V4::Raw win[K - 1];
 #pragma unroll
-      for (int q = 0; q < K - 1; ++q) win[q] = V4::load_raw(&lds.x[(rows >> (8 * (K - 2 - q))) & 255][off]);
-      conv4_raw<T, K>(tap, bias, a.b != nullptr, win, V4::load_raw(&lds.x[K - 1 + t][off]), SILU, y);
-    }
+    for (int q = 0; q < K - 1; ++q) win[q] = V4::load_raw(&lds.x[(rows >> (8 * (K - 2 - q))) & 255][off]);
+    float y[4];
+    conv4_raw<T, K>(tap, bias, a.b != nullptr, win, V4::load_raw(&lds.x[K - 1 + t][off]), SILU, y);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) y[e] = t < n ? y[e] : 0.f;  // (rows past the tree hold anything)
     const auto row_sum = [](float z) {  // over the D / 4 lanes of a row
       z = group_sum<(D / 4 < 16 ? D / 4 : 16)>(z);
-      if constexpr (D / 4 > 16) z += __shfl_xor(z, 16);
+      if constexpr (D / 4 > 16) z = across16(z, [](float p, float q) { return p + q; });
       return z;
     };
     float ss = 0.f;
@@ -347,18 +413,18 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
       hi[e] = half_hi(y[e], mul);
       lo[e] = half_lo(y[e], mul, hi[e]);
     }
-    *reinterpret_cast<f16x4*>(&lds.qk[is_k][0][t][place(d0)]) = hi;
-    *reinterpret_cast<f16x4*>(&lds.qk[is_k][1][t][place(d0)]) = lo;
+    *reinterpret_cast<f16x4*>(&lds.qk()[is_k][0][t][place(d0)]) = hi;
+    *reinterpret_cast<f16x4*>(&lds.qk()[is_k][1][t][place(d0)]) = lo;
   }
   barrier_lds();
 
   const auto frag = [&](int which, int b, int step) {
     const int at = step * 32 + c4 * 8;
-    return Half2{*reinterpret_cast<const f16x8*>(&lds.qk[which][0][16 * b + l16][at]),
-                 *reinterpret_cast<const f16x8*>(&lds.qk[which][1][16 * b + l16][at])};
+    return Half2{*reinterpret_cast<const f16x8*>(&lds.qk()[which][0][16 * b + l16][at]),
+                 *reinterpret_cast<const f16x8*>(&lds.qk()[which][1][16 * b + l16][at])};
   };
   // A and P of all heads: the lower blocks of k k^T and q k^T, dealt to the waves, k k^T's diagonal
-  // blocks first; the wave that has one inverts I - A there (lane 16 t + c: column c for head t)
+  // blocks first; the wave that has one inverts I - A there, for all heads at once
   {
     constexpr int NL = NB * (NB + 1) / 2;
     for (int task = w; task < 2 * NL; task += W) {
@@ -372,46 +438,47 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
         while (rest >= (is_p ? bi + 1 : bi)) rest -= is_p ? ++bi : bi++;
         bj = rest;
       }
-      f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      if (16 * bi >= n) continue;
+      const int col = 16 * bj + l16, row = 16 * bi + 4 * c4;
+      f32x4 acc3[3];
+      zero3(acc3);
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) mma_f16x3(acc, frag(is_p ? 0 : 1, bi, e), frag(1, bj, e));
-      const int col = 16 * bj + l16;
-      const float icol = lds.inv[1][col];
+      for (int e = 0; e < D / 32; ++e) mma_f16x3(acc3, frag(is_p ? 0 : 1, bi, e), frag(1, bj, e));
       bool use[4];
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int row = 16 * bi + 4 * c4 + q;
-        use[q] = ((lds.anc[row][col >> 5] >> (col & 31)) & 1u) || (is_p && row == col);
-        acc[q] *= lds.inv[is_p ? 0 : 1][row] * icol;
-      }
-      for (int t = 0; t < nh; ++t) {
-        const float gcol = lds.gam[t][col];
+      for (int q = 0; q < 4; ++q)
+        use[q] = ((lds.anc[row + q][col >> 5] >> (col & 31)) & 1u) || (is_p && row + q == col);
+      const f32x4 acc = total(acc3) * *reinterpret_cast<const f32x4*>(&lds.inv[is_p ? 0 : 1][row]) * lds.inv[1][col];
+      f32x4 tile[HP];
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const int row = 16 * bi + 4 * c4 + q;
-          const float f = use[q] ? expf(lds.gam[t][row] - gcol) * (is_p ? 1.0f : -lds.beta[t][row]) : 0.f;
-          (is_p ? lds.m[t].p : lds.m[t].a)[row][col] = use[q] ? f * acc[q] : 0.f;
-        }
+      for (int t = 0; t < HP; ++t) {
+        tile[t] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (t >= nh) break;
+        const float gcol = lds.gam[t][col];
+        const f32x4 grow = *reinterpret_cast<const f32x4*>(&lds.gam[t][row]);
+        const f32x4 brow = *reinterpret_cast<const f32x4*>(&lds.beta[t][row]);
+#pragma unroll
+        for (int q = 0; q < 4; ++q)
+          tile[t][q] = use[q] ? acc[q] * expf(grow[q] - gcol) * (is_p ? 1.0f : -brow[q]) : 0.f;
       }
       if (task < NB) {
-        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
-        __builtin_amdgcn_wave_barrier();
-        __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
-        if (lane < 16 * nh) {
-          auto& mh = lds.m[lane / 16];
-          float cl[16];
 #pragma unroll
-          for (int q = 0; q < 16; ++q) {
-            float z = q == l16 ? 1.0f : 0.0f;
+        for (int t = 0; t < HP; ++t)
+          if (t < nh) {
+            const f32x4 x2 = unit_lower_inverse(tile[t], lane);
 #pragma unroll
-            for (int t = 0; t < q; ++t) z = fmaf(mh.a[16 * bi + q][16 * bi + t], cl[t], z);
-            cl[q] = z;
-            mh.t[bi][q][l16] = z;
+            for (int q = 0; q < 4; ++q) lds.m[t].t[bi][4 * c4 + q][l16] = x2[q];
           }
-        }
+      } else {
+#pragma unroll
+        for (int t = 0; t < HP; ++t)
+          if (t < nh)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) (is_p ? lds.m[t].p : lds.m[t].a)[row + q][col] = tile[t][q];
       }
     }
   }
+  if constexpr (NB == 1) conv_v();
   const int64_t step = static_cast<int64_t>(r.hv) * D;  // values from a node's o (or u) to the next one's
 #pragma unroll
   for (int sq = 0; sq < SEQ; ++sq) {
@@ -427,8 +494,8 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
       for (int e = 0; e < D / 16; ++e)
 #pragma unroll
         for (int q = 0; q < 4; ++q) top = fmaxf(top, fabsf(s[e][q]));
-      top = fmaxf(top, __shfl_xor(top, 16));
-      top = fmaxf(top, __shfl_xor(top, 32));
+      const auto larger = [](float p, float q) { return fmaxf(p, q); };
+      top = across32(across16(top, larger), larger);
       const int sh = f16_shift(__builtin_amdgcn_frexp_expf(top));
       const float smul = ldexpf(1.0f, sh);
       sinv = ldexpf(1.0f, -sh);
@@ -441,10 +508,11 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
           sf.lo[q] = half_lo(s[2 * e + q / 4][q % 4], smul, sf.hi[q]);
         }
 #pragma unroll
-        for (int b = 0; b < NB; ++b) {
-          mma_f16x3(m[b], frag(1, b, e), sf);
-          mma_f16x3(o[b], frag(0, b, e), sf);
-        }
+        for (int b = 0; b < NB; ++b)
+          if (16 * b < n) {
+            mma_f16x3(m[b], frag(1, b, e), sf);
+            mma_f16x3(o[b], frag(0, b, e), sf);
+          }
       }
       if (lh + PAR < nh) load_state(lh + PAR);
     }
@@ -452,22 +520,22 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
     if (lh >= nh) break;
     // block substitution; u of block b replaces m[b]
     const auto& mh = lds.m[lh];
-    const int64_t base = static_cast<int64_t>(first + 4 * c4) * step + (j0 + lh) * D + row_w + l16;
-    uint16_t* o16 = static_cast<uint16_t*>(r.o) + base;
-    float* o32 = static_cast<float*>(r.o) + base;
-    float* u32 = a.u_rec ? a.u_rec + base : nullptr;
     uint32_t bad[2] = {lds.kbad[0], lds.kbad[1]};  // marked nodes of the lane's state row
     const uint32_t qbad[2] = {lds.qbad[0], lds.qbad[1]};
     bool dirty = (bad[0] | bad[1] | qbad[0] | qbad[1]) != 0;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
+      if (16 * b >= n) break;
+      const int t0 = 16 * b + 4 * c4;
+      const f32x4 eg = *reinterpret_cast<const f32x4*>(&lds.eg[lh][t0]) * sinv;
+      const f32x4 mf = eg * *reinterpret_cast<const f32x4*>(&lds.inv[1][t0]);
+      const f32x4 of = eg * *reinterpret_cast<const f32x4*>(&lds.inv[0][t0]);
+      const f32x4 beta = *reinterpret_cast<const f32x4*>(&lds.beta[lh][t0]);
       f32x4 rhs;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
-        const int t = 16 * b + 4 * c4 + q;
-        const float eg = lds.eg[lh][t] * sinv;
-        rhs[q] = lds.beta[lh][t] * (v[sq][b][q] - m[b][q] * (eg * lds.inv[1][t]));
-        o[b][q] *= eg * lds.inv[0][t];
+        rhs[q] = t0 + q < n ? beta[q] * fmaf(-m[b][q], mf[q], v[sq][b][q]) : 0.f;
+        o[b][q] *= of[q];
       }
       if (__any(!((fabsf(rhs[0]) + fabsf(rhs[1])) + (fabsf(rhs[2]) + fabsf(rhs[3])) < __builtin_inff()))) {
         dirty = true;
@@ -481,22 +549,21 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
         }
       }
 #pragma unroll
-      for (int b2 = 0; b2 < b; ++b2) {
-        const f32x4 left = *reinterpret_cast<const f32x4*>(&mh.a[16 * b + l16][16 * b2 + 4 * c4]);
+      for (int b2 = 0; b2 < b; ++b2)
+        rhs = mul16(*reinterpret_cast<const f32x4*>(&mh.a[16 * b + l16][16 * b2 + 4 * c4]), m[b2], rhs);
+      m[b] = mul16(*reinterpret_cast<const f32x4*>(&mh.t[b][l16][4 * c4]), rhs, f32x4{0.f, 0.f, 0.f, 0.f});
 #pragma unroll
-        for (int q = 0; q < 4; ++q) rhs = __builtin_amdgcn_mfma_f32_16x16x4f32(left[q], m[b2][q], rhs, 0, 0, 0);
-      }
-      const f32x4 inv = *reinterpret_cast<const f32x4*>(&mh.t[b][l16][4 * c4]);
-      f32x4 u = {0.f, 0.f, 0.f, 0.f};
+      for (int b2 = 0; b2 <= b; ++b2)
+        o[b] = mul16(*reinterpret_cast<const f32x4*>(&mh.p[16 * b + l16][16 * b2 + 4 * c4]), m[b2], o[b]);
+    }
+    // (stores after all of it: nothing the substitution waits for queues behind them)
+    const int64_t base = static_cast<int64_t>(first + 4 * c4) * step + (j0 + lh) * D + row_w + l16;
+    uint16_t* o16 = static_cast<uint16_t*>(r.o) + base;
+    float* o32 = static_cast<float*>(r.o) + base;
+    float* u32 = a.u_rec ? a.u_rec + base : nullptr;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) u = __builtin_amdgcn_mfma_f32_16x16x4f32(inv[q], rhs[q], u, 0, 0, 0);
-      m[b] = u;
-#pragma unroll
-      for (int b2 = 0; b2 <= b; ++b2) {
-        const f32x4 left = *reinterpret_cast<const f32x4*>(&mh.p[16 * b + l16][16 * b2 + 4 * c4]);
-#pragma unroll
-        for (int q = 0; q < 4; ++q) o[b] = __builtin_amdgcn_mfma_f32_16x16x4f32(left[q], m[b2][q], o[b], 0, 0, 0);
-      }
+    for (int b = 0; b < NB; ++b) {
+      if (16 * b >= n) break;
 #pragma unroll
       for (int q = 0; q < 4; ++q) {
         const int t = 16 * b + 4 * c4 + q;
@@ -504,7 +571,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
           const uint32_t self = 1u << (t & 31);
           const bool hit = (((lds.anc[t][0] | (t < 32 ? self : 0u)) & bad[0]) |
                             ((lds.anc[t][1] | (t < 32 ? 0u : self)) & bad[1])) != 0;
-          if (hit) u[q] = __builtin_nanf("");
+          if (hit) m[b][q] = __builtin_nanf("");
           if (hit || (qbad[t >> 5] & self)) o[b][q] = __builtin_nanf("");
         }
         if (t < n) {
@@ -512,7 +579,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
             o16[(16 * b + q) * step] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[b][q]));
           else
             o32[(16 * b + q) * step] = o[b][q];
-          if (u32) u32[(16 * b + q) * step] = u[q];
+          if (u32) u32[(16 * b + q) * step] = m[b][q];
         }
       }
     }
@@ -524,12 +591,13 @@ hipError_t verify_nb(const TreeArgs& a, int32_t m, hipStream_t s) {
   // both heads of a pair on one workgroup once that leaves a workgroup for every CU
   const int32_t pairs = (a.r.group + kVerifyHeads - 1) / kVerifyHeads;
   const int32_t heads = static_cast<int64_t>(m) * a.r.hk * pairs >= 256 ? kVerifyHeads : 1;
-  const dim3 grid(static_cast<unsigned>(a.r.hk * (heads == 1 ? a.r.group : pairs)), static_cast<unsigned>(m));
+  const int32_t chunks = heads == 1 ? a.r.group : pairs;  // workgroups of a k-head
+  const dim3 grid(static_cast<unsigned>(a.r.hk * chunks), static_cast<unsigned>(m));
   constexpr int threads = D * 4 * verify_par(NB);
   if (a.silu)
-    tree_verify_kernel<T, K, D, NB, true><<<grid, threads, 0, s>>>(a, heads);
+    tree_verify_kernel<T, K, D, NB, true><<<grid, threads, 0, s>>>(a, heads, chunks);
   else
-    tree_verify_kernel<T, K, D, NB, false><<<grid, threads, 0, s>>>(a, heads);
+    tree_verify_kernel<T, K, D, NB, false><<<grid, threads, 0, s>>>(a, heads, chunks);
   return hipGetLastError();
 }
 
