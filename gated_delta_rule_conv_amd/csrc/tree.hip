@@ -24,6 +24,10 @@ __device__ __forceinline__ float elem_f32(T v) {
   else return v;
 }
 
+// e^x for x <= 0, a decay: 2^(x log2 e) on the hardware's base-2 exponential. The rounding of the
+// exponent is off by |x| 2^-24 of the result, at most 0.37 x 2^-24 of 1 for any x.
+__device__ __forceinline__ float decay(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
+
 // Slot i's rows: the first, and how many the call works on (none where cu_nodes does not lie
 // inside [0, total]).
 __device__ __forceinline__ void tree_span(const int32_t* cu, int i, int total, int max_nodes, int& first, int& n) {
@@ -329,7 +333,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
         lds.anc[lane][1] = hi;
       }
       lds.gam[w][lane] = gam;
-      lds.eg[w][lane] = expf(gam);
+      lds.eg[w][lane] = decay(gam);
       lds.beta[w][lane] = bval;
       if (lane < n && a.gamma_rec) a.gamma_rec[gi] = gam;
     }
@@ -459,7 +463,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
         const f32x4 brow = *reinterpret_cast<const f32x4*>(&lds.beta[t][row]);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          tile[t][q] = use[q] ? acc[q] * expf(grow[q] - gcol) * (is_p ? 1.0f : -brow[q]) : 0.f;
+          tile[t][q] = use[q] ? acc[q] * decay(grow[q] - gcol) * (is_p ? 1.0f : -brow[q]) : 0.f;
       }
       if (task < NB) {
 #pragma unroll
@@ -684,10 +688,11 @@ __global__ __launch_bounds__(AcceptCfg<D>::NW* kWave) void tree_accept_kernel(Ac
     for (int e = 0; e < 4; ++e)
       s[p][e] = __builtin_nontemporal_load(S + static_cast<int64_t>(row0 + p * RPP) * (D / 4) + c + LPR * e);
 
-  // lane t < n: is node t on the path? bits of the path by doubling the ancestors
+  // lane t < n: G_t, and its root path's nodes by doubling the ancestors
+  const float gam = lane < n ? a.gamma_rec[static_cast<int64_t>(first + lane) * a.hv + j] : 0.f;
   int up = lane < n ? parent_of(a.parents, first, lane) : -1;
   uint32_t lo = lane < 32 ? 1u << lane : 0u, hi = lane >= 32 ? 1u << (lane - 32) : 0u;
-  for (int s2 = 1; s2 < n; s2 *= 2) {
+  while (__any(up >= 0)) {
     const int from = up >= 0 ? up : lane;
     const uint32_t lo2 = __shfl(lo, from), hi2 = __shfl(hi, from);
     const int up2 = __shfl(up, from);
@@ -699,32 +704,49 @@ __global__ __launch_bounds__(AcceptCfg<D>::NW* kWave) void tree_accept_kernel(Ac
   }
   uint64_t path = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(lo), last)) |
                   static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(hi), last))) << 32;
-  const float* gam = a.gamma_rec + static_cast<int64_t>(first) * a.hv + j;
-  const float gend = gam[static_cast<int64_t>(last) * a.hv];
-  const float alpha = expf(gend);
+  // lane t: e^(G_a - G_t), the factor of node t's update
+  const float gend = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gam), last));
+  const float alpha = decay(gend);
+  const float f = decay(gend - gam);
+  const f32x4* kb = reinterpret_cast<const f32x4*>(a.k_rec + (static_cast<int64_t>(first) * a.hk + h) * D) + c;
+  const float* ub = a.u_rec + (static_cast<int64_t>(first) * a.hv + j) * D + row0;
+  const int64_t kstep = static_cast<int64_t>(a.hk) * (D / 4), ustep = static_cast<int64_t>(a.hv) * D;
 #pragma unroll
   for (int p = 0; p < P; ++p)
 #pragma unroll
     for (int e = 0; e < 4; ++e)
 #pragma unroll
       for (int q = 0; q < 4; ++q) s[p][e][q] *= alpha;
+  // the path in order, BATCH nodes' k and u loaded before the first is used (past the path's end the last
+  // one's again, unused)
+  constexpr int BATCH = 4;
   while (path) {
-    const int t = __builtin_ctzll(path);
-    path &= path - 1;
-    const int64_t node = first + t;
-    const float f = expf(gend - gam[static_cast<int64_t>(t) * a.hv]);
-    const f32x4* kp = reinterpret_cast<const f32x4*>(a.k_rec + (node * a.hk + h) * D);
-    const float* up_ = a.u_rec + (node * a.hv + j) * D + row0;
-    f32x4 kv[4];
+    f32x4 kv[BATCH][4];
+    float uv[BATCH][P], fv[BATCH];
+    bool have[BATCH];
+    int t = 0;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) kv[e] = kp[c + LPR * e];
+    for (int b = 0; b < BATCH; ++b) {
+      have[b] = path != 0;
+      t = have[b] ? __builtin_ctzll(path) : t;
+      path &= path - 1;
+      fv[b] = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(f), t));
 #pragma unroll
-    for (int p = 0; p < P; ++p) {
-      const float u = f * up_[p * RPP];
+      for (int e = 0; e < 4; ++e) kv[b][e] = kb[t * kstep + LPR * e];
 #pragma unroll
-      for (int e = 0; e < 4; ++e)
+      for (int p = 0; p < P; ++p) uv[b][p] = ub[t * ustep + p * RPP];
+    }
 #pragma unroll
-        for (int q = 0; q < 4; ++q) s[p][e][q] = fmaf(u, kv[e][q], s[p][e][q]);
+    for (int b = 0; b < BATCH; ++b) {
+      if (!have[b]) break;
+#pragma unroll
+      for (int p = 0; p < P; ++p) {
+        const float u = fv[b] * uv[b][p];
+#pragma unroll
+        for (int e = 0; e < 4; ++e)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) s[p][e][q] = fmaf(u, kv[b][e][q], s[p][e][q]);
+      }
     }
   }
 #pragma unroll
