@@ -195,6 +195,8 @@ struct NormArgs {
   int32_t gate_first;
   int32_t shared;
   float eps;
+  uint32_t groups_inverse;  // set by launch_group_norm, as size_inverse
+  float size_inverse;
 };
 
 hipError_t launch_group_norm(const NormArgs& a, hipStream_t s);
