@@ -206,14 +206,16 @@ __device__ __forceinline__ constexpr int place(int k) {
   return (k / 32) * 32 + ((k % 16) / 4) * 8 + ((k % 32) / 16) * 4 + k % 4;
 }
 
-// Heads of a workgroup, and how many of them side by side, by the blocks of nodes.
+// Heads of a workgroup (HP); how many of them side by side on waves of their own (PAR) and how many
+// together on the same waves (JOIN), the rest one after the other.
 constexpr int kVerifyHeads = 2;
-constexpr int verify_par(int nb) { return nb > 2 ? 2 : 1; }
+constexpr int verify_par(int nb, int d) { return nb > 2 && d < 128 ? 2 : 1; }
+constexpr int verify_join(int nb, int d) { return nb > 2 && d == 128 ? 2 : 1; }
 
 template <typename T, int K, int D, int NB, bool SILU>
-__global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tree_verify_kernel(TreeArgs a, int32_t heads,
-                                                                                               int32_t chunks) {
-  constexpr int HP = kVerifyHeads, PAR = verify_par(NB), SEQ = HP / PAR;
+__global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_verify_kernel(
+    TreeArgs a, int32_t heads, int32_t chunks) {
+  constexpr int HP = kVerifyHeads, PAR = verify_par(NB, D), SEQ = HP / PAR, JOIN = verify_join(NB, D);
   using Lds = VerifyLds<T, K, D, NB, HP>;
   constexpr int WH = D / 16;         // waves of a head
   constexpr int W = WH * PAR;        // waves
@@ -288,14 +290,16 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
   for (int t = 0; t < K; ++t) tap[t] = V4::load_raw(static_cast<const T*>(a.w) + static_cast<int64_t>(ch0) * K + 4 * t);
   bias = V4::load_raw(static_cast<const T*>(a.b ? a.b : a.w) + ch0);
   // the wave's state rows of its head lh: lane (c4, l16) holds columns 16 e + 4 c4 .. + 3 of row l16
-  f32x4 s[D / 16];
-  const auto load_state = [&](int lh) {
+  f32x4 s[JOIN][D / 16];
+  const auto load_state = [&](f32x4 (&s)[D / 16], int lh) {
     const gf32x4* S = (const gf32x4*)(reinterpret_cast<const float*>(sp) +
                                       (static_cast<int64_t>(j0 + lh) * D + row_w + l16) * D);
 #pragma unroll
     for (int e = 0; e < D / 16; ++e) s[e] = __builtin_nontemporal_load(S + 4 * e + c4);
   };
-  if (hw < nh) load_state(hw);
+#pragma unroll
+  for (int t = 0; t < JOIN; ++t)
+    if (t * PAR + hw < nh) load_state(s[t], t * PAR + hw);
   __builtin_amdgcn_sched_barrier(0);  // every load above is issued before the first wait
   if (tid < 2) lds.kbad[tid] = lds.qbad[tid] = 0;
   // lane t: the LDS rows of the K-1 rows before node t, 8 bits each, the nearest one lowest
@@ -485,105 +489,132 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB), (D < 128 ? 1 : 4)) void tre
   if constexpr (NB == 1) conv_v();
   const int64_t step = static_cast<int64_t>(r.hv) * D;  // values from a node's o (or u) to the next one's
 #pragma unroll
-  for (int sq = 0; sq < SEQ; ++sq) {
-    const int lh = sq * PAR + hw;
+  for (int sq = 0; sq < SEQ; sq += JOIN) {
+    const auto head = [&](int t) { return (sq + t) * PAR + hw; };  // t < JOIN: the wave's heads of this round
     // the state rows as fp16 pairs, then M and W
-    f32x4 m[NB], o[NB];
-    float sinv = 1.0f;
-    if (lh < nh) {
+    f32x4 m[JOIN][NB], o[JOIN][NB];
+    float smul[JOIN], sinv[JOIN];
+    if (head(0) < nh) {
 #pragma unroll
-      for (int b = 0; b < NB; ++b) m[b] = o[b] = f32x4{0.f, 0.f, 0.f, 0.f};
-      float top = 0.f;
+      for (int t = 0; t < JOIN; ++t) {
 #pragma unroll
-      for (int e = 0; e < D / 16; ++e)
+        for (int b = 0; b < NB; ++b) m[t][b] = o[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float top = 0.f;
 #pragma unroll
-        for (int q = 0; q < 4; ++q) top = fmaxf(top, fabsf(s[e][q]));
-      const auto larger = [](float p, float q) { return fmaxf(p, q); };
-      top = across32(across16(top, larger), larger);
-      const int sh = f16_shift(__builtin_amdgcn_frexp_expf(top));
-      const float smul = ldexpf(1.0f, sh);
-      sinv = ldexpf(1.0f, -sh);
+        for (int e = 0; e < D / 16; ++e)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) top = fmaxf(top, fabsf(s[t][e][q]));
+        const auto larger = [](float p, float q) { return fmaxf(p, q); };
+        top = across32(across16(top, larger), larger);
+        const int sh = f16_shift(__builtin_amdgcn_frexp_expf(top));
+        smul[t] = ldexpf(1.0f, sh);
+        sinv[t] = ldexpf(1.0f, -sh);
+      }
 #pragma unroll
       for (int e = 0; e < D / 32; ++e) {
-        Half2 sf;
+        Half2 sf[JOIN];
 #pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          sf.hi[q] = half_hi(s[2 * e + q / 4][q % 4], smul);
-          sf.lo[q] = half_lo(s[2 * e + q / 4][q % 4], smul, sf.hi[q]);
-        }
+        for (int t = 0; t < JOIN; ++t)
+#pragma unroll
+          for (int q = 0; q < 8; ++q) {
+            const float y = s[t][2 * e + q / 4][q % 4];
+            sf[t].hi[q] = half_hi(y, smul[t]);
+            sf[t].lo[q] = half_lo(y, smul[t], sf[t].hi[q]);
+          }
 #pragma unroll
         for (int b = 0; b < NB; ++b)
           if (16 * b < n) {
-            mma_f16x3(m[b], frag(1, b, e), sf);
-            mma_f16x3(o[b], frag(0, b, e), sf);
+            const Half2 kf = frag(1, b, e), qf = frag(0, b, e);
+#pragma unroll
+            for (int t = 0; t < JOIN; ++t) {
+              mma_f16x3(m[t][b], kf, sf[t]);
+              mma_f16x3(o[t][b], qf, sf[t]);
+            }
           }
       }
-      if (lh + PAR < nh) load_state(lh + PAR);
+      if constexpr (JOIN == 1) {
+        if (head(1) < nh) load_state(s[0], head(1));
+      }
     }
     if (sq == 0) barrier_lds();  // A, P and the inverses of every head
-    if (lh >= nh) break;
+    if (head(0) >= nh) break;
     // block substitution; u of block b replaces m[b]
-    const auto& mh = lds.m[lh];
-    uint32_t bad[2] = {lds.kbad[0], lds.kbad[1]};  // marked nodes of the lane's state row
+    uint32_t bad[JOIN][2];  // marked nodes of the lane's state row
     const uint32_t qbad[2] = {lds.qbad[0], lds.qbad[1]};
-    bool dirty = (bad[0] | bad[1] | qbad[0] | qbad[1]) != 0;
+    bool dirty = (lds.kbad[0] | lds.kbad[1] | qbad[0] | qbad[1]) != 0;
+#pragma unroll
+    for (int t = 0; t < JOIN; ++t) {
+      bad[t][0] = lds.kbad[0];
+      bad[t][1] = lds.kbad[1];
+    }
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if (16 * b >= n) break;
       const int t0 = 16 * b + 4 * c4;
-      const f32x4 eg = *reinterpret_cast<const f32x4*>(&lds.eg[lh][t0]) * sinv;
-      const f32x4 mf = eg * *reinterpret_cast<const f32x4*>(&lds.inv[1][t0]);
-      const f32x4 of = eg * *reinterpret_cast<const f32x4*>(&lds.inv[0][t0]);
-      const f32x4 beta = *reinterpret_cast<const f32x4*>(&lds.beta[lh][t0]);
-      f32x4 rhs;
+      const f32x4 kinv = *reinterpret_cast<const f32x4*>(&lds.inv[1][t0]);
+      const f32x4 qinv = *reinterpret_cast<const f32x4*>(&lds.inv[0][t0]);
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        rhs[q] = t0 + q < n ? beta[q] * fmaf(-m[b][q], mf[q], v[sq][b][q]) : 0.f;
-        o[b][q] *= of[q];
-      }
-      if (__any(!((fabsf(rhs[0]) + fabsf(rhs[1])) + (fabsf(rhs[2]) + fabsf(rhs[3])) < __builtin_inff()))) {
-        dirty = true;
+      for (int t = 0; t < JOIN; ++t) {
+        const int lh = head(t);
+        if (lh >= nh) break;
+        const auto& mh = lds.m[lh];
+        const f32x4 eg = *reinterpret_cast<const f32x4*>(&lds.eg[lh][t0]) * sinv[t];
+        const f32x4 beta = *reinterpret_cast<const f32x4*>(&lds.beta[lh][t0]);
+        f32x4 rhs;
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-          const uint64_t off = __ballot(!(fabsf(rhs[q]) < __builtin_inff()));
-#pragma unroll
-          for (int g = 0; g < 4; ++g)
-            if ((off >> (16 * g + l16)) & 1u) bad[b / 2] |= 1u << (16 * (b % 2) + 4 * g + q);
-          if ((off >> lane) & 1u) rhs[q] = 0.f;
+          rhs[q] = t0 + q < n ? beta[q] * fmaf(-m[t][b][q], eg[q] * kinv[q], v[sq + t][b][q]) : 0.f;
+          o[t][b][q] *= eg[q] * qinv[q];
         }
+        if (__any(!((fabsf(rhs[0]) + fabsf(rhs[1])) + (fabsf(rhs[2]) + fabsf(rhs[3])) < __builtin_inff()))) {
+          dirty = true;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const uint64_t off = __ballot(!(fabsf(rhs[q]) < __builtin_inff()));
+#pragma unroll
+            for (int g = 0; g < 4; ++g)
+              if ((off >> (16 * g + l16)) & 1u) bad[t][b / 2] |= 1u << (16 * (b % 2) + 4 * g + q);
+            if ((off >> lane) & 1u) rhs[q] = 0.f;
+          }
+        }
+#pragma unroll
+        for (int b2 = 0; b2 < b; ++b2)
+          rhs = mul16(*reinterpret_cast<const f32x4*>(&mh.a[16 * b + l16][16 * b2 + 4 * c4]), m[t][b2], rhs);
+        m[t][b] = mul16(*reinterpret_cast<const f32x4*>(&mh.t[b][l16][4 * c4]), rhs, f32x4{0.f, 0.f, 0.f, 0.f});
+#pragma unroll
+        for (int b2 = 0; b2 <= b; ++b2)
+          o[t][b] = mul16(*reinterpret_cast<const f32x4*>(&mh.p[16 * b + l16][16 * b2 + 4 * c4]), m[t][b2], o[t][b]);
       }
-#pragma unroll
-      for (int b2 = 0; b2 < b; ++b2)
-        rhs = mul16(*reinterpret_cast<const f32x4*>(&mh.a[16 * b + l16][16 * b2 + 4 * c4]), m[b2], rhs);
-      m[b] = mul16(*reinterpret_cast<const f32x4*>(&mh.t[b][l16][4 * c4]), rhs, f32x4{0.f, 0.f, 0.f, 0.f});
-#pragma unroll
-      for (int b2 = 0; b2 <= b; ++b2)
-        o[b] = mul16(*reinterpret_cast<const f32x4*>(&mh.p[16 * b + l16][16 * b2 + 4 * c4]), m[b2], o[b]);
     }
     // (stores after all of it: nothing the substitution waits for queues behind them)
-    const int64_t base = static_cast<int64_t>(first + 4 * c4) * step + (j0 + lh) * D + row_w + l16;
-    uint16_t* o16 = static_cast<uint16_t*>(r.o) + base;
-    float* o32 = static_cast<float*>(r.o) + base;
-    float* u32 = a.u_rec ? a.u_rec + base : nullptr;
 #pragma unroll
-    for (int b = 0; b < NB; ++b) {
-      if (16 * b >= n) break;
+    for (int t = 0; t < JOIN; ++t) {
+      const int lh = head(t);
+      if (lh >= nh) break;
+      const int64_t base = static_cast<int64_t>(first + 4 * c4) * step + (j0 + lh) * D + row_w + l16;
+      uint16_t* o16 = static_cast<uint16_t*>(r.o) + base;
+      float* o32 = static_cast<float*>(r.o) + base;
+      float* u32 = a.u_rec ? a.u_rec + base : nullptr;
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        const int t = 16 * b + 4 * c4 + q;
-        if (dirty) {
-          const uint32_t self = 1u << (t & 31);
-          const bool hit = (((lds.anc[t][0] | (t < 32 ? self : 0u)) & bad[0]) |
-                            ((lds.anc[t][1] | (t < 32 ? 0u : self)) & bad[1])) != 0;
-          if (hit) m[b][q] = __builtin_nanf("");
-          if (hit || (qbad[t >> 5] & self)) o[b][q] = __builtin_nanf("");
-        }
-        if (t < n) {
-          if (r.o_bf16)
-            o16[(16 * b + q) * step] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[b][q]));
-          else
-            o32[(16 * b + q) * step] = o[b][q];
-          if (u32) u32[(16 * b + q) * step] = m[b][q];
+      for (int b = 0; b < NB; ++b) {
+        if (16 * b >= n) break;
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          const int node = 16 * b + 4 * c4 + q;
+          if (dirty) {
+            const uint32_t self = 1u << (node & 31);
+            const bool hit = (((lds.anc[node][0] | (node < 32 ? self : 0u)) & bad[t][0]) |
+                              ((lds.anc[node][1] | (node < 32 ? 0u : self)) & bad[t][1])) != 0;
+            if (hit) m[t][b][q] = __builtin_nanf("");
+            if (hit || (qbad[node >> 5] & self)) o[t][b][q] = __builtin_nanf("");
+          }
+          if (node < n) {
+            if (r.o_bf16)
+              o16[(16 * b + q) * step] = __builtin_bit_cast(uint16_t, static_cast<__bf16>(o[t][b][q]));
+            else
+              o32[(16 * b + q) * step] = o[t][b][q];
+            if (u32) u32[(16 * b + q) * step] = m[t][b][q];
+          }
         }
       }
     }
@@ -597,7 +628,7 @@ hipError_t verify_nb(const TreeArgs& a, int32_t m, hipStream_t s) {
   const int32_t heads = static_cast<int64_t>(m) * a.r.hk * pairs >= 256 ? kVerifyHeads : 1;
   const int32_t chunks = heads == 1 ? a.r.group : pairs;  // workgroups of a k-head
   const dim3 grid(static_cast<unsigned>(a.r.hk * chunks), static_cast<unsigned>(m));
-  constexpr int threads = D * 4 * verify_par(NB);
+  constexpr int threads = D * 4 * verify_par(NB, D);
   if (a.silu)
     tree_verify_kernel<T, K, D, NB, true><<<grid, threads, 0, s>>>(a, heads, chunks);
   else
