@@ -194,7 +194,11 @@ def _stream(stream, *tensors) -> int | None:
 def _launch(name: str, fn, stream, t, *args) -> None:
     """fn(*args, stream) on the device of tensor t (an int address: the current device), on the
     given stream or torch's current one there."""
-    device = -1 if t is None or isinstance(t, int) or not t.is_cuda else t.get_device()
+    device = -1
+    if t is not None and not isinstance(t, int):
+        if not t.is_cuda:
+            raise ValueError(f"{name}: tensors must be on the GPU")
+        device = t.get_device()
     if stream is not None:
         stream = stream if isinstance(stream, int) else stream.cuda_stream
     elif device >= 0:

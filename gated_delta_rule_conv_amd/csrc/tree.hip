@@ -74,8 +74,9 @@ __device__ __forceinline__ void mma_f16x3(f32x4& acc, const Half2& a, const Half
 // The exponent that takes a magnitude below 2^e to below 2^13 (kept where its inverse is finite too).
 __device__ __forceinline__ int f16_shift(int e) { return e < -97 ? 110 : 13 - e; }
 
-// x * mul (mul a power of two, or a factor whose product with x is wanted to 22 bits) in two halves,
-// one instruction a half: fp16(x mul + 0) and fp16(x mul - hi).
+// x * mul, mul a power of two, in two halves, one instruction a half: fp16(x mul + 0) and
+// fp16(x mul - hi). (With any other factor the first would be rounded once in this form and twice as a
+// product and a conversion, and the compiler takes either.)
 __device__ __forceinline__ _Float16 half_hi(float x, float mul) { return static_cast<_Float16>(fmaf(x, mul, 0.0f)); }
 __device__ __forceinline__ _Float16 half_lo(float x, float mul, _Float16 hi) {
   return static_cast<_Float16>(fmaf(x, mul, -static_cast<float>(hi)));
@@ -207,7 +208,11 @@ __device__ __forceinline__ constexpr int place(int k) {
 }
 
 // Heads of a workgroup (HP); how many of them side by side on waves of their own (PAR) and how many
-// together on the same waves (JOIN), the rest one after the other.
+// together on the same waves (JOIN), the rest one after the other. Together, a fragment of K or Q read from
+// LDS serves both heads and both states are in flight from the start, at 64 more registers: 64 slots x 64
+// nodes take 129 us against 131 us one after the other, but 64 slots x 16 nodes 49 us against 44 us (their
+// 128-register budget, which keeps two workgroups on a CU, spills). Side by side is for the smaller head
+// dims' larger trees, whose four or two waves a head would convolve the tokens alone.
 constexpr int kVerifyHeads = 2;
 constexpr int verify_par(int nb, int d) { return nb > 2 && d < 128 ? 2 : 1; }
 constexpr int verify_join(int nb, int d) { return nb > 2 && d == 128 ? 2 : 1; }
@@ -298,8 +303,14 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
     for (int e = 0; e < D / 16; ++e) s[e] = __builtin_nontemporal_load(S + 4 * e + c4);
   };
 #pragma unroll
-  for (int t = 0; t < JOIN; ++t)
-    if (t * PAR + hw < nh) load_state(s[t], t * PAR + hw);
+  for (int t = 0; t < JOIN; ++t) {
+    if (t * PAR + hw < nh) {
+      load_state(s[t], t * PAR + hw);
+    } else {
+#pragma unroll
+      for (int e = 0; e < D / 16; ++e) s[t][e] = f32x4{0.f, 0.f, 0.f, 0.f};  // (an odd group's last head alone)
+    }
+  }
   __builtin_amdgcn_sched_barrier(0);  // every load above is issued before the first wait
   if (tid < 2) lds.kbad[tid] = lds.qbad[tid] = 0;
   // lane t: the LDS rows of the K-1 rows before node t, 8 bits each, the nearest one lowest
@@ -414,12 +425,14 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
     }
     const int sh = f16_shift((__builtin_amdgcn_frexp_expf(ss * f * f) + 1) >> 1);  // (|row| < 2^((e + 1) / 2))
     if (d0 == 0) lds.inv[is_k][t] = ldexpf(1.0f, -sh);
-    const float mul = ldexpf(f, sh);
+    const float mul = ldexpf(1.0f, sh);
     f16x4 hi, lo;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      hi[e] = half_hi(y[e], mul);
-      lo[e] = half_lo(y[e], mul, hi[e]);
+      float z = y[e] * f;
+      asm("" : "+v"(z));  // (rounded here, whatever becomes of it)
+      hi[e] = half_hi(z, mul);
+      lo[e] = half_lo(z, mul, hi[e]);
     }
     *reinterpret_cast<f16x4*>(&lds.qk()[is_k][0][t][place(d0)]) = hi;
     *reinterpret_cast<f16x4*>(&lds.qk()[is_k][1][t][place(d0)]) = lo;

@@ -76,37 +76,36 @@ class SlotPool:
                            dc if conv_state else None, n, stream)
 
 
-    def pack_slots(self, slot_idx: torch.Tensor, packed: torch.Tensor, fmt: int, conv_state: bool = True,
-                   stream=None) -> None:
+    def pack_slots(self, slot_idx: torch.Tensor, packed: torch.Tensor, fmt: int, conv_state: bool = True) -> None:
         """8-bit snapshots: slot slot_idx[i] into row i of packed (from packed_slots())."""
+        assert slot_idx.numel() <= packed.shape[0]
         sp, cp = self.pointers(slot_idx)
-        slot_pack(self.dims, fmt, sp, cp if conv_state else None, _block_pointers(packed, slot_idx), stream)
+        slot_pack(self.dims, fmt, sp, cp if conv_state else None, self._blocks(packed, slot_idx))
 
     def unpack_slots(self, packed: torch.Tensor, block_idx: torch.Tensor, slot_idx: torch.Tensor, fmt: int,
-                     conv_state: bool = True, stream=None) -> None:
-        """Slot slot_idx[i] filled from row block_idx[i] of packed (int32 device index tensors;
-        one block may fill several slots)."""
+                     conv_state: bool = True) -> None:
+        """Slot slot_idx[i] filled from row block_idx[i] of packed (int32 device index tensors, slots
+        distinct; one block may fill several slots). An index outside its pool skips the entry."""
         assert block_idx.numel() == slot_idx.numel()
         sp, cp = self.pointers(slot_idx)
-        slot_unpack(self.dims, fmt, _block_pointers(packed, slot_idx, block_idx), sp, cp if conv_state else None,
-                    stream)
+        slot_unpack(self.dims, fmt, self._blocks(packed, slot_idx, block_idx), sp, cp if conv_state else None)
+
+    def _blocks(self, packed: torch.Tensor, slot_idx: torch.Tensor, block_idx=None) -> torch.Tensor:
+        """Device addresses of packed's rows block_idx (default: 0, 1, ..), 0 outside it."""
+        n = slot_idx.numel()
+        assert packed.dtype == torch.uint8 and packed.dim() == 2 and packed.is_contiguous()
+        assert packed.shape[1] == _lib.gdn_slot_packed_size(self.dims, _lib.GDN_PACK_INT8)  # (both formats')
+        if block_idx is None:
+            block_idx = torch.arange(n, dtype=torch.int32, device=slot_idx.device)
+        assert block_idx.dtype == torch.int32 and block_idx.is_cuda
+        out = torch.empty(n, dtype=torch.int64, device=slot_idx.device)
+        _lib.gdn_slot_pointers(packed.data_ptr(), packed.shape[1], packed.shape[0], block_idx, n, out)
+        return out
 
 
 def packed_slots(dims: gdn_dims, n: int, fmt: int, device="cuda") -> torch.Tensor:
     """Room for n 8-bit snapshots: uint8 [n, gdn_slot_packed_size]."""
     return torch.zeros((n, _lib.gdn_slot_packed_size(dims, fmt)), dtype=torch.uint8, device=device)
-
-
-def _block_pointers(packed: torch.Tensor, slot_idx: torch.Tensor, block_idx=None) -> torch.Tensor:
-    """Device addresses of packed's rows block_idx (default: 0, 1, ..), 0 outside it."""
-    assert packed.dtype == torch.uint8 and packed.dim() == 2 and packed.is_contiguous()
-    n = slot_idx.numel()
-    if block_idx is None:
-        block_idx = torch.arange(n, dtype=torch.int32, device=slot_idx.device)
-    assert block_idx.dtype == torch.int32 and block_idx.is_cuda
-    out = torch.empty(n, dtype=torch.int64, device=slot_idx.device)
-    _lib.gdn_slot_pointers(packed.data_ptr(), packed.shape[1], packed.shape[0], block_idx, n, out)
-    return out
 
 
 def qkv_views(dims: gdn_dims, y: torch.Tensor):
@@ -171,9 +170,19 @@ def tree_record(dims: gdn_dims, total_nodes: int, device="cuda"):
             torch.empty((total_nodes, Hv), dtype=torch.float32, device=device))
 
 
-def _check_tree(x, parents, cu_nodes, state_ptrs) -> None:
-    assert x.stride(-1) == 1 and cu_nodes.dtype == torch.int32 and cu_nodes.numel() == state_ptrs.numel() + 1
-    assert parents is None or (parents.dtype == torch.int32 and parents.numel() == x.shape[0])
+def _check_tree(dims, x, parents, cu_nodes, state_ptrs, conv_state_ptrs) -> None:
+    m = state_ptrs.numel()
+    assert x.shape[1] == channels(dims) and x.stride(1) == 1 and x.dtype == torch_in_dtype(dims)
+    assert cu_nodes.dtype == torch.int32 and cu_nodes.is_cuda and cu_nodes.numel() == m + 1
+    assert conv_state_ptrs.numel() == m
+    assert parents is None or (parents.dtype == torch.int32 and parents.is_cuda and parents.numel() == x.shape[0])
+
+
+def _check_record(dims, record, rows: int):
+    k, u, gamma = record
+    Hk, Hv, d = dims.num_k_heads, dims.num_v_heads, dims.head_dim
+    assert k.numel() == rows * Hk * d and u.numel() == rows * Hv * d and gamma.numel() == rows * Hv
+    return record
 
 
 def tree_verify(dims: gdn_dims, x: torch.Tensor, conv_w: torch.Tensor, conv_b, g: torch.Tensor, beta: torch.Tensor,
@@ -181,10 +190,11 @@ def tree_verify(dims: gdn_dims, x: torch.Tensor, conv_w: torch.Tensor, conv_b, g
                 conv_state_ptrs: torch.Tensor, record=None, stream=None) -> None:
     """The drafted trees of m slots answered against their states, which stay as they are;
     parents None: chains. record (from tree_record()) is needed to accept nodes afterwards."""
-    _check_tree(x, parents, cu_nodes, state_ptrs)
-    assert g.is_contiguous() and beta.is_contiguous() and o.is_contiguous()
-    assert g.shape[0] == beta.shape[0] == o.shape[0] == x.shape[0]
-    k, u, gamma = record if record is not None else (None, None, None)
+    _check_tree(dims, x, parents, cu_nodes, state_ptrs, conv_state_ptrs)
+    rows = x.shape[0]
+    gates = rows * dims.num_v_heads
+    assert g.numel() == gates and beta.numel() == gates and o.numel() == gates * dims.head_dim and o.is_contiguous()
+    k, u, gamma = _check_record(dims, record, rows) if record is not None else (None, None, None)
     _lib.gdn_tree_verify(dims, x, x.stride(0), conv_w, conv_b, g, beta, o, parents, cu_nodes, state_ptrs.numel(),
                          x.shape[0], max_nodes, state_ptrs, conv_state_ptrs, k, u, gamma, stream)
 
@@ -192,9 +202,9 @@ def tree_verify(dims: gdn_dims, x: torch.Tensor, conv_w: torch.Tensor, conv_b, g
 def tree_accept(dims: gdn_dims, x: torch.Tensor, record, parents, cu_nodes: torch.Tensor, max_nodes: int,
                 accepted: torch.Tensor, state_ptrs: torch.Tensor, conv_state_ptrs: torch.Tensor, stream=None) -> None:
     """Slot i's state and conv state moved along the root path of node accepted[i] (-1: none)."""
-    _check_tree(x, parents, cu_nodes, state_ptrs)
-    assert accepted.dtype == torch.int32 and accepted.numel() == state_ptrs.numel()
-    k, u, gamma = record
+    _check_tree(dims, x, parents, cu_nodes, state_ptrs, conv_state_ptrs)
+    assert accepted.dtype == torch.int32 and accepted.is_cuda and accepted.numel() == state_ptrs.numel()
+    k, u, gamma = _check_record(dims, record, x.shape[0])
     _lib.gdn_tree_accept(dims, x, x.stride(0), k, u, gamma, parents, cu_nodes, accepted, state_ptrs.numel(),
                          x.shape[0], max_nodes, state_ptrs, conv_state_ptrs, stream)
 

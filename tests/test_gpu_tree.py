@@ -229,6 +229,48 @@ def test_a_slot_alone_gives_the_bits_it_gives_in_a_batch():
             np.testing.assert_array_equal(bits_of(f["pool"].state)[slot], S[slot])
 
 
+@pytest.mark.parametrize("hk,hv,d,dtype,m,top", [
+    (32, 64, 32, "bf16", 9, 16),
+    (16, 48, 32, "f32", 12, 40),   # groups of three: a pair and one alone
+    (32, 32, 64, "bf16", 9, 30),   # one v-head a k-head
+    (16, 32, 64, "f32", 17, 64),
+    (16, 32, 128, "bf16", 17, 16),
+    (16, 48, 128, "bf16", 9, 32),
+    (8, 24, 128, "bf16", 17, 64),  # larger trees, a pair and one alone
+    (8, 16, 128, "f32", 33, 50),
+])
+def test_large_batches_give_the_bits_of_single_slots(hk, hv, d, dtype, m, top):
+    """From m * hk * ceil(hv / hk / 2) = 256 on a workgroup takes two v-heads of a k-head (below, as
+    in every one-slot call here, one): the same bits for every slot."""
+    import torch
+
+    announce(f"tree: batch of {m}, hk={hk} hv={hv} d={d} {dtype} up to {top} nodes")
+    r = np.random.default_rng(d + m)
+    lens = [top] + [int(v) for v in r.integers(0, top + 1, m - 1)]
+    assert m * hk * ((hv // hk + 1) // 2) >= 256
+    c, e = _rig(lens, seed=m, shape=LayerShape(hk, hv, d, in_dtype=dtype))
+    last = [int(r.integers(-1, n)) if n else -1 for n in lens]
+    verify(e)
+    accept(e, last)
+    torch.cuda.synchronize()
+    f = device(c, e["dims"])
+    for i in range(m):
+        a, b = int(c["cu"][i]), int(c["cu"][i + 1])
+        if a == b:
+            continue
+        one = dict(x=f["x"][a:b], g=f["g"][a:b], beta=f["beta"][a:b], o=f["o"][a:b], parents=f["parents"][a:b],
+                   rec=tuple(t[a:b] for t in f["rec"]), cu=torch.tensor([0, b - a], dtype=torch.int32, device="cuda"),
+                   sp=f["sp"][i:i + 1], cp=f["cp"][i:i + 1], mx=b - a)
+        verify(f, **one)
+        accept(f, [last[i]], **one)
+    torch.cuda.synchronize()
+    assert torch.equal(e["o"], f["o"])
+    for x, y in zip(e["rec"], f["rec"]):
+        assert torch.equal(x, y)
+    assert torch.equal(e["pool"].state, f["pool"].state)
+    assert torch.equal(e["pool"].conv_state, f["pool"].conv_state)
+
+
 def test_no_parents_is_a_chain():
     import torch
 

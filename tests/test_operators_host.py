@@ -167,3 +167,15 @@ def test_null_dims():
     assert lib.gdn_slot_pack(None, 0, FAKE, None, FAKE, 1, None) == _lib.GDN_ERR_NULL
     assert lib.gdn_tree_accept(None, *ACCEPT.values()) == _lib.GDN_ERR_NULL
     assert ctypes.sizeof(_lib.gdn_norm_dims) == 12 * 4
+
+
+def test_host_tensors_are_refused_before_any_launch():
+    import torch
+
+    t = torch.zeros(4, 128)
+    with pytest.raises(ValueError):
+        gdn.group_norm(gdn.make_norm_dims(4, 32), t, None, t.clone(), gate=None)
+    d = gdn.make_dims(1, 1, 32)
+    p = torch.zeros(1, dtype=torch.int64)
+    with pytest.raises(ValueError):
+        gdn.slot_pack(d, gdn.GDN_PACK_INT8, p, None, p)
