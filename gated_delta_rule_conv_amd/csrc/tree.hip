@@ -166,6 +166,16 @@ __device__ __forceinline__ void barrier_lds() {
 // then gathers each node's window there), parents, g and beta. The barriers order LDS only, so the state
 // rows stay in flight across them.
 //
+// What bounds it. At 16/32 heads, d = 128, bf16, 64 slots read 134 MB of states: 16-node trees take 42 us (182 MB
+// in all, 4.3 TB/s), 64-node trees 129 us (290 MB and 8.6 GFLOP, of which the products with d terms are issued
+// three times). HBM is busy at its streaming rate while the workgroups of a round load, and mostly idle while
+// they compute: the two workgroups that a CU holds (one, for the largest trees, whose K and Q fill half of the
+// LDS) start together and stay in step. Neither the vector units (34% of the time) nor MFMA (14%; 22% for
+// the largest trees) is the limit there, LDS fragment reads and the substitution's dependent products are.
+// A workgroup that took several items in turn and loaded the next one's state and x during the
+// substitution needed 130 to 300 bytes of spilled registers a lane. One slot with 4 nodes takes 8.3 us, a chain
+// of about 17k cycles: two dependent memory round trips, the conv, A's diagonal blocks, M and W, the substitution.
+//
 // A zero of A or P times an infinity or a NaN would carry a broken token into branches that do not
 // see it. So such values never enter the products: a k that is not finite marks its node, a right
 // side beta (v - e^G M) that is not finite marks its node for that state row, zeros go in their
@@ -676,6 +686,10 @@ hipError_t verify_t(const TreeArgs& a, int32_t m, hipStream_t s) {
 
 // ------------------------------------------------------------------------------- accept
 
+// Bound by HBM: every moved slot's state is read and written once (64 slots of a 16/32-head, d = 128 layer
+// in 48.5 us: 250 MB by the counters, 5.2 TB/s; the path's k and u are a few rows from L2). The state rows are
+// the first loads, and wait for nothing but the slot's address and number of nodes.
+//
 // One workgroup per (slot, v-head): wave w takes D / NW state rows, lanes as in the decode kernel (D / 16
 // lanes a row, 16 columns each), all of them loaded first; then one rank-one update per path node. The
 // workgroups past the heads move the conv state, 8 channels a thread.

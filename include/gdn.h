@@ -17,6 +17,9 @@
  * P5); conv and delta-rule kernels carry a sequence dimension with per-sequence
  * conv and SSM state (same issue, comment "Where concurrency is lost", item 3).
  *
+ * Around it, over the same slots: gdn_tree_verify / gdn_tree_accept (speculative decoding),
+ * gdn_slot_pack / gdn_slot_unpack (8-bit snapshots) and gdn_group_norm (the norm of o).
+ *
  * Conventions for every entry point
  *  - Every pointer argument except `dims`, `bytes` and `stream` is a DEVICE pointer
  *    (HIP global memory) owned by the caller. The library allocates nothing, keeps
