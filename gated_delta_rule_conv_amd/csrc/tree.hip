@@ -375,21 +375,22 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
   float v[SEQ][NB][4];
   const auto conv_v = [&]() {
 #pragma unroll
-  for (int b = 0; b < NB; ++b)
-    if (16 * b < n)
+    for (int b = 0; b < NB; ++b) {
+      if (16 * b >= n) break;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int t = 16 * b + 4 * c4 + e;
-      const int rows = __shfl(back, t);
+      for (int e = 0; e < 4; ++e) {
+        const int t = 16 * b + 4 * c4 + e;
+        const int rows = __shfl(back, t);
 #pragma unroll
-      for (int sq = 0; sq < SEQ; ++sq) {
-        const int off = (sq * PAR + hw) * D + row_w + l16;
-        float acc = a.b ? elem_f32<T>(vbias[sq]) : 0.f;
+        for (int sq = 0; sq < SEQ; ++sq) {
+          const int off = (sq * PAR + hw) * D + row_w + l16;
+          float acc = a.b ? elem_f32<T>(vbias[sq]) : 0.f;
 #pragma unroll
-        for (int q = 0; q < K - 1; ++q)
-          acc = fmaf(elem_f32<T>(vtap[sq][q]), elem_f32<T>(lds.xv[(rows >> (8 * (K - 2 - q))) & 255][off]), acc);
-        acc = fmaf(elem_f32<T>(vtap[sq][K - 1]), elem_f32<T>(lds.xv[K - 1 + t][off]), acc);
-        v[sq][b][e] = SILU ? silu(acc) : acc;  // (rows past the tree hold anything)
+          for (int q = 0; q < K - 1; ++q)
+            acc = fmaf(elem_f32<T>(vtap[sq][q]), elem_f32<T>(lds.xv[(rows >> (8 * (K - 2 - q))) & 255][off]), acc);
+          acc = fmaf(elem_f32<T>(vtap[sq][K - 1]), elem_f32<T>(lds.xv[K - 1 + t][off]), acc);
+          v[sq][b][e] = SILU ? silu(acc) : acc;  // (rows past the tree hold anything)
+        }
       }
     }
   };

@@ -362,10 +362,12 @@ gdn_status gdn_slot_copy(const gdn_dims* dims, const uint64_t* src_state_ptrs, c
  *             their children; an entry outside [-1, own number) is read as -1.
  *             NULL: every tree is a chain (node i's parent is i - 1).
  *  cu_nodes   device int32 [m+1]; slot i owns rows [cu_nodes[i], cu_nodes[i+1]), possibly none.
- *  max_nodes  the largest tree of the call, 1 .. 64 (GDN_TREE_MAX_NODES). Rows of a tree beyond
- *             its first max_nodes, and rows outside [0, total_nodes), are not touched.
- *  state_ptrs, conv_state_ptrs  device u64 [m], read only; an entry of 0 in either marks an
- *             inactive slot (nothing read or written for it). Two slots may share a state here.
+ *  max_nodes  the largest tree of the call, 1 .. 64 (GDN_TREE_MAX_NODES); the launch is sized by it
+ *             (up to 16, 32 or 64 nodes), so name the real one. Rows of a tree beyond its first
+ *             max_nodes, and rows outside [0, total_nodes), are not touched.
+ *  state_ptrs, conv_state_ptrs  device u64 [m], 16-byte aligned blocks as for gdn_decode_fused, only
+ *             read; an entry of 0 in either marks an inactive slot (nothing read or written for it).
+ *             Two slots may share a state here.
  *  k_rec, u_rec, gamma_rec  the record gdn_tree_accept needs, all three or none: fp32
  *             [total_nodes][Hk][d] (normalised k), [total_nodes][Hv][d] (u) and
  *             [total_nodes][Hv] (G).

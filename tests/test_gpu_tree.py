@@ -467,3 +467,62 @@ def test_two_slots_may_verify_on_one_state():
     torch.cuda.synchronize()
     o = bits_of(e["o"])
     np.testing.assert_array_equal(o[:8], o[8:])
+
+
+@pytest.mark.parametrize("d,dtype", [(32, "f32"), (128, "bf16")])
+@pytest.mark.parametrize("kind", ["same", "two", "signs"])
+def test_drafts_that_repeat_their_keys(d, dtype, kind):
+    """Chains and trees whose keys are one direction, two in turn, or one with changing signs, next to no decay
+    and write strengths of 1: the triangular system at its fullest (every entry below the diagonal near
+    +-1 or 0). The rule is stable there (I + the lower part of a Gram matrix has an inverse of norm at most
+    2), so the usual gate holds."""
+    import torch
+
+    announce(f"tree: repeated keys {kind} d={d}")
+    sh = LayerShape(1, 2, d, conv_width=2, in_dtype=dtype)
+    c = make_case(sh, [64, 50], "chain" if kind != "two" else "tree", seed=6)
+    r = np.random.default_rng(3)
+    x = storage_to_f64(c["x"], dtype)
+    two = r.standard_normal((2, d))
+    for t in range(len(x)):
+        x[t, d:2 * d] = two[0] if kind == "same" else two[t % 2] if kind == "two" else two[0] * r.choice([-1, 1])
+    c["x"] = _store(x, dtype)
+    w = np.zeros((sh.channels, 2))
+    w[:, 1] = 1.0  # the conv hands the token on
+    c["conv_w"] = _store(w, dtype)
+    c["g"][:] = -1e-4
+    c["beta"][:] = 1.0
+    dims = make_dims(sh)
+    o, S, cs = oracle_tree(c, {})
+    e = device(c, dims)
+    verify(e)
+    last = [63, 49]
+    accept(e, last)
+    torch.cuda.synchronize()
+    check_o(c, e["o"], o, TOL_F32)
+    got = e["pool"].state.cpu().numpy()
+    for i, slot in enumerate(c["slots"]):
+        for j in range(2):
+            assert normwise_err(got[slot, j], S[c["cu"][i] + last[i]][j]) <= TOL_F32
+
+
+def test_as_many_slots_as_a_call_takes():
+    """65535 slots of one node each, on one state: equal rows for equal tokens."""
+    import torch
+
+    import gated_delta_rule_conv_amd as gdn
+
+    announce("tree: 65535 slots")
+    sh = LayerShape(1, 1, 32, in_dtype="bf16")
+    c = make_case(sh, [1], seed=2)
+    e = device(c, make_dims(sh))
+    verify(e)
+    m = 65535
+    many = {k: e[k].expand(m, *e[k].shape[1:]).contiguous() for k in ("x", "g", "beta", "o", "parents", "sp", "cp")}
+    many["cu"] = torch.arange(m + 1, dtype=torch.int32, device="cuda")
+    rec = gdn.tree_record(e["dims"], m)
+    verify(dict(e, rec=rec), **many)
+    torch.cuda.synchronize()
+    assert torch.equal(many["o"], e["o"].expand_as(many["o"]))
+    for a, b in zip(rec, e["rec"]):
+        assert torch.equal(a, b.expand_as(a))
