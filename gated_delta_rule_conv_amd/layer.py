@@ -224,15 +224,15 @@ def group_norm(dims, x: torch.Tensor, weight, y: torch.Tensor, gate=None, bias=N
     make_norm_dims()). Rows are the first axis; the other axes of x, gate and y are contiguous."""
     rows = x.shape[0]
     n = rows * dims.groups * dims.group_size
-    assert _rows_whole(x, rows, n) and _rows_whole(y, rows, n) and (gate is None or _rows_whole(gate, rows, n))
-    _lib.gdn_group_norm(dims, x, x.stride(0), gate, 0 if gate is None else gate.stride(0), weight, bias, y,
-                        y.stride(0), rows, stream)
+    _lib.gdn_group_norm(dims, x, _row_stride(x, rows, n), gate, 0 if gate is None else _row_stride(gate, rows, n),
+                        weight, bias, y, _row_stride(y, rows, n), rows, stream)
 
 
-def _rows_whole(t: torch.Tensor, rows: int, n: int) -> bool:
-    """Whether t holds n values in `rows` contiguous rows, [rows, width] or [rows, a, b]."""
-    s = t.stride()
-    return s[-1] == 1 and t.shape[0] == rows and t.numel() == n and (len(s) == 2 or (len(s) == 3 and s[1] == t.shape[2]))
+def _row_stride(t: torch.Tensor, rows: int, n: int) -> int:
+    """Row stride of t, which holds n values in `rows` contiguous rows, [rows, width] or [rows, a, b]."""
+    s, shape = t.stride(), t.shape
+    assert s[-1] == 1 and shape[0] == rows and t.numel() == n and (len(s) == 2 or (len(s) == 3 and s[1] == shape[2]))
+    return s[0]
 
 
 def prefill_workspace(dims: gdn_dims, num_seqs: int, total_tokens: int, device="cuda") -> torch.Tensor:
