@@ -159,9 +159,7 @@ def lib() -> ctypes.CDLL:
 
 def _ptr(t) -> int | None:
     """Device address of a tensor, an int address, or None (NULL)."""
-    if t is None:
-        return None
-    if isinstance(t, int):
+    if t is None or isinstance(t, int):
         return t
     return t.data_ptr()
 
@@ -194,20 +192,21 @@ def _stream(stream, *tensors) -> int | None:
 def _launch(name: str, fn, stream, t, *args) -> None:
     """fn(*args, stream) on the device of tensor t (an int address: the current device), on the
     given stream or torch's current one there."""
-    device = -1
-    if t is not None and not isinstance(t, int):
-        if not t.is_cuda:
-            raise ValueError(f"{name}: tensors must be on the GPU")
-        device = t.get_device()
-    if stream is not None:
-        stream = stream if isinstance(stream, int) else stream.cuda_stream
-    elif device >= 0:
-        stream = _raw_stream(device)
-    if device >= 0 and device != _current_device():
-        with _device_guard(device):
-            st = fn(*args, stream)
+    if t is None or isinstance(t, int):
+        st = fn(*args, stream if stream is None or isinstance(stream, int) else stream.cuda_stream)
     else:
-        st = fn(*args, stream)
+        device = t.get_device()
+        if device < 0:
+            raise ValueError(f"{name}: tensors must be on the GPU")
+        if stream is None:
+            stream = _raw_stream(device)
+        elif not isinstance(stream, int):
+            stream = stream.cuda_stream
+        if device == _current_device():
+            st = fn(*args, stream)
+        else:
+            with _device_guard(device):
+                st = fn(*args, stream)
     if st != GDN_OK:
         raise GDNError(name, st, (_LIB.gdn_last_error() or b"").decode())
 
