@@ -89,6 +89,11 @@ __device__ __forceinline__ void mma_f16x3(f32x4 (&acc)[3], const Half2& a, const
   acc[2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.lo, acc[2], 0, 0, 0);
 }
 
+// (where the magnitudes' sum overflows: false as well)
+__device__ __forceinline__ bool all_finite(const f32x4& v) {
+  return (fabsf(v[0]) + fabsf(v[1])) + (fabsf(v[2]) + fabsf(v[3])) < __builtin_inff();
+}
+
 // v of the lane 16 (or 32) away combined with the lane's own by op.
 template <typename F>
 __device__ __forceinline__ float across16(float v, F op) {
@@ -177,9 +182,10 @@ __device__ __forceinline__ void barrier_lds() {
 // of about 17k cycles: two dependent memory round trips, the conv, A's diagonal blocks, M and W, the substitution.
 //
 // A zero of A or P times an infinity or a NaN would carry a broken token into branches that do not
-// see it. So such values never enter the products: a k that is not finite marks its node, a right
-// side beta (v - e^G M) that is not finite marks its node for that state row, zeros go in their
-// place, and the results of the marked nodes and their descendants are set to NaN at the end.
+// see it. So such values never enter the products: a k that is not finite marks its node, a row of A that is
+// not (g or beta) marks its node for that head, a right side beta (v - e^G M) that is not marks it for that
+// state row, zeros go in their place, and the results of the marked nodes and their descendants are set to
+// NaN at the end.
 template <typename T, int K, int D, int NB, int HP>
 struct VerifyLds {
   static constexpr int N = 16 * NB;
@@ -208,6 +214,7 @@ struct VerifyLds {
   alignas(16) float gam[HP][N], eg[HP][N], beta[HP][N];
   uint32_t anc[N][2];         // ancestors (bit j: node j), not itself
   uint32_t kbad[2], qbad[2];  // nodes whose k (q) is not finite
+  uint32_t abad[HP][2];       // nodes whose row of A is not finite, by head
 };
 
 // Where value k of a row of q or k lies in LDS: a lane's 8 values of a 32-wide MFMA step are adjacent. The
@@ -322,7 +329,11 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
     }
   }
   __builtin_amdgcn_sched_barrier(0);  // every load above is issued before the first wait
-  if (tid < 2) lds.kbad[tid] = lds.qbad[tid] = 0;
+  if (tid < 2) {
+    lds.kbad[tid] = lds.qbad[tid] = 0;
+#pragma unroll
+    for (int t = 0; t < HP; ++t) lds.abad[t][tid] = 0;
+  }
   // lane t: the LDS rows of the K-1 rows before node t, 8 bits each, the nearest one lowest
   int back = 0;
   {
@@ -492,6 +503,15 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
 #pragma unroll
         for (int q = 0; q < 4; ++q)
           tile[t][q] = use[q] ? acc[q] * decay(grow[q] - gcol) * (is_p ? 1.0f : -brow[q]) : 0.f;
+        // (a row of P reaches its own node's o alone)
+        if (!is_p && __any(!all_finite(tile[t]))) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (!(fabsf(tile[t][q]) < __builtin_inff())) {
+              atomicOr(&lds.abad[t][(row + q) >> 5], 1u << ((row + q) & 31));
+              tile[t][q] = 0.f;
+            }
+        }
       }
       if (task < NB) {
 #pragma unroll
@@ -565,12 +585,15 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
     // block substitution; u of block b replaces m[b]
     uint32_t bad[JOIN][2];  // marked nodes of the lane's state row
     const uint32_t qbad[2] = {lds.qbad[0], lds.qbad[1]};
-    bool dirty = (lds.kbad[0] | lds.kbad[1] | qbad[0] | qbad[1]) != 0;
+    uint32_t marks = qbad[0] | qbad[1];
 #pragma unroll
-    for (int t = 0; t < JOIN; ++t) {
-      bad[t][0] = lds.kbad[0];
-      bad[t][1] = lds.kbad[1];
-    }
+    for (int t = 0; t < JOIN; ++t)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        bad[t][e] = lds.kbad[e] | (head(t) < nh ? lds.abad[head(t)][e] : 0u);
+        marks |= bad[t][e];
+      }
+    bool dirty = marks != 0;
 #pragma unroll
     for (int b = 0; b < NB; ++b) {
       if (16 * b >= n) break;
@@ -590,7 +613,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
           rhs[q] = t0 + q < n ? beta[q] * fmaf(-m[t][b][q], eg[q] * kinv[q], v[sq + t][b][q]) : 0.f;
           o[t][b][q] *= eg[q] * qinv[q];
         }
-        if (__any(!((fabsf(rhs[0]) + fabsf(rhs[1])) + (fabsf(rhs[2]) + fabsf(rhs[3])) < __builtin_inff()))) {
+        if (__any(!all_finite(rhs))) {
           dirty = true;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {

@@ -1,0 +1,117 @@
+"""gdn_tree_verify with nodes that are not finite, or whose products are not: their descendants'
+results are NaN, and every other node keeps the bits it has in the same call without them."""
+
+import numpy as np
+import pytest
+
+from gen.inputs import LayerShape, _store
+from tests.gpu_helpers import announce, bits_of
+from tests.test_gpu_tree import accept, device, make_case, make_dims, verify
+
+pytestmark = pytest.mark.gpu
+
+# one shape a form of the kernel: 16, 32 and 64 nodes, heads after each other, side by side and joined
+FORMS = [(1, 2, 32, "f32", 16), (2, 4, 32, "bf16", 31), (1, 3, 64, "f32", 64), (1, 2, 128, "bf16", 16), (1, 2, 128, "f32", 30),
+         (2, 4, 128, "bf16", 64)]
+
+
+def descendants(c, tree, node):
+    """The node (a number inside its tree) and those below it."""
+    a, hit = int(c["cu"][tree]), {node}
+    for t in range(node + 1, c["lens"][tree]):
+        if int(c["parents"][a + t]) in hit:
+            hit.add(t)
+    return hit
+
+
+def token_conv(c):
+    """The conv hands each token on as it is (width 2), so a token is seen by itself and below only
+    through the rule."""
+    w = np.zeros((c["shape"].channels, 2))
+    w[:, 1] = 1.0
+    c["conv_w"] = _store(w, c["shape"].in_dtype)
+
+
+def rig(hk, hv, d, dtype, n, seed=11, kind="tree", **kw):
+    sh = LayerShape(hk, hv, d, conv_width=2, in_dtype=dtype)
+    c = make_case(sh, [5, n], kind, seed=seed)
+    token_conv(c)
+    return c, device(c, make_dims(sh, **kw))
+
+
+def same_but(c, tree, hit, clean, got, heads=None):
+    """Every row but the hit nodes' (of the given heads) has the clean run's bits."""
+    import torch
+
+    a = int(c["cu"][tree])
+    for name, x, y in (("o", clean["o"], got["o"]), ("u", clean["rec"][1], got["rec"][1])):
+        for t in range(len(c["parents"])):
+            for j in range(x.shape[1]):
+                if t - a in hit and (heads is None or j in heads):
+                    continue
+                assert torch.equal(x[t, j], y[t, j]), (name, t, j)
+
+
+@pytest.mark.parametrize("hk,hv,d,dtype,n", FORMS)
+@pytest.mark.parametrize("what,bad", [("g", float("nan")), ("g", float("inf")), ("beta", float("nan")), ("beta", float("inf"))])
+def test_a_broken_gate_reaches_only_its_descendants(hk, hv, d, dtype, n, what, bad):
+    """One v-head's gate of one node, in the tree's first block of 16 and in its last."""
+    import torch
+
+    announce(f"tree: {what} = {bad}, hk={hk} hv={hv} d={d} {dtype} {n} nodes")
+    c, e = rig(hk, hv, d, dtype, n)
+    verify(e)
+    for node in sorted({1, n - 9}):
+        for head in (0, hv - 1):
+            f = device(c, e["dims"])
+            f[what][5 + node, head] = bad
+            verify(f)
+            torch.cuda.synchronize()
+            hit = descendants(c, 1, node)
+            same_but(c, 1, hit, e, f, heads={head})
+            for t in hit:
+                assert torch.isnan(f["o"][5 + t, head]).all() and torch.isnan(f["rec"][1][5 + t, head]).all(), (node, t)
+            ok = max(t for t in range(n) if t not in hit)
+            g = device(c, e["dims"])
+            accept(dict(f), [3, ok])
+            accept(dict(g, rec=e["rec"]), [3, ok])
+            torch.cuda.synchronize()
+            np.testing.assert_array_equal(bits_of(f["pool"].state), bits_of(g["pool"].state))
+
+
+@pytest.mark.parametrize("hk,hv,d,dtype,n", FORMS)
+def test_a_wholly_broken_token(hk, hv, d, dtype, n):
+    """NaN in x, g and beta of two nodes, as a broken hidden state gives."""
+    import torch
+
+    announce(f"tree: broken token, hk={hk} hv={hv} d={d} {dtype} {n} nodes")
+    c, e = rig(hk, hv, d, dtype, n)
+    verify(e)
+    f = device(c, e["dims"])
+    hit = set()
+    for node in (2, n - 3):
+        for k in ("x", "g", "beta"):
+            f[k][5 + node] = float("nan")
+        hit |= descendants(c, 1, node)
+    verify(f)
+    torch.cuda.synchronize()
+    same_but(c, 1, hit, e, f)
+    for t in hit:
+        assert torch.isnan(f["o"][5 + t]).all()
+
+
+def test_a_state_row_that_is_not_finite_stays_alone():
+    """One NaN (infinity) in one row of the slot's state: that row's results of every node, no other."""
+    import torch
+
+    announce("tree: state rows not finite")
+    c, e = rig(1, 2, 64, "f32", 40)
+    verify(e)
+    for bad in (float("nan"), float("inf")):
+        f = device(c, e["dims"])
+        f["pool"].state[c["slots"][1], 1, 21, 5] = bad
+        verify(f)
+        torch.cuda.synchronize()
+        rows = [r for r in range(64) if r != 21]
+        assert torch.equal(f["o"][:, 0], e["o"][:, 0]) and torch.equal(f["o"][:, 1, rows], e["o"][:, 1, rows])
+        assert torch.equal(f["o"][:5], e["o"][:5]) and not torch.isfinite(f["o"][5:, 1, 21]).any()
