@@ -434,27 +434,38 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
     ss = row_sum(ss);
     float f = r.qk_norm && t < n ? __builtin_amdgcn_rsqf(ss + r.eps) : 1.0f;
     if (!is_k) f *= r.scale;
+    float z[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      z[e] = y[e] * f;
+      asm("" : "+v"(z[e]));  // (rounded here, whatever becomes of it)
+    }
     if (t < n && is_k && a.k_rec && g0 == 0)
       *reinterpret_cast<f32x4*>(a.k_rec + (static_cast<int64_t>(first + t) * r.hk + h) * D + d0) =
-          f32x4{y[0] * f, y[1] * f, y[2] * f, y[3] * f};
-    if (!(ss < __builtin_inff())) {  // (the row's threads agree on ss)
-      if (row_sum((y[0] * 0.f + y[1] * 0.f) + (y[2] * 0.f + y[3] * 0.f)) != 0.f) {
+          f32x4{z[0], z[1], z[2], z[3]};
+    // |row| < 2^((e + 1) / 2), from the sum of squares where that is far inside the fp32 range
+    const float norm2 = ss * f * f;
+    int top = (__builtin_amdgcn_frexp_expf(norm2) + 1) >> 1;
+    if (!(norm2 > 0x1p-100f && norm2 < 0x1p100f) && t < n) {  // (the row's threads agree on ss and f)
+      // a row of zeros, of very large or small values, or with a value that is not finite: its largest
+      if (row_sum((z[0] * 0.f + z[1] * 0.f) + (z[2] * 0.f + z[3] * 0.f)) != 0.f) {
         atomicOr(&(is_k ? lds.kbad : lds.qbad)[t >> 5], 1u << (t & 31));
 #pragma unroll
-        for (int e = 0; e < 4; ++e) y[e] = 0.f;
-        f = 0.f;
+        for (int e = 0; e < 4; ++e) z[e] = 0.f;
       }
+      float most = fmaxf(fmaxf(fabsf(z[0]), fabsf(z[1])), fmaxf(fabsf(z[2]), fabsf(z[3])));
+#pragma unroll
+      for (int m = 1; m < D / 4; m *= 2) most = fmaxf(most, __shfl_xor(most, m));
+      top = __builtin_amdgcn_frexp_expf(most);
     }
-    const int sh = f16_shift((__builtin_amdgcn_frexp_expf(ss * f * f) + 1) >> 1);  // (|row| < 2^((e + 1) / 2))
+    const int sh = f16_shift(top);
     if (d0 == 0) lds.inv[is_k][t] = ldexpf(1.0f, -sh);
     const float mul = ldexpf(1.0f, sh);
     f16x4 hi, lo;
 #pragma unroll
     for (int e = 0; e < 4; ++e) {
-      float z = y[e] * f;
-      asm("" : "+v"(z));  // (rounded here, whatever becomes of it)
-      hi[e] = half_hi(z, mul);
-      lo[e] = half_lo(z, mul, hi[e]);
+      hi[e] = half_hi(z[e], mul);
+      lo[e] = half_lo(z[e], mul, hi[e]);
     }
     *reinterpret_cast<f16x4*>(&lds.qk()[is_k][0][t][place(d0)]) = hi;
     *reinterpret_cast<f16x4*>(&lds.qk()[is_k][1][t][place(d0)]) = lo;

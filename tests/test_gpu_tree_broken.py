@@ -5,8 +5,8 @@ import numpy as np
 import pytest
 
 from gen.inputs import LayerShape, _store
-from tests.gpu_helpers import announce, bits_of
-from tests.test_gpu_tree import accept, device, make_case, make_dims, verify
+from tests.gpu_helpers import TOL_F32, announce, bits_of
+from tests.test_gpu_tree import accept, check_o, device, make_case, make_dims, oracle_tree, verify
 
 pytestmark = pytest.mark.gpu
 
@@ -115,3 +115,51 @@ def test_a_state_row_that_is_not_finite_stays_alone():
         rows = [r for r in range(64) if r != 21]
         assert torch.equal(f["o"][:, 0], e["o"][:, 0]) and torch.equal(f["o"][:, 1, rows], e["o"][:, 1, rows])
         assert torch.equal(f["o"][:5], e["o"][:5]) and not torch.isfinite(f["o"][5:, 1, 21]).any()
+
+
+@pytest.mark.parametrize("hk,hv,d,dtype,n", FORMS)
+@pytest.mark.parametrize("what", ["k", "q"])
+def test_a_zero_row_without_epsilon(hk, hv, d, dtype, n, what):
+    """l2_eps = 0 and a key (query) of zeros: 0 / 0, in its own node and, for a key, below it."""
+    import torch
+
+    announce(f"tree: zero {what}, l2_eps 0, hk={hk} hv={hv} d={d} {dtype} {n} nodes")
+    c, e = rig(hk, hv, d, dtype, n, l2_eps=0.0)
+    verify(e)
+    for node in (1, n - 4):
+        f = device(c, e["dims"])
+        first = hk * d if what == "k" else 0
+        f["x"][5 + node, first:first + d] = 0.0  # (k-head 0: v-heads 0 .. hv / hk - 1)
+        verify(f)
+        torch.cuda.synchronize()
+        hit = descendants(c, 1, node) if what == "k" else {node}
+        heads = set(range(hv // hk))
+        a = 5
+        for t in range(n):
+            for j in range(hv):
+                if t in hit and j in heads:
+                    assert torch.isnan(f["o"][a + t, j]).all(), (node, t, j)
+                else:
+                    assert torch.equal(f["o"][a + t, j], e["o"][a + t, j]), (node, t, j)
+
+
+@pytest.mark.parametrize("hk,hv,d,dtype,n", FORMS)
+def test_an_unnormalised_key_beyond_the_square_root(hk, hv, d, dtype, n):
+    """qk_l2norm_off, one leaf with q of 1e20 (1e-25) and beta = 0: o = e^G S q, finite, to the usual gate."""
+    import torch
+
+    announce(f"tree: q of 1e20 and 1e-25, no norm, hk={hk} hv={hv} d={d} {dtype}")
+    c, _ = rig(hk, hv, d, dtype, 12, kind="star")
+    for size in (1e20, 1e-25):
+        r = np.random.default_rng(3)
+        x = r.standard_normal((len(c["parents"]), c["shape"].channels)) * d ** -0.5
+        x[:, :hk * d] *= size
+        x[:, hk * d:2 * hk * d] *= 1e-3 if size > 1 else size
+        c["x"] = _store(x, dtype)
+        c["beta"][:] = 0.0
+        dims = make_dims(c["shape"], qk_l2norm=False)
+        o, _, _ = oracle_tree(c, dict(qk_l2norm=False))
+        e = device(c, dims)
+        verify(e)
+        torch.cuda.synchronize()
+        check_o(c, e["o"], o, TOL_F32)
