@@ -146,6 +146,26 @@ __device__ __forceinline__ f32x4 unit_lower_inverse(const f32x4& a, int lane) {
   return mul16(sqt, y, y);
 }
 
+// The same where a path's products overflow: lane c < 16 substitutes for column c, over the entries that are
+// not zero alone, so that an infinity stays on the path it belongs to. a: room for the tile, rows of `stride`.
+// (A call of its own: inlined, its loops cost the kernels registers, 64 slots x 16 nodes of fp32 x 45 -> 51 us.)
+__device__ __attribute__((noinline)) void careful_inverse(f32x4 tile, float* a, int stride, float (*t)[20], int lane) {
+#pragma unroll
+  for (int q = 0; q < 4; ++q) a[(4 * (lane / 16) + q) * stride + lane % 16] = tile[q];
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront");
+  if (lane >= 16) return;
+  for (int i = 0; i < 16; ++i) {
+    float x = i == lane ? 1.f : 0.f;
+    for (int k = 0; k < i; ++k) {
+      const float v = a[i * stride + k];
+      if (v != 0.f) x = fmaf(v, t[k][lane], x);
+    }
+    t[i][lane] = x;
+  }
+}
+
 __device__ __forceinline__ void barrier_lds() {
   __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
   __builtin_amdgcn_s_barrier();
@@ -183,9 +203,10 @@ __device__ __forceinline__ void barrier_lds() {
 //
 // A zero of A or P times an infinity or a NaN would carry a broken token into branches that do not
 // see it. So such values never enter the products: a k that is not finite marks its node, a row of A that is
-// not (g or beta) marks its node for that head, a right side beta (v - e^G M) that is not marks it for that
+// not (g or beta) marks its node for that head, a right side beta (v - e^G M) - .. or a u that is not marks it for that
 // state row, zeros go in their place, and the results of the marked nodes and their descendants are set to
-// NaN at the end.
+// NaN at the end. An inverse that is not finite (a path of unnormalised keys that diverges) is formed
+// again without products by zeros; its rows are then not finite on that path alone, and so u's.
 template <typename T, int K, int D, int NB, int HP>
 struct VerifyLds {
   static constexpr int N = 16 * NB;
@@ -531,6 +552,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
             const f32x4 x2 = unit_lower_inverse(tile[t], lane);
 #pragma unroll
             for (int q = 0; q < 4; ++q) lds.m[t].t[bi][4 * c4 + q][l16] = x2[q];
+            if (__any(!all_finite(x2))) careful_inverse(tile[t], &lds.m[t].a[16 * bi][16 * bi], Lds::PS, lds.m[t].t[bi], lane);
           }
       } else {
 #pragma unroll
@@ -624,21 +646,24 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
           rhs[q] = t0 + q < n ? beta[q] * fmaf(-m[t][b][q], eg[q] * kinv[q], v[sq + t][b][q]) : 0.f;
           o[t][b][q] *= eg[q] * qinv[q];
         }
-        if (__any(!all_finite(rhs))) {
+        const auto mark = [&](f32x4& v) {  // values that are not finite: zeros, their nodes marked
+          if (!__any(!all_finite(v))) return;
           dirty = true;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            const uint64_t off = __ballot(!(fabsf(rhs[q]) < __builtin_inff()));
+            const uint64_t off = __ballot(!(fabsf(v[q]) < __builtin_inff()));
 #pragma unroll
             for (int g = 0; g < 4; ++g)
               if ((off >> (16 * g + l16)) & 1u) bad[t][b / 2] |= 1u << (16 * (b % 2) + 4 * g + q);
-            if ((off >> lane) & 1u) rhs[q] = 0.f;
+            if ((off >> lane) & 1u) v[q] = 0.f;
           }
-        }
+        };
 #pragma unroll
         for (int b2 = 0; b2 < b; ++b2)
           rhs = mul16(*reinterpret_cast<const f32x4*>(&mh.a[16 * b + l16][16 * b2 + 4 * c4]), m[t][b2], rhs);
+        mark(rhs);
         m[t][b] = mul16(*reinterpret_cast<const f32x4*>(&mh.t[b][l16][4 * c4]), rhs, f32x4{0.f, 0.f, 0.f, 0.f});
+        mark(m[t][b]);
 #pragma unroll
         for (int b2 = 0; b2 <= b; ++b2)
           o[t][b] = mul16(*reinterpret_cast<const f32x4*>(&mh.p[16 * b + l16][16 * b2 + 4 * c4]), m[t][b2], o[t][b]);

@@ -163,3 +163,72 @@ def test_an_unnormalised_key_beyond_the_square_root(hk, hv, d, dtype, n):
         verify(e)
         torch.cuda.synchronize()
         check_o(c, e["o"], o, TOL_F32)
+@pytest.mark.parametrize("hk,hv,d,dtype,n", FORMS)
+def test_keys_whose_square_overflows(hk, hv, d, dtype, n):
+    """qk_l2norm_off and one finite key of 1e20s, whose |k|^2 is above the largest fp32 number: its
+    descendants' products overflow, nobody else's do."""
+    import torch
+
+    announce(f"tree: k of 1e20, no norm, hk={hk} hv={hv} d={d} {dtype} {n} nodes")
+    c, e = rig(hk, hv, d, dtype, n, qk_l2norm=False)
+    e["x"].mul_(d ** -0.5)
+    verify(e)
+    for node in (1, n - 4):
+        f = device(c, e["dims"])
+        f["x"].mul_(d ** -0.5)
+        f["x"][5 + node, hk * d:hk * d + d] = 1e20
+        verify(f)
+        torch.cuda.synchronize()
+        same_but(c, 1, descendants(c, 1, node), e, f, heads=set(range(hv // hk)))
+
+
+@pytest.mark.parametrize("hk,hv,d,dtype,n", FORMS)
+def test_a_path_that_diverges_reaches_only_itself(hk, hv, d, dtype, n):
+    """qk_l2norm_off and keys of |k|^2 = 1e6 on one chain: (I - beta k k^T) expands its state until it
+    overflows. Every second node is on the chain; the others are children of the slot or of each other."""
+    import torch
+
+    announce(f"tree: diverging chain, hk={hk} hv={hv} d={d} {dtype} {n} nodes")
+    c, _ = rig(hk, hv, d, dtype, n)
+    for t in range(n):
+        c["parents"][5 + t] = t - 2 if t % 2 else (-1 if t % 4 == 0 else t - 2)
+    odd = [5 + t for t in range(1, n, 2)]
+    dims = make_dims(c["shape"], qk_l2norm=False)
+    runs = []
+    for size in (d ** -0.5, 1e3 * d ** -0.5):
+        e = device(c, dims)
+        e["x"].mul_(d ** -0.5)
+        e["x"][odd, hk * d:2 * hk * d] = size
+        e["beta"][odd] = 1.0
+        e["g"][odd] = -1e-3
+        verify(e)
+        runs.append(e)
+    torch.cuda.synchronize()
+    if n > 32:
+        assert not torch.isfinite(runs[1]["o"][odd]).all()  # (it did diverge)
+    same_but(c, 1, set(range(1, n, 2)), *runs)
+
+
+@pytest.mark.parametrize("hk,hv,d,dtype,n", FORMS)
+def test_values_next_to_the_largest_number(hk, hv, d, dtype, n):
+    """v of 3e38 along a chain of equal keys: u overflows below it, not beside it."""
+    import torch
+
+    announce(f"tree: v of 3e38, hk={hk} hv={hv} d={d} {dtype} {n} nodes")
+    c, _ = rig(hk, hv, d, dtype, n)
+    for t in range(n):
+        c["parents"][5 + t] = t - 2 if t % 2 else (-1 if t % 4 == 0 else t - 2)
+    odd = [5 + t for t in range(1, n, 2)]
+    runs = []
+    for sign in (0.0, 1.0):
+        e = device(c, make_dims(c["shape"]))
+        e["x"][odd, hk * d:2 * hk * d] = 1.0
+        # signs that add up in u: v, -v, v ..
+        for i, t in enumerate(odd):
+            e["x"][t, 2 * hk * d:] = 3e38 * sign * (-1) ** i
+        e["beta"][odd] = 1.0
+        e["g"][odd] = 0.0
+        verify(e)
+        runs.append(e)
+    torch.cuda.synchronize()
+    same_but(c, 1, set(range(1, n, 2)), *runs)
