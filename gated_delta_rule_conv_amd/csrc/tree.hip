@@ -28,6 +28,21 @@ __device__ __forceinline__ float elem_f32(T v) {
 // exponent is off by |x| 2^-24 of the result, at most 0.37 x 2^-24 of 1 for any x.
 __device__ __forceinline__ float decay(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896341f); }
 
+// A sum of g over a path in two halves, so that the difference of two of them keeps the digits of the mild
+// tokens behind a strongly forgetting one. A g below -128 counts as -128: e^-128 is 0 in fp32 as well, and
+// the sums of 64 nodes stay above -8192, whose halves are good to 2^-35.
+constexpr float kForget = -128.0f;
+struct Gamma {
+  float hi, lo;
+};
+__device__ __forceinline__ Gamma gamma_of(float g) { return Gamma{g < kForget ? kForget : g, 0.f}; }  // (a NaN stays)
+__device__ __forceinline__ Gamma operator+(const Gamma& a, const Gamma& b) {
+  const float s = a.hi + b.hi, bb = s - a.hi;
+  const float lo = ((a.hi - (s - bb)) + (b.hi - bb)) + (a.lo + b.lo);
+  const float hi = s + lo;
+  return Gamma{hi, lo - (hi - s)};
+}
+
 // Slot i's rows: the first, and how many the call works on (none where cu_nodes does not lie
 // inside [0, total]).
 __device__ __forceinline__ void tree_span(const int32_t* cu, int i, int total, int max_nodes, int& first, int& n) {
@@ -43,6 +58,20 @@ __device__ __forceinline__ int parent_of(const int32_t* parents, int first, int 
   if (!parents) return t - 1;
   const int p = parents[first + t];
   return p >= -1 && p < t ? p : -1;
+}
+
+// The record's G holds one fp32 number, whose steps grow with it. So where a parent's is below -128 and the
+// node's own g above that, the sum starts again from the node: G = g. Such a parent is at the end of a
+// path whose sum of g is below -128, and no other node's G behind it rises above its parent's, which is how the
+// reader knows. Lane t: sum = the path's sum (used while above -128), g and parent of node t.
+__device__ __forceinline__ float restarted_sum(float sum, float g, int par, int n) {
+  float rec = sum;
+  for (int s = 0; s < n; ++s) {  // (after s rounds right down to depth s)
+    const float above = __shfl(rec, par >= 0 ? par : 0);
+    const bool past = par >= 0 && above < kForget;
+    if (past || sum <= kForget) rec = par < 0 || (past && g > above) ? g : above + g;
+  }
+  return rec;
 }
 
 // Renumbers grid.x so that consecutive k-heads, which read and write neighbouring bytes, share an
@@ -232,7 +261,7 @@ struct VerifyLds {
   // q, k; hi, lo; inside a row see place()
   __device__ __forceinline__ _Float16 (*qk())[2][N][KS] { return NB > 1 ? qk_shared : qk_own; }
   alignas(16) float inv[2][N];  // inverse of the row's power of two, q and k
-  alignas(16) float gam[HP][N], eg[HP][N], beta[HP][N];
+  alignas(16) float gam[HP][N], gam_lo[HP][N], eg[HP][N], beta[HP][N];
   uint32_t anc[N][2];         // ancestors (bit j: node j), not itself
   uint32_t kbad[2], qbad[2];  // nodes whose k (q) is not finite
   uint32_t abad[HP][2];       // nodes whose row of A is not finite, by head
@@ -369,30 +398,33 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
   if (tree_wave) {
     // ancestors and sums of g along the root path by doubling: after round s they cover 2^s levels
     int up = par;
-    float gam = gval;
+    Gamma gam = gamma_of(gval);
     uint32_t lo = up >= 0 && up < 32 ? 1u << up : 0u, hi = 0u;
     if constexpr (N > 32) hi = up >= 32 ? 1u << (up - 32) : 0u;
     while (__any(up >= 0)) {
       const int from = up >= 0 ? up : lane;
       const uint32_t lo2 = __shfl(lo, from), hi2 = N > 32 ? __shfl(hi, from) : 0u;
-      const float g2 = __shfl(gam, from);
+      const Gamma g2 = {__shfl(gam.hi, from), __shfl(gam.lo, from)};
       const int up2 = __shfl(up, from);
       if (up >= 0) {
         lo |= lo2;
         hi |= hi2;
-        gam += g2;
+        gam = gam + g2;
         up = up2;
       }
     }
+    float rec = gam.hi;
+    if (a.gamma_rec && __any(gam.hi <= kForget)) rec = restarted_sum(gam.hi, gval, par, n);
     if (lane < N) {
       if (w == 0) {
         lds.anc[lane][0] = lo;
         lds.anc[lane][1] = hi;
       }
-      lds.gam[w][lane] = gam;
-      lds.eg[w][lane] = decay(gam);
+      lds.gam[w][lane] = gam.hi;
+      lds.gam_lo[w][lane] = gam.lo;
+      lds.eg[w][lane] = expf(gam.hi) * (1.0f + gam.lo);
       lds.beta[w][lane] = bval;
-      if (lane < n && a.gamma_rec) a.gamma_rec[gi] = gam;
+      if (lane < n && a.gamma_rec) a.gamma_rec[gi] = rec;
     }
   }
 #pragma unroll
@@ -529,12 +561,14 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
       for (int t = 0; t < HP; ++t) {
         tile[t] = f32x4{0.f, 0.f, 0.f, 0.f};
         if (t >= nh) break;
-        const float gcol = lds.gam[t][col];
+        const float gcol = lds.gam[t][col], lcol = lds.gam_lo[t][col];
         const f32x4 grow = *reinterpret_cast<const f32x4*>(&lds.gam[t][row]);
+        const f32x4 lrow = *reinterpret_cast<const f32x4*>(&lds.gam_lo[t][row]);
         const f32x4 brow = *reinterpret_cast<const f32x4*>(&lds.beta[t][row]);
 #pragma unroll
         for (int q = 0; q < 4; ++q)
-          tile[t][q] = use[q] ? acc[q] * decay(grow[q] - gcol) * (is_p ? 1.0f : -brow[q]) : 0.f;
+          tile[t][q] =
+              use[q] ? acc[q] * decay((grow[q] - gcol) + (lrow[q] - lcol)) * (is_p ? 1.0f : -brow[q]) : 0.f;
         // (a row of P reaches its own node's o alone)
         if (!is_p && __any(!all_finite(tile[t]))) {
 #pragma unroll
@@ -809,23 +843,34 @@ __global__ __launch_bounds__(AcceptCfg<D>::NW* kWave) void tree_accept_kernel(Ac
   // lane t < n: G_t, and its root path's nodes by doubling the ancestors
   const float gam = lane < n ? a.gamma_rec[static_cast<int64_t>(first + lane) * a.hv + j] : 0.f;
   int up = lane < n ? parent_of(a.parents, first, lane) : -1;
+  // sums that started again on the way (restarted_sum): g of every node out of them, summed in two halves
+  const bool again = __any(gam < kForget);
+  Gamma sum = {gam, 0.f};
+  if (again) {
+    const float before = __shfl(gam, up >= 0 ? up : 0);
+    // (two sums of -inf: finite g whose sum is not)
+    sum = gamma_of(up < 0 || (before < kForget && gam > before) ? gam : gam == -__builtin_inff() ? gam : gam - before);
+  }
   uint32_t lo = lane < 32 ? 1u << lane : 0u, hi = lane >= 32 ? 1u << (lane - 32) : 0u;
   while (__any(up >= 0)) {
     const int from = up >= 0 ? up : lane;
     const uint32_t lo2 = __shfl(lo, from), hi2 = __shfl(hi, from);
     const int up2 = __shfl(up, from);
+    const Gamma s2 = {__shfl(sum.hi, from), __shfl(sum.lo, from)};
     if (up >= 0) {
       lo |= lo2;
       hi |= hi2;
       up = up2;
+      if (again) sum = sum + s2;
     }
   }
   uint64_t path = static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(lo), last)) |
                   static_cast<uint64_t>(static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(hi), last))) << 32;
   // lane t: e^(G_a - G_t), the factor of node t's update
-  const float gend = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gam), last));
-  const float alpha = decay(gend);
-  const float f = decay(gend - gam);
+  const float end_hi = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sum.hi), last));
+  const float end_lo = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(sum.lo), last));
+  const float alpha = expf(end_hi) * (1.0f + end_lo);
+  const float f = expf((end_hi - sum.hi) + (end_lo - sum.lo));
   const f32x4* kb = reinterpret_cast<const f32x4*>(a.k_rec + (static_cast<int64_t>(first) * a.hk + h) * D) + c;
   const float* ub = a.u_rec + (static_cast<int64_t>(first) * a.hv + j) * D + row0;
   const int64_t kstep = static_cast<int64_t>(a.hk) * (D / 4), ustep = static_cast<int64_t>(a.hv) * D;

@@ -370,7 +370,8 @@ gdn_status gdn_slot_copy(const gdn_dims* dims, const uint64_t* src_state_ptrs, c
  *             Two slots may share a state here.
  *  k_rec, u_rec, gamma_rec  the record gdn_tree_accept needs, all three or none: fp32
  *             [total_nodes][Hk][d] (normalised k), [total_nodes][Hv][d] (u) and
- *             [total_nodes][Hv] (G).
+ *             [total_nodes][Hv] (G, except below a path whose sum of g is under -128: where the parent's
+ *             entry is and the node's own g lies above it, the entry is g, the sum starting again).
  * Each slot's result is the same bits whatever else is in the call. The products with the state
  * and between the tokens are as exact as fp32 ones whatever dims->mma is.
  *  Alignment: x, conv_w, conv_b, k_rec, u_rec 16-byte aligned, x_stride a multiple of 16 bytes.
@@ -387,8 +388,9 @@ gdn_status gdn_tree_verify(const gdn_dims* dims, const void* x, int64_t x_stride
  * gdn_tree_accept -- the step after gdn_tree_verify: moves each slot to its accepted node a,
  *   S <- e^G_a S + sum_{j above or at a} e^(G_a - G_j) u_j k_j^T,
  * and its conv state to the last K-1 rows of [conv state, x of a's root path], both in place:
- * the state and conv state that decoding the path token by token would leave (to rounding; the
- * conv state bit for bit).
+ * the state and conv state that decoding the path token by token would leave (to rounding, to which the
+ * fp32 sums G add: a decay e^(G_a - G_j) is off by half a step of either, 2^-24 of |G| and 2^-18 at most;
+ * the conv state bit for bit).
  *
  *  x, parents, cu_nodes, m, total_nodes, max_nodes  as given to gdn_tree_verify.
  *  k_rec, u_rec, gamma_rec  its record (read only).
