@@ -563,6 +563,7 @@ gdn_status gdn_tree_verify(const gdn_dims* dims, const void* x, int64_t x_stride
   a.width = dims->conv_width;
   a.silu = dims->activation == GDN_ACT_SILU;
   a.bf16 = dims->in_dtype == GDN_BF16;
+  a.mma = resolve_mma(dims);
   return hip_status(gdn::launch_tree_verify(a, m, static_cast<hipStream_t>(stream)), fn);
 }
 

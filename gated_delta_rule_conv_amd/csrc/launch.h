@@ -133,6 +133,7 @@ struct TreeArgs {
   int32_t width;
   int32_t silu;
   int32_t bf16;
+  int32_t mma;  // 1 = fp32, 2 = bf16x3's place: fp16 pairs (resolved)
 };
 
 hipError_t launch_tree_verify(const TreeArgs& a, int32_t m, hipStream_t s);

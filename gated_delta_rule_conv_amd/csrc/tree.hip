@@ -81,12 +81,15 @@ __device__ __forceinline__ int xcd_head() {
   return (n % 8 == 0) ? (b % 8) * (n / 8) + b / 8 : b;
 }
 
-// fp16 operands that carry an fp32 value in two halves: hi = fp16(x), lo = fp16(x - hi), about 22
-// significant bits. A product is hi hi' + hi lo' + lo hi' on v_mfma_f32_16x16x32_f16 with fp32
-// accumulation; what is left out is 2^-22 of it at most, typically 2^-24, as an fp32 product's own
-// rounding. fp16 has little range, so every row is first multiplied by a power of two (exact) that
-// puts its norm (or largest value) at 2^11 .. 2^13, and the result by its inverse: parts below fp16's
-// normal range are then under 2^-25 of the row.
+// The products with d terms, in the two policies of gdn_mma. FP32: v_mfma_f32_16x16x4_f32.
+// BF16X3, for inputs of 8 significant bits: fp16 operands that carry an fp32 value in two halves: hi = fp16(x),
+// lo = fp16(x - hi), about 22 significant bits. A product is hi hi' + hi lo' + lo hi' on
+// v_mfma_f32_16x16x32_f16 with fp32 accumulation; what is left out is 2^-22 of it at most, typically 2^-24, as
+// an fp32 product's own rounding. fp16 has little range, so every row is first multiplied by a power of two
+// (exact) that puts its norm (or largest value) at 2^12 .. 2^13, and the result by its inverse. A value far
+// below its row's norm is so held to 2^-37 of the norm, not to 2^-22 of itself: what a sum loses is small beside
+// the rows' norms, but not always beside the sum, which is why fp32 inputs do not take this form by default.
+// 64 slots x 64 nodes of bf16 x take 123 us with pairs and 169 us in fp32, x 16 nodes 44 and 48 us.
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
@@ -94,11 +97,38 @@ struct Half2 {
   f16x8 hi, lo;
 };
 
-__device__ __forceinline__ void mma_f16x3(f32x4& acc, const Half2& a, const Half2& b) {
-  acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.lo, b.hi, acc, 0, 0, 0);
-  acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.lo, acc, 0, 0, 0);
-  acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.hi, acc, 0, 0, 0);
-}
+struct PairMma {
+  static constexpr bool kFull = false;
+  static constexpr int kStep = 32;
+  typedef Half2 Frag;
+  __device__ __forceinline__ static void mma(f32x4& acc, const Frag& a, const Frag& b) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.lo, b.hi, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.lo, acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.hi, acc, 0, 0, 0);
+  }
+  __device__ __forceinline__ static void mma3(f32x4 (&acc)[3], const Frag& a, const Frag& b) {
+    acc[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.hi, acc[0], 0, 0, 0);
+    acc[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.lo, b.hi, acc[1], 0, 0, 0);
+    acc[2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.lo, acc[2], 0, 0, 0);
+  }
+};
+
+// (The steps' LDS reads are fenced in twos where two workgroups share a CU: all of them ahead of the products
+// spill, 64 slots x 16 nodes of fp32 x 51 -> 67 us.)
+struct FullMma {
+  static constexpr bool kFull = true;
+  static constexpr int kStep = 16;
+  typedef f32x4 Frag;
+  __device__ __forceinline__ static void mma(f32x4& acc, const Frag& a, const Frag& b) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[q], b[q], acc, 0, 0, 0);
+  }
+  // ... on three independent chains (summed by total())
+  __device__ __forceinline__ static void mma3(f32x4 (&acc)[3], const Frag& a, const Frag& b) {
+#pragma unroll
+    for (int q = 0; q < 4; ++q) acc[q % 3] = __builtin_amdgcn_mfma_f32_16x16x4f32(a[q], b[q], acc[q % 3], 0, 0, 0);
+  }
+};
 
 // The exponent that takes a magnitude below 2^e to below 2^13 (kept where its inverse is finite too).
 __device__ __forceinline__ int f16_shift(int e) { return e < -97 ? 110 : 13 - e; }
@@ -109,13 +139,6 @@ __device__ __forceinline__ int f16_shift(int e) { return e < -97 ? 110 : 13 - e;
 __device__ __forceinline__ _Float16 half_hi(float x, float mul) { return static_cast<_Float16>(fmaf(x, mul, 0.0f)); }
 __device__ __forceinline__ _Float16 half_lo(float x, float mul, _Float16 hi) {
   return static_cast<_Float16>(fmaf(x, mul, -static_cast<float>(hi)));
-}
-
-// a * b of 32-wide steps on three independent chains (summed by total())
-__device__ __forceinline__ void mma_f16x3(f32x4 (&acc)[3], const Half2& a, const Half2& b) {
-  acc[0] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.hi, acc[0], 0, 0, 0);
-  acc[1] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.lo, b.hi, acc[1], 0, 0, 0);
-  acc[2] = __builtin_amdgcn_mfma_f32_16x16x32_f16(a.hi, b.lo, acc[2], 0, 0, 0);
 }
 
 // (where the magnitudes' sum overflows: false as well)
@@ -211,8 +234,8 @@ __device__ __forceinline__ void barrier_lds() {
 //   A_ij = -beta_i e^(G_i - G_j) k_i.k_j for j above i, else 0;   P_ij = e^(G_i - G_j) q_i.k_j, j above or at i
 //   U = (I - A)^-1 (beta (V - e^G M)), O = e^G W + P U
 // (I - A) is unit lower triangular (parents come first): its 16x16 diagonal blocks are inverted by
-// substitution, the rest is block substitution. The products with d terms (M, W, A, P) run on fp16
-// pairs, the others on fp32 MFMA with the contraction index dealt as 4 (l / 16) + r, so that a result
+// substitution, the rest is block substitution. The products with d terms (M, W, A, P) run in the call's
+// policy (MMA), the others on fp32 MFMA with the contraction index dealt as 4 (l / 16) + r, so that a result
 // tile (lane l: rows 4 (l / 16) + r of column l % 16) is the right operand of the next product as it stands.
 //
 // Everything a workgroup reads from memory is loaded before anything is computed: its state rows
@@ -236,10 +259,21 @@ __device__ __forceinline__ void barrier_lds() {
 // state row, zeros go in their place, and the results of the marked nodes and their descendants are set to
 // NaN at the end. An inverse that is not finite (a path of unnormalised keys that diverges) is formed
 // again without products by zeros; its rows are then not finite on that path alone, and so u's.
-template <typename T, int K, int D, int NB, int HP>
+// q and k in LDS: fp32 rows, or hi and lo rows of halves (inside a row see place()).
+template <typename MMA, int N, int D>
+struct QkRows {
+  static constexpr int S = D + 16;  // fp16 values of a row (conflict-free fragment reads)
+  _Float16 v[2][2][N][S];           // q, k; hi, lo
+};
+template <int N, int D>
+struct QkRows<FullMma, N, D> {
+  static constexpr int S = D + 4;
+  float v[2][N][S];
+};
+
+template <typename MMA, typename T, int K, int D, int NB, int HP>
 struct VerifyLds {
   static constexpr int N = 16 * NB;
-  static constexpr int KS = D + 16;  // fp16 values of a row of K and Q (conflict-free fragment reads)
   static constexpr int PS = N + 4;   // floats of a row of A and P
   static constexpr int XS = 2 * D + 16 / sizeof(T);  // values of a row of x's q and k channels
   static constexpr int VS = HP * D + 16 / sizeof(T);  // ... and of the heads' v channels
@@ -255,12 +289,11 @@ struct VerifyLds {
   };
   union {
     T xv[K - 1 + N][VS];
-    _Float16 qk_shared[NB > 1 ? 2 : 0][2][N][KS];  // (larger trees: written once v is convolved)
+    QkRows<MMA, N, D> qk_shared[NB > 1 ? 1 : 0];  // (larger trees: written once v is convolved)
   };
-  _Float16 qk_own[NB > 1 ? 0 : 2][2][N][KS];
-  // q, k; hi, lo; inside a row see place()
-  __device__ __forceinline__ _Float16 (*qk())[2][N][KS] { return NB > 1 ? qk_shared : qk_own; }
-  alignas(16) float inv[2][N];  // inverse of the row's power of two, q and k
+  QkRows<MMA, N, D> qk_own[NB > 1 ? 0 : 1];
+  __device__ __forceinline__ auto& qk() { return (NB > 1 ? qk_shared : qk_own)[0].v; }
+  alignas(16) float inv[2][N];  // pairs: inverse of the row's power of two, q and k
   alignas(16) float gam[HP][N], gam_lo[HP][N], eg[HP][N], beta[HP][N];
   uint32_t anc[N][2];         // ancestors (bit j: node j), not itself
   uint32_t kbad[2], qbad[2];  // nodes whose k (q) is not finite
@@ -284,11 +317,12 @@ constexpr int kVerifyHeads = 2;
 constexpr int verify_par(int nb, int d) { return nb > 2 && d < 128 ? 2 : 1; }
 constexpr int verify_join(int nb, int d) { return nb > 2 && d == 128 ? 2 : 1; }
 
-template <typename T, int K, int D, int NB, bool SILU>
+template <typename MMA, typename T, int K, int D, int NB, int SILU>  // (SILU -1: as the arguments say)
 __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_verify_kernel(
     TreeArgs a, int32_t heads, int32_t chunks) {
   constexpr int HP = kVerifyHeads, PAR = verify_par(NB, D), SEQ = HP / PAR, JOIN = verify_join(NB, D);
-  using Lds = VerifyLds<T, K, D, NB, HP>;
+  using Lds = VerifyLds<MMA, T, K, D, NB, HP>;
+  const bool silu_on = SILU < 0 ? a.silu != 0 : SILU != 0;
   constexpr int WH = D / 16;         // waves of a head
   constexpr int W = WH * PAR;        // waves
   constexpr int NT = W * kWave;      // threads
@@ -358,9 +392,16 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
   const int d0 = (piece * 4) % D;
   const int ch0 = (is_k ? r.hk * D : 0) + h * D + d0;
   typename V4::Raw tap[K], bias;
+  const auto load_taps = [&]() {
 #pragma unroll
-  for (int t = 0; t < K; ++t) tap[t] = V4::load_raw(static_cast<const T*>(a.w) + static_cast<int64_t>(ch0) * K + 4 * t);
-  bias = V4::load_raw(static_cast<const T*>(a.b ? a.b : a.w) + ch0);
+    for (int t = 0; t < K; ++t) tap[t] = V4::load_raw(static_cast<const T*>(a.w) + static_cast<int64_t>(ch0) * K + 4 * t);
+    bias = V4::load_raw(static_cast<const T*>(a.b ? a.b : a.w) + ch0);
+  };
+  // (fp32 rows of up to 32 nodes, their taps and the state do not fit two workgroups' registers together:
+  // 64 slots x 32 nodes take 78 us (pairs 61) with the taps' loads behind the rows', 89 us (66) with all of them
+  // here, spilled)
+  constexpr bool kLateTaps = sizeof(T) == 4 && NB == 2 && D == 128;
+  if constexpr (!kLateTaps) load_taps();
   // the wave's state rows of its head lh: lane (c4, l16) holds columns 16 e + 4 c4 .. + 3 of row l16
   f32x4 s[JOIN][D / 16];
   const auto load_state = [&](f32x4 (&s)[D / 16], int lh) {
@@ -432,6 +473,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
     const int row = it * RW + rx;
     if (row < K - 1 + n && px < pn) *reinterpret_cast<Raw*>(px < 2 * D ? &lds.x[row][px] : &lds.xv[row][px - 2 * D]) = raw[it];
   }
+  if constexpr (kLateTaps) load_taps();
 
   barrier_lds();
 
@@ -453,7 +495,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
           for (int q = 0; q < K - 1; ++q)
             acc = fmaf(elem_f32<T>(vtap[sq][q]), elem_f32<T>(lds.xv[(rows >> (8 * (K - 2 - q))) & 255][off]), acc);
           acc = fmaf(elem_f32<T>(vtap[sq][K - 1]), elem_f32<T>(lds.xv[K - 1 + t][off]), acc);
-          v[sq][b][e] = SILU ? silu(acc) : acc;  // (rows past the tree hold anything)
+          v[sq][b][e] = silu_on ? silu(acc) : acc;  // (rows past the tree hold anything)
         }
       }
     }
@@ -473,7 +515,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
 #pragma unroll
     for (int q = 0; q < K - 1; ++q) win[q] = V4::load_raw(&lds.x[(rows >> (8 * (K - 2 - q))) & 255][off]);
     float y[4];
-    conv4_raw<T, K>(tap, bias, a.b != nullptr, win, V4::load_raw(&lds.x[K - 1 + t][off]), SILU, y);
+    conv4_raw<T, K>(tap, bias, a.b != nullptr, win, V4::load_raw(&lds.x[K - 1 + t][off]), silu_on, y);
 #pragma unroll
     for (int e = 0; e < 4; ++e) y[e] = t < n ? y[e] : 0.f;  // (rows past the tree hold anything)
     const auto row_sum = [](float z) {  // over the D / 4 lanes of a row
@@ -511,24 +553,32 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
       for (int m = 1; m < D / 4; m *= 2) most = fmaxf(most, __shfl_xor(most, m));
       top = __builtin_amdgcn_frexp_expf(most);
     }
-    const int sh = f16_shift(top);
-    if (d0 == 0) lds.inv[is_k][t] = ldexpf(1.0f, -sh);
-    const float mul = ldexpf(1.0f, sh);
-    f16x4 hi, lo;
+    if constexpr (MMA::kFull) {
+      *reinterpret_cast<f32x4*>(&lds.qk()[is_k][t][d0]) = f32x4{z[0], z[1], z[2], z[3]};
+    } else {
+      const int sh = f16_shift(top);
+      if (d0 == 0) lds.inv[is_k][t] = ldexpf(1.0f, -sh);
+      const float mul = ldexpf(1.0f, sh);
+      f16x4 hi, lo;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      hi[e] = half_hi(z[e], mul);
-      lo[e] = half_lo(z[e], mul, hi[e]);
+      for (int e = 0; e < 4; ++e) {
+        hi[e] = half_hi(z[e], mul);
+        lo[e] = half_lo(z[e], mul, hi[e]);
+      }
+      *reinterpret_cast<f16x4*>(&lds.qk()[is_k][0][t][place(d0)]) = hi;
+      *reinterpret_cast<f16x4*>(&lds.qk()[is_k][1][t][place(d0)]) = lo;
     }
-    *reinterpret_cast<f16x4*>(&lds.qk()[is_k][0][t][place(d0)]) = hi;
-    *reinterpret_cast<f16x4*>(&lds.qk()[is_k][1][t][place(d0)]) = lo;
   }
   barrier_lds();
 
-  const auto frag = [&](int which, int b, int step) {
-    const int at = step * 32 + c4 * 8;
-    return Half2{*reinterpret_cast<const f16x8*>(&lds.qk()[which][0][16 * b + l16][at]),
-                 *reinterpret_cast<const f16x8*>(&lds.qk()[which][1][16 * b + l16][at])};
+  const auto frag = [&](int which, int b, int step) -> typename MMA::Frag {
+    if constexpr (MMA::kFull) {
+      return *reinterpret_cast<const f32x4*>(&lds.qk()[which][16 * b + l16][step * 16 + c4 * 4]);
+    } else {
+      const int at = step * 32 + c4 * 8;
+      return Half2{*reinterpret_cast<const f16x8*>(&lds.qk()[which][0][16 * b + l16][at]),
+                   *reinterpret_cast<const f16x8*>(&lds.qk()[which][1][16 * b + l16][at])};
+    }
   };
   // A and P of all heads: the lower blocks of k k^T and q k^T, dealt to the waves, k k^T's diagonal
   // blocks first; the wave that has one inverts I - A there, for all heads at once
@@ -550,12 +600,16 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
       f32x4 acc3[3];
       zero3(acc3);
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) mma_f16x3(acc3, frag(is_p ? 0 : 1, bi, e), frag(1, bj, e));
+      for (int e = 0; e < D / MMA::kStep; ++e) {
+        MMA::mma3(acc3, frag(is_p ? 0 : 1, bi, e), frag(1, bj, e));
+        if (MMA::kFull && NB <= 2 && e % 2) __builtin_amdgcn_sched_barrier(0);
+      }
       bool use[4];
 #pragma unroll
       for (int q = 0; q < 4; ++q)
         use[q] = ((lds.anc[row + q][col >> 5] >> (col & 31)) & 1u) || (is_p && row + q == col);
-      const f32x4 acc = total(acc3) * *reinterpret_cast<const f32x4*>(&lds.inv[is_p ? 0 : 1][row]) * lds.inv[1][col];
+      f32x4 acc = total(acc3);
+      if constexpr (!MMA::kFull) acc = acc * *reinterpret_cast<const f32x4*>(&lds.inv[is_p ? 0 : 1][row]) * lds.inv[1][col];
       f32x4 tile[HP];
 #pragma unroll
       for (int t = 0; t < HP; ++t) {
@@ -602,46 +656,55 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
 #pragma unroll
   for (int sq = 0; sq < SEQ; sq += JOIN) {
     const auto head = [&](int t) { return (sq + t) * PAR + hw; };  // t < JOIN: the wave's heads of this round
-    // the state rows as fp16 pairs, then M and W
+    // M and W (the state rows as fp16 pairs)
     f32x4 m[JOIN][NB], o[JOIN][NB];
-    float smul[JOIN], sinv[JOIN];
+    float smul[JOIN], sinv[JOIN];  // pairs: the row's power of two and its inverse
     if (head(0) < nh) {
 #pragma unroll
       for (int t = 0; t < JOIN; ++t) {
 #pragma unroll
         for (int b = 0; b < NB; ++b) m[t][b] = o[t][b] = f32x4{0.f, 0.f, 0.f, 0.f};
-        float top = 0.f;
+        smul[t] = sinv[t] = 1.f;
+        if constexpr (!MMA::kFull) {
+          float top = 0.f;
 #pragma unroll
-        for (int e = 0; e < D / 16; ++e)
+          for (int e = 0; e < D / 16; ++e)
 #pragma unroll
-          for (int q = 0; q < 4; ++q) top = fmaxf(top, fabsf(s[t][e][q]));
-        const auto larger = [](float p, float q) { return fmaxf(p, q); };
-        top = across32(across16(top, larger), larger);
-        const int sh = f16_shift(__builtin_amdgcn_frexp_expf(top));
-        smul[t] = ldexpf(1.0f, sh);
-        sinv[t] = ldexpf(1.0f, -sh);
+            for (int q = 0; q < 4; ++q) top = fmaxf(top, fabsf(s[t][e][q]));
+          const auto larger = [](float p, float q) { return fmaxf(p, q); };
+          top = across32(across16(top, larger), larger);
+          const int sh = f16_shift(__builtin_amdgcn_frexp_expf(top));
+          smul[t] = ldexpf(1.0f, sh);
+          sinv[t] = ldexpf(1.0f, -sh);
+        }
       }
 #pragma unroll
-      for (int e = 0; e < D / 32; ++e) {
-        Half2 sf[JOIN];
+      for (int e = 0; e < D / MMA::kStep; ++e) {
+        typename MMA::Frag sf[JOIN];
 #pragma unroll
-        for (int t = 0; t < JOIN; ++t)
+        for (int t = 0; t < JOIN; ++t) {
+          if constexpr (MMA::kFull) {
+            sf[t] = s[t][e];
+          } else {
 #pragma unroll
-          for (int q = 0; q < 8; ++q) {
-            const float y = s[t][2 * e + q / 4][q % 4];
-            sf[t].hi[q] = half_hi(y, smul[t]);
-            sf[t].lo[q] = half_lo(y, smul[t], sf[t].hi[q]);
+            for (int q = 0; q < 8; ++q) {
+              const float y = s[t][2 * e + q / 4][q % 4];
+              sf[t].hi[q] = half_hi(y, smul[t]);
+              sf[t].lo[q] = half_lo(y, smul[t], sf[t].hi[q]);
+            }
           }
+        }
 #pragma unroll
         for (int b = 0; b < NB; ++b)
           if (16 * b < n) {
-            const Half2 kf = frag(1, b, e), qf = frag(0, b, e);
+            const typename MMA::Frag kf = frag(1, b, e), qf = frag(0, b, e);
 #pragma unroll
             for (int t = 0; t < JOIN; ++t) {
-              mma_f16x3(m[t][b], kf, sf[t]);
-              mma_f16x3(o[t][b], qf, sf[t]);
+              MMA::mma(m[t][b], kf, sf[t]);
+              MMA::mma(o[t][b], qf, sf[t]);
             }
           }
+        if (MMA::kFull && NB <= 2 && e % 2) __builtin_amdgcn_sched_barrier(0);
       }
       if constexpr (JOIN == 1) {
         if (head(1) < nh) load_state(s[0], head(1));
@@ -665,8 +728,11 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
     for (int b = 0; b < NB; ++b) {
       if (16 * b >= n) break;
       const int t0 = 16 * b + 4 * c4;
-      const f32x4 kinv = *reinterpret_cast<const f32x4*>(&lds.inv[1][t0]);
-      const f32x4 qinv = *reinterpret_cast<const f32x4*>(&lds.inv[0][t0]);
+      f32x4 kinv = {1.f, 1.f, 1.f, 1.f}, qinv = kinv;
+      if constexpr (!MMA::kFull) {
+        kinv = *reinterpret_cast<const f32x4*>(&lds.inv[1][t0]);
+        qinv = *reinterpret_cast<const f32x4*>(&lds.inv[0][t0]);
+      }
 #pragma unroll
       for (int t = 0; t < JOIN; ++t) {
         const int lh = head(t);
@@ -746,10 +812,12 @@ hipError_t verify_nb(const TreeArgs& a, int32_t m, hipStream_t s) {
   const int32_t chunks = heads == 1 ? a.r.group : pairs;  // workgroups of a k-head
   const dim3 grid(static_cast<unsigned>(a.r.hk * chunks), static_cast<unsigned>(m));
   constexpr int threads = D * 4 * verify_par(NB, D);
-  if (a.silu)
-    tree_verify_kernel<T, K, D, NB, true><<<grid, threads, 0, s>>>(a, heads, chunks);
+  if (a.mma == kPolFP32)  // (one kernel for either activation: fp32 MFMA leaves the vector units idle enough)
+    tree_verify_kernel<FullMma, T, K, D, NB, -1><<<grid, threads, 0, s>>>(a, heads, chunks);
+  else if (a.silu)
+    tree_verify_kernel<PairMma, T, K, D, NB, 1><<<grid, threads, 0, s>>>(a, heads, chunks);
   else
-    tree_verify_kernel<T, K, D, NB, false><<<grid, threads, 0, s>>>(a, heads, chunks);
+    tree_verify_kernel<PairMma, T, K, D, NB, 0><<<grid, threads, 0, s>>>(a, heads, chunks);
   return hipGetLastError();
 }
 

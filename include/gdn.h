@@ -65,7 +65,8 @@ typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
  * causal Conv1d, so the default is the identity; SiLU is offered as an option. */
 typedef enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
 
-/* Matrix-core precision of the prefill contractions (decode is plain fp32 FMA).
+/* Matrix-core precision of the prefill contractions (decode is plain fp32 FMA), and of
+ * gdn_tree_verify's products over d, for which BF16X3 is closer than its name: see there.
  *  AUTO   : FP32 when in_dtype is F32, BF16X3 when in_dtype is BF16.
  *  FP32   : v_mfma_f32_16x16x4_f32, fp32 operands.
  *  BF16X3 : every fp32 operand split as hi + lo (two bf16 values); each product is
@@ -372,8 +373,10 @@ gdn_status gdn_slot_copy(const gdn_dims* dims, const uint64_t* src_state_ptrs, c
  *             [total_nodes][Hk][d] (normalised k), [total_nodes][Hv][d] (u) and
  *             [total_nodes][Hv] (G, except below a path whose sum of g is under -128: where the parent's
  *             entry is and the node's own g lies above it, the entry is g, the sum starting again).
- * Each slot's result is the same bits whatever else is in the call. The products with the state
- * and between the tokens are as exact as fp32 ones whatever dims->mma is.
+ * Each slot's result is the same bits whatever else is in the call. The products over d (S k, S q, k . k,
+ * q . k) are fp32 ones under GDN_MMA_FP32 (AUTO with fp32 input). Under GDN_MMA_BF16X3 (AUTO with bf16
+ * input) they take each value of q, k and S as two fp16 halves under one power of two a row: held to
+ * 2^-22 of itself or, if that is more, to 2^-37 of the row's norm.
  *  Alignment: x, conv_w, conv_b, k_rec, u_rec 16-byte aligned, x_stride a multiple of 16 bytes.
  *  Errors: GDN_ERR_UNSUPPORTED for max_nodes above GDN_TREE_MAX_NODES; else as gdn_decode_fused.
  */
