@@ -452,8 +452,9 @@ gdn_status gdn_slot_unpack(const gdn_dims* dims, int32_t format, const uint64_t*
  *   y = (n * weight + bias) * act(gate)        with a gate
  *   y = act(n * weight + bias)                 without
  *   y = n' * weight + bias, n' the norm of x * act(gate)      gate_first
- * No statistic crosses tokens, so prefill and decode rows give the same bits. Sums are fp32: x (for
- * gate_first x act(gate)) up to about 1e18 in magnitude.
+ * No statistic crosses tokens, so prefill and decode rows give the same bits. Sums are fp32, under a
+ * power of two where the squares leave its range: any finite x will do (for gate_first any finite
+ * x act(gate)). A group of zeros with eps = 0 is 0 / 0: NaN.
  */
 typedef struct gdn_norm_dims {
   int32_t struct_size;   /* sizeof(gdn_norm_dims) as compiled by the caller */
