@@ -365,8 +365,8 @@ hipError_t launch_t(const NormArgs& a, hipStream_t s) {
 }  // namespace
 
 // A launch holds fewer than 2^32 threads: a call of more than 2^23 groups goes in pieces of rows
-// (2^23 groups of 256 threads; a single row of more groups than that has groups of one or two
-// values, 8 threads each).
+// (2^23 groups of 256 threads at most; a single row of 2^23 groups or more has groups of one or two
+// values, 4 lanes each).
 hipError_t launch_group_norm(const NormArgs& args, hipStream_t s) {
   const int32_t most = args.groups < (1 << 23) ? (1 << 23) / args.groups : 1;
   for (int32_t r = 0; r < args.rows;) {

@@ -1,4 +1,4 @@
-"""gdn_group_norm over the whole range of x.
+"""gdn_group_norm over the whole range of x, and in calls of more groups than one launch takes.
 
 Tolerances as in test_gpu_group_norm: 40 x 2^-24 of |n w| (plus the mean's share, centred); rows are
 scaled by powers of two where their squares leave the fp32 range, which rounds nothing."""
@@ -68,3 +68,17 @@ def test_gate_first_of_large_products(size):
     x *= 2.0 ** 70
     run(o, x, gate, w, b, y)
     check(o, x, gate, w, b, y)
+
+
+@pytest.mark.parametrize("groups,size,rows,pad", [(3, 2, (1 << 23) // 3 + 5, 3), (1, 1, (1 << 23) + 3, 1), (4096, 2, 2050, 7),
+                                                  ((1 << 23) + 1, 1, 2, 0), (1 << 23, 2, 2, 5)])
+def test_more_groups_than_a_launch_takes(groups, size, rows, pad):
+    """A call of more than 2^23 groups goes in pieces of rows; so does a row of as many by itself."""
+    announce(f"norm: {rows} x {groups} groups of {size}")
+    o = dict(groups=groups, size=size, gate="bf16", y="f32")
+    t = make(o, rows, seed=3, pad=pad)
+    t[4].fill_(7.0)
+    run(o, *t)
+    for a in range(0, rows, 1 << 21):
+        part = slice(a, min(rows, a + (1 << 21)))
+        check(o, t[0][part], t[1][part], t[2], None, t[4][part])
