@@ -14,6 +14,8 @@ tensors and call the library; all arithmetic happens in the HIP kernels.
 
 from __future__ import annotations
 
+import ctypes
+
 import torch
 
 from . import _lib
@@ -170,19 +172,30 @@ def tree_record(dims: gdn_dims, total_nodes: int, device="cuda"):
             torch.empty((total_nodes, Hv), dtype=torch.float32, device=device))
 
 
-def _check_tree(dims, x, parents, cu_nodes, state_ptrs, conv_state_ptrs) -> None:
-    m = state_ptrs.numel()
-    assert x.shape[1] == channels(dims) and x.stride(1) == 1 and x.dtype == torch_in_dtype(dims)
-    assert cu_nodes.dtype == torch.int32 and cu_nodes.is_cuda and cu_nodes.numel() == m + 1
-    assert conv_state_ptrs.numel() == m
-    assert parents is None or (parents.dtype == torch.int32 and parents.is_cuda and parents.numel() == x.shape[0])
+_F32, _I32, _I64 = torch.float32, torch.int32, torch.int64
+_DTYPES = {GDN_F32: torch.float32, GDN_BF16: torch.bfloat16}
 
 
-def _check_record(dims, record, rows: int):
+def _at(fn: str, name: str, t: torch.Tensor, dtype, n: int, device: int) -> int:
+    """The address of t, which must be n contiguous values of dtype on the device: the kernels see no more of it."""
+    if t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.get_device() == device:
+        return t.data_ptr()
+    raise ValueError(f"{fn}: {name} must be {n} contiguous values of {dtype} on the device of the first operand (got "
+                     f"{t.numel()} of {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}, device {t.device})")
+
+
+def _check_rows(fn: str, dims, x: torch.Tensor, wide: int):
+    dtype = _DTYPES.get(dims.in_dtype)
+    if x.dtype is not dtype or x.dim() != 2 or x.shape[1] != wide or x.stride(1) != 1:
+        raise ValueError(f"{fn}: x must be rows of {wide} adjacent values of {dtype} (got {x.dtype}, shape "
+                         f"{tuple(x.shape)}, strides {x.stride()})")
+    return dtype
+
+
+def _record_at(fn: str, record, rows: int, Hk: int, Hv: int, d: int, device: int):
     k, u, gamma = record
-    Hk, Hv, d = dims.num_k_heads, dims.num_v_heads, dims.head_dim
-    assert k.numel() == rows * Hk * d and u.numel() == rows * Hv * d and gamma.numel() == rows * Hv
-    return record
+    return (_at(fn, "k of the record", k, _F32, rows * Hk * d, device), _at(fn, "u of the record", u, _F32, rows * Hv * d, device),
+            _at(fn, "gamma of the record", gamma, _F32, rows * Hv, device))
 
 
 def tree_verify(dims: gdn_dims, x: torch.Tensor, conv_w: torch.Tensor, conv_b, g: torch.Tensor, beta: torch.Tensor,
@@ -190,23 +203,31 @@ def tree_verify(dims: gdn_dims, x: torch.Tensor, conv_w: torch.Tensor, conv_b, g
                 conv_state_ptrs: torch.Tensor, record=None, stream=None) -> None:
     """The drafted trees of m slots answered against their states, which stay as they are;
     parents None: chains. record (from tree_record()) is needed to accept nodes afterwards."""
-    _check_tree(dims, x, parents, cu_nodes, state_ptrs, conv_state_ptrs)
-    rows = x.shape[0]
-    gates = rows * dims.num_v_heads
-    assert g.numel() == gates and beta.numel() == gates and o.numel() == gates * dims.head_dim and o.is_contiguous()
-    k, u, gamma = _check_record(dims, record, rows) if record is not None else (None, None, None)
-    _lib.gdn_tree_verify(dims, x, x.stride(0), conv_w, conv_b, g, beta, o, parents, cu_nodes, state_ptrs.numel(),
-                         x.shape[0], max_nodes, state_ptrs, conv_state_ptrs, k, u, gamma, stream)
+    fn, Hk, Hv, d = "tree_verify", dims.num_k_heads, dims.num_v_heads, dims.head_dim
+    rows, m, at = x.shape[0], state_ptrs.numel(), x.get_device()
+    wide, gates = (2 * Hk + Hv) * d, rows * Hv
+    dtype = _check_rows(fn, dims, x, wide)
+    k, u, gamma = _record_at(fn, record, rows, Hk, Hv, d, at) if record is not None else (None, None, None)
+    _lib._launch(
+        "gdn_tree_verify", _lib._LIB.gdn_tree_verify, stream, x, ctypes.byref(dims), x.data_ptr(), x.stride(0), _at(fn, "conv_w", conv_w, dtype, wide * dims.conv_width, at),
+        None if conv_b is None else _at(fn, "conv_b", conv_b, dtype, wide, at), _at(fn, "g", g, _F32, gates, at),
+        _at(fn, "beta", beta, _F32, gates, at), _at(fn, "o", o, _DTYPES.get(dims.out_dtype), gates * d, at),
+        None if parents is None else _at(fn, "parents", parents, _I32, rows, at),
+        _at(fn, "cu_nodes", cu_nodes, _I32, m + 1, at), m, rows, max_nodes,
+        _at(fn, "state_ptrs", state_ptrs, _I64, m, at), _at(fn, "conv_state_ptrs", conv_state_ptrs, _I64, m, at), k, u, gamma)
 
 
 def tree_accept(dims: gdn_dims, x: torch.Tensor, record, parents, cu_nodes: torch.Tensor, max_nodes: int,
                 accepted: torch.Tensor, state_ptrs: torch.Tensor, conv_state_ptrs: torch.Tensor, stream=None) -> None:
     """Slot i's state and conv state moved along the root path of node accepted[i] (-1: none)."""
-    _check_tree(dims, x, parents, cu_nodes, state_ptrs, conv_state_ptrs)
-    assert accepted.dtype == torch.int32 and accepted.is_cuda and accepted.numel() == state_ptrs.numel()
-    k, u, gamma = _check_record(dims, record, x.shape[0])
-    _lib.gdn_tree_accept(dims, x, x.stride(0), k, u, gamma, parents, cu_nodes, accepted, state_ptrs.numel(),
-                         x.shape[0], max_nodes, state_ptrs, conv_state_ptrs, stream)
+    fn, Hk, Hv, d = "tree_accept", dims.num_k_heads, dims.num_v_heads, dims.head_dim
+    rows, m, at = x.shape[0], state_ptrs.numel(), x.get_device()
+    _check_rows(fn, dims, x, (2 * Hk + Hv) * d)
+    k, u, gamma = _record_at(fn, record, rows, Hk, Hv, d, at)
+    _lib._launch(
+        "gdn_tree_accept", _lib._LIB.gdn_tree_accept, stream, x, ctypes.byref(dims), x.data_ptr(), x.stride(0), k, u, gamma, None if parents is None else _at(fn, "parents", parents, _I32, rows, at),
+        _at(fn, "cu_nodes", cu_nodes, _I32, m + 1, at), _at(fn, "accepted", accepted, _I32, m, at), m, rows, max_nodes,
+        _at(fn, "state_ptrs", state_ptrs, _I64, m, at), _at(fn, "conv_state_ptrs", conv_state_ptrs, _I64, m, at))
 
 
 def slot_pack(dims: gdn_dims, fmt: int, state_ptrs: torch.Tensor, conv_state_ptrs, packed_ptrs: torch.Tensor,

@@ -1,0 +1,133 @@
+"""The tensor helpers hand addresses to the kernels, so they refuse operands of another type, size, layout or
+device first (no GPU: operands are host tensors, or stand in for tensors of a GPU, and the launch is watched)."""
+
+import pytest
+import torch
+
+import gated_delta_rule_conv_amd as gdn
+from gated_delta_rule_conv_amd import _lib
+
+BF16, F32, I32, I64 = torch.bfloat16, torch.float32, torch.int32, torch.int64
+
+
+class OnGpu:
+    """A host tensor that says it is on a GPU's device."""
+
+    def __init__(self, t, index=0):
+        self._t, self._index = t, index
+
+    def __getattr__(self, name):
+        return getattr(self._t, name)
+
+    def get_device(self):
+        return self._index
+
+    @property
+    def device(self):
+        return torch.device("cuda", self._index)
+
+    @property
+    def is_cuda(self):
+        return True
+
+
+@pytest.fixture
+def launches(monkeypatch):
+    seen = []
+    monkeypatch.setattr(_lib, "_launch", lambda name, *a: seen.append(name))
+    return seen
+
+
+def wrong_forms(t, rows_may_be_apart=False):
+    """t in another type, one value short, and with gaps."""
+    other = {BF16: F32, F32: BF16, I32: I64, I64: I32, torch.uint8: I32}[t.dtype]
+    yield "type", t.to(other)
+    yield "short", t.reshape(-1)[:-1].clone() if t.dim() == 1 else t[..., :-1].clone()
+    yield "gaps", torch.stack([t, t], -1)[..., 0]
+
+
+def refused_one_at_a_time(operands, call, launches):
+    """call(operands) launches once; with any one operand in a wrong form, or on the host, or on another GPU, not."""
+    gpu = {k: None if t is None else OnGpu(t) for k, t in operands.items()}
+    call(gpu)
+    assert len(launches) == 1
+    for name, t in operands.items():
+        if t is None:
+            continue
+        forms = [(what, OnGpu(w)) for what, w in wrong_forms(t)] + [("host", t), ("elsewhere", OnGpu(t, 1))]
+        for what, w in forms:
+            with pytest.raises(ValueError):
+                call(dict(gpu, **{name: w}))
+            assert len(launches) == 1, (name, what)
+
+
+def tree_operands(dtype=BF16, out=F32, bias=True):
+    hk, hv, d, width, rows, m = 2, 4, 32, 3, 5, 2
+    ch = (2 * hk + hv) * d
+    return dict(x=torch.zeros(rows, ch, dtype=dtype), conv_w=torch.zeros(ch, width, dtype=dtype),
+                conv_b=torch.zeros(ch, dtype=dtype) if bias else None, g=torch.zeros(rows, hv), beta=torch.zeros(rows, hv),
+                o=torch.zeros(rows, hv, d, dtype=out), parents=torch.zeros(rows, dtype=I32), cu=torch.zeros(m + 1, dtype=I32),
+                accepted=torch.zeros(m, dtype=I32), sp=torch.zeros(m, dtype=I64), cp=torch.zeros(m, dtype=I64),
+                k=torch.zeros(rows, hk, d), u=torch.zeros(rows, hv, d), gamma=torch.zeros(rows, hv))
+
+
+def tree_dims(dtype, out):
+    kinds = {BF16: gdn.GDN_BF16, F32: gdn.GDN_F32}
+    return gdn.make_dims(2, 4, 32, conv_width=3, in_dtype=kinds[dtype], out_dtype=kinds[out])
+
+
+@pytest.mark.parametrize("dtype,out,bias", [(BF16, F32, True), (F32, BF16, False)])
+def test_tree_verify_operands(dtype, out, bias, launches):
+    t = tree_operands(dtype, out, bias)
+    del t["accepted"]
+    d = tree_dims(dtype, out)
+    refused_one_at_a_time(t, lambda a: gdn.tree_verify(d, a["x"], a["conv_w"], a["conv_b"], a["g"], a["beta"], a["o"],
+                                                       a["parents"], a["cu"], 8, a["sp"], a["cp"],
+                                                       record=(a["k"], a["u"], a["gamma"])), launches)
+
+
+def test_tree_accept_operands(launches):
+    t = tree_operands()
+    for k in ("conv_w", "conv_b", "g", "beta", "o"):
+        del t[k]
+    d = tree_dims(BF16, F32)
+    refused_one_at_a_time(t, lambda a: gdn.tree_accept(d, a["x"], (a["k"], a["u"], a["gamma"]), a["parents"], a["cu"], 8,
+                                                       a["accepted"], a["sp"], a["cp"]), launches)
+
+
+def test_tree_calls_that_are_fine(launches):
+    """x rows apart, no parents, no record, one node, none."""
+    d = tree_dims(BF16, F32)
+    t = tree_operands()
+    g = {k: OnGpu(v) for k, v in t.items()}
+    wide = OnGpu(torch.zeros(5, t["x"].shape[1] + 8, dtype=BF16)[:, :t["x"].shape[1]])
+    gdn.tree_verify(d, wide, g["conv_w"], None, g["g"], g["beta"], g["o"], None, g["cu"], 8, g["sp"], g["cp"])
+    for n in (1, 0):
+        c = {k: OnGpu(t[k][:n]) for k in ("x", "g", "beta", "o", "parents", "k", "u", "gamma")}
+        rec = (c["k"], c["u"], c["gamma"])
+        gdn.tree_verify(d, c["x"], g["conv_w"], g["conv_b"], c["g"], c["beta"], c["o"], c["parents"], g["cu"], 8, g["sp"], g["cp"],
+                        record=rec)
+        gdn.tree_accept(d, c["x"], rec, None, g["cu"], 8, g["accepted"], g["sp"], g["cp"])
+    assert len(launches) == 5
+
+
+def test_the_wrong_operand_is_named():
+    """(state_ptrs gives the number of slots: a short one is told by cu_nodes)"""
+    t = tree_operands()
+    d = tree_dims(BF16, F32)
+
+    def call(**kw):
+        a = dict(t, **kw)
+        gdn.tree_verify(d, a["x"], a["conv_w"], a["conv_b"], a["g"], a["beta"], a["o"], a["parents"], a["cu"], 8, a["sp"],
+                        a["cp"], record=(a["k"], a["u"], a["gamma"]))
+
+    for name, said in dict(t, x="x must", conv_w="conv_w", conv_b="conv_b", g="g must", beta="beta", o="o must",
+                           parents="parents", cu="cu_nodes", sp="state_ptrs|cu_nodes", cp="conv_state_ptrs", k="k of the record",
+                           u="u of the record", gamma="gamma of the record").items():
+        if name == "accepted":
+            continue
+        for what, w in wrong_forms(t[name]):
+            with pytest.raises(ValueError, match=said):
+                call(**{name: w})
+    with pytest.raises(ValueError, match="on the GPU"):
+        call()
