@@ -80,26 +80,31 @@ class SlotPool:
 
     def pack_slots(self, slot_idx: torch.Tensor, packed: torch.Tensor, fmt: int, conv_state: bool = True) -> None:
         """8-bit snapshots: slot slot_idx[i] into row i of packed (from packed_slots())."""
-        assert slot_idx.numel() <= packed.shape[0]
+        if slot_idx.numel() > packed.shape[0]:
+            raise ValueError(f"pack_slots: {slot_idx.numel()} slots for {packed.shape[0]} rows of packed")
+        blocks = self._blocks(packed, slot_idx)
         sp, cp = self.pointers(slot_idx)
-        slot_pack(self.dims, fmt, sp, cp if conv_state else None, self._blocks(packed, slot_idx))
+        slot_pack(self.dims, fmt, sp, cp if conv_state else None, blocks)
 
     def unpack_slots(self, packed: torch.Tensor, block_idx: torch.Tensor, slot_idx: torch.Tensor, fmt: int,
                      conv_state: bool = True) -> None:
         """Slot slot_idx[i] filled from row block_idx[i] of packed (int32 device index tensors, slots
         distinct; one block may fill several slots). An index outside its pool skips the entry."""
-        assert block_idx.numel() == slot_idx.numel()
+        blocks = self._blocks(packed, slot_idx, block_idx)
         sp, cp = self.pointers(slot_idx)
-        slot_unpack(self.dims, fmt, self._blocks(packed, slot_idx, block_idx), sp, cp if conv_state else None)
+        slot_unpack(self.dims, fmt, blocks, sp, cp if conv_state else None)
 
     def _blocks(self, packed: torch.Tensor, slot_idx: torch.Tensor, block_idx=None) -> torch.Tensor:
         """Device addresses of packed's rows block_idx (default: 0, 1, ..), 0 outside it."""
-        n = slot_idx.numel()
-        assert packed.dtype == torch.uint8 and packed.dim() == 2 and packed.is_contiguous()
-        assert packed.shape[1] == _lib.gdn_slot_packed_size(self.dims, _lib.GDN_PACK_INT8)  # (both formats')
+        n, at, size = slot_idx.numel(), self.state.get_device(), \
+            _lib.gdn_slot_packed_size(self.dims, _lib.GDN_PACK_INT8)  # (both formats')
+        _at("packed slots", "packed", packed, torch.uint8, packed.shape[0] * size, at)
+        if packed.dim() != 2:
+            raise ValueError(f"packed slots: packed must be rows of {size} bytes (got shape {tuple(packed.shape)})")
         if block_idx is None:
             block_idx = torch.arange(n, dtype=torch.int32, device=slot_idx.device)
-        assert block_idx.dtype == torch.int32 and block_idx.is_cuda
+        _at("packed slots", "the slots' indices", slot_idx, _I32, n, at)
+        _at("packed slots", "the blocks' indices", block_idx, _I32, n, at)
         out = torch.empty(n, dtype=torch.int64, device=slot_idx.device)
         _lib.gdn_slot_pointers(packed.data_ptr(), packed.shape[1], packed.shape[0], block_idx, n, out)
         return out
@@ -230,14 +235,23 @@ def tree_accept(dims: gdn_dims, x: torch.Tensor, record, parents, cu_nodes: torc
         _at(fn, "state_ptrs", state_ptrs, _I64, m, at), _at(fn, "conv_state_ptrs", conv_state_ptrs, _I64, m, at))
 
 
+def _block_operands(fn: str, state_ptrs: torch.Tensor, conv_state_ptrs, packed_ptrs: torch.Tensor):
+    n, at = state_ptrs.numel(), state_ptrs.get_device()
+    _at(fn, "state_ptrs", state_ptrs, _I64, n, at)
+    return (None if conv_state_ptrs is None else _at(fn, "conv_state_ptrs", conv_state_ptrs, _I64, n, at),
+            _at(fn, "packed_ptrs", packed_ptrs, _I64, n, at), n)
+
+
 def slot_pack(dims: gdn_dims, fmt: int, state_ptrs: torch.Tensor, conv_state_ptrs, packed_ptrs: torch.Tensor,
               stream=None) -> None:
-    _lib.gdn_slot_pack(dims, fmt, state_ptrs, conv_state_ptrs, packed_ptrs, state_ptrs.numel(), stream)
+    cp, bp, n = _block_operands("slot_pack", state_ptrs, conv_state_ptrs, packed_ptrs)
+    _lib.gdn_slot_pack(dims, fmt, state_ptrs, cp, bp, n, stream)
 
 
 def slot_unpack(dims: gdn_dims, fmt: int, packed_ptrs: torch.Tensor, state_ptrs: torch.Tensor, conv_state_ptrs,
                 stream=None) -> None:
-    _lib.gdn_slot_unpack(dims, fmt, packed_ptrs, state_ptrs, conv_state_ptrs, state_ptrs.numel(), stream)
+    cp, bp, n = _block_operands("slot_unpack", state_ptrs, conv_state_ptrs, packed_ptrs)
+    _lib.gdn_slot_unpack(dims, fmt, bp, state_ptrs, cp, n, stream)
 
 
 def group_norm(dims, x: torch.Tensor, weight, y: torch.Tensor, gate=None, bias=None, stream=None) -> None:

@@ -49,6 +49,7 @@ def wrong_forms(t, rows_may_be_apart=False):
 def refused_one_at_a_time(operands, call, launches):
     """call(operands) launches once; with any one operand in a wrong form, or on the host, or on another GPU, not."""
     gpu = {k: None if t is None else OnGpu(t) for k, t in operands.items()}
+    launches.clear()
     call(gpu)
     assert len(launches) == 1
     for name, t in operands.items():
@@ -131,3 +132,46 @@ def test_the_wrong_operand_is_named():
                 call(**{name: w})
     with pytest.raises(ValueError, match="on the GPU"):
         call()
+
+
+@pytest.mark.parametrize("fn", [gdn.slot_pack, gdn.slot_unpack])
+def test_snapshot_operands(fn, launches):
+    """Pointer arrays of another type or length, with gaps or on another device."""
+    d = gdn.make_dims(1, 2, 32)
+    order = ("state", "conv", "packed") if fn is gdn.slot_pack else ("packed", "state", "conv")
+
+    def call(a):
+        fn(d, gdn.GDN_PACK_INT8, *(a[k] for k in order))
+
+    # (the state pointers give the number of slots)
+    t = {k: torch.zeros(3, dtype=I64) for k in ("state", "conv", "packed")}
+    refused_one_at_a_time(t, call, launches)
+    refused_one_at_a_time(dict(t, conv=None), call, launches)
+
+
+def test_snapshot_store_operands(launches, monkeypatch):
+    """pack_slots and unpack_slots: a store of another size, type or layout, on the host or on another GPU; more slots
+    than rows; indices of another type, length or device."""
+    made = []
+    monkeypatch.setattr(_lib, "gdn_slot_pointers", lambda *a: made.append(a))
+    d = gdn.make_dims(1, 2, 32)
+    size = gdn.gdn_slot_packed_size(d, gdn.GDN_PACK_INT8)
+    pool = gdn.SlotPool(d, 4, device="cpu")
+    pool.state, pool.conv_state = OnGpu(pool.state), OnGpu(pool.conv_state)
+    monkeypatch.setattr(gdn.SlotPool, "pointers", lambda self, idx: (OnGpu(torch.zeros(idx.numel(), dtype=I64)),) * 2)
+    good = OnGpu(torch.zeros(2, size, dtype=torch.uint8))
+    idx = OnGpu(torch.zeros(2, dtype=I32))
+    bad = [good._t, OnGpu(good._t, 1), OnGpu(good._t[:, :-16].contiguous()), OnGpu(good._t[:, ::2]), OnGpu(good._t.to(I32)),
+           OnGpu(torch.zeros(2 * size, dtype=torch.uint8)), OnGpu(torch.zeros(2, size + 16, dtype=torch.uint8)[:, :size])]
+    for store in bad:
+        with pytest.raises(ValueError):
+            pool.pack_slots(idx, store, gdn.GDN_PACK_INT8)
+        with pytest.raises(ValueError):
+            pool.unpack_slots(store, idx, idx, gdn.GDN_PACK_INT8)
+    with pytest.raises(ValueError):
+        pool.pack_slots(OnGpu(torch.zeros(3, dtype=I32)), good, gdn.GDN_PACK_INT8)
+    for other in (OnGpu(torch.zeros(2, dtype=I64)), torch.zeros(2, dtype=I32), OnGpu(idx._t, 1), OnGpu(torch.zeros(3, dtype=I32)),
+                  OnGpu(torch.zeros(4, dtype=I32)[::2])):
+        with pytest.raises(ValueError):
+            pool.unpack_slots(good, other, idx, gdn.GDN_PACK_INT8)
+    assert not made and not launches
