@@ -182,8 +182,10 @@ _DTYPES = {GDN_F32: torch.float32, GDN_BF16: torch.bfloat16}
 
 
 def _at(fn: str, name: str, t: torch.Tensor, dtype, n: int, device: int) -> int:
-    """The address of t, which must be n contiguous values of dtype on the device: the kernels see no more of it."""
-    if t.dtype is dtype and t.numel() == n and t.is_contiguous() and t.get_device() == device:
+    """The address of t, which must be n contiguous values of dtype (addresses: of int64 or uint64) on the device:
+    the kernels see no more of it."""
+    if (t.dtype is dtype or (dtype is _I64 and t.dtype is torch.uint64)) and t.numel() == n and t.is_contiguous() \
+            and t.get_device() == device:
         return t.data_ptr()
     raise ValueError(f"{fn}: {name} must be {n} contiguous values of {dtype} on the device of the first operand (got "
                      f"{t.numel()} of {t.dtype}, shape {tuple(t.shape)}, strides {t.stride()}, device {t.device})")

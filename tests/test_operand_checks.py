@@ -175,3 +175,10 @@ def test_snapshot_store_operands(launches, monkeypatch):
         with pytest.raises(ValueError):
             pool.unpack_slots(good, other, idx, gdn.GDN_PACK_INT8)
     assert not made and not launches
+
+
+def test_addresses_may_be_unsigned(launches):
+    d = gdn.make_dims(1, 2, 32)
+    p = OnGpu(torch.zeros(3, dtype=torch.uint64))
+    gdn.slot_pack(d, gdn.GDN_PACK_INT8, p, OnGpu(torch.zeros(3, dtype=I64)), p)
+    assert len(launches) == 1
