@@ -258,18 +258,32 @@ def slot_unpack(dims: gdn_dims, fmt: int, packed_ptrs: torch.Tensor, state_ptrs:
 
 def group_norm(dims, x: torch.Tensor, weight, y: torch.Tensor, gate=None, bias=None, stream=None) -> None:
     """y = the norm of every group of every row of x, times weight, plus bias, gated (dims from
-    make_norm_dims()). Rows are the first axis; the other axes of x, gate and y are contiguous."""
-    rows = x.shape[0]
-    n = rows * dims.groups * dims.group_size
-    _lib.gdn_group_norm(dims, x, _row_stride(x, rows, n), gate, 0 if gate is None else _row_stride(gate, rows, n),
-                        weight, bias, y, _row_stride(y, rows, n), rows, stream)
+    make_norm_dims(), the types of x, gate, weight, bias and y among them). Rows are the first axis; the other
+    axes of x, gate and y are contiguous. weight and bias: [group_size], or with their own for every group
+    [groups * group_size]."""
+    rows, size, at = x.shape[0], dims.group_size, x.get_device()
+    n = rows * dims.groups * size
+    per, param = size if dims.shared_params else dims.groups * size, _DTYPES.get(dims.param_dtype)
+    _lib._launch(
+        "gdn_group_norm", _lib._LIB.gdn_group_norm, stream, x, ctypes.byref(dims), x.data_ptr(),
+        _row_stride("x", x, _DTYPES.get(dims.in_dtype), rows, n, at), None if gate is None else gate.data_ptr(),
+        0 if gate is None else _row_stride("gate", gate, _DTYPES.get(dims.gate_dtype), rows, n, at),
+        None if weight is None else _at("group_norm", "weight", weight, param, per, at),
+        None if bias is None else _at("group_norm", "bias", bias, param, per, at), y.data_ptr(),
+        _row_stride("y", y, _DTYPES.get(dims.out_dtype), rows, n, at), rows)
 
 
-def _row_stride(t: torch.Tensor, rows: int, n: int) -> int:
-    """Row stride of t, which holds n values in `rows` contiguous rows, [rows, width] or [rows, a, b]."""
+def _row_stride(name: str, t: torch.Tensor, dtype, rows: int, n: int, device: int) -> int:
+    """Row stride of t, which holds n values in `rows` contiguous rows, [rows, width] or [rows, a, b] (an axis of
+    length 1 has no stride to speak of)."""
     s, shape = t.stride(), t.shape
-    assert s[-1] == 1 and shape[0] == rows and t.numel() == n and (len(s) == 2 or (len(s) == 3 and s[1] == shape[2]))
-    return s[0]
+    if t.dtype is dtype and t.get_device() == device and t.numel() == n and shape[0] == rows and (
+            len(s) == 2 and (s[1] == 1 or shape[1] == 1)
+            or len(s) == 3 and (s[2] == 1 or shape[2] == 1) and (s[1] == shape[2] or shape[1] == 1) or n == 0):
+        return s[0]
+    raise ValueError(f"group_norm: {name} must be {rows} rows of {n // rows if rows else 0} adjacent values of {dtype}, [rows, "
+                     f"width] or [rows, a, b], on the device of x (got {t.dtype}, shape {tuple(shape)}, strides {s}, "
+                     f"device {t.device})")
 
 
 def prefill_workspace(dims: gdn_dims, num_seqs: int, total_tokens: int, device="cuda") -> torch.Tensor:

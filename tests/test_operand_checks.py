@@ -182,3 +182,45 @@ def test_addresses_may_be_unsigned(launches):
     p = OnGpu(torch.zeros(3, dtype=torch.uint64))
     gdn.slot_pack(d, gdn.GDN_PACK_INT8, p, OnGpu(torch.zeros(3, dtype=I64)), p)
     assert len(launches) == 1
+
+
+@pytest.mark.parametrize("shared", [True, False])
+@pytest.mark.parametrize("x,gate,param,y", [(F32, BF16, BF16, BF16), (BF16, F32, F32, F32)])
+def test_group_norm_operands(x, gate, param, y, shared, launches):
+    kinds = {BF16: gdn.GDN_BF16, F32: gdn.GDN_F32}
+    d = gdn.make_norm_dims(3, 8, in_dtype=kinds[x], gate_dtype=kinds[gate], param_dtype=kinds[param], out_dtype=kinds[y],
+                           shared_params=shared)
+    per = 8 if shared else 24
+    t = dict(x=torch.zeros(5, 24, dtype=x), gate=torch.zeros(5, 24, dtype=gate), weight=torch.zeros(per, dtype=param),
+             bias=torch.zeros(per, dtype=param), y=torch.zeros(5, 24, dtype=y))
+    refused_one_at_a_time(t, lambda a: gdn.group_norm(d, a["x"], a["weight"], a["y"], gate=a["gate"], bias=a["bias"]), launches)
+
+
+def test_a_bf16_o_needs_dims_that_say_so(launches):
+    """make_norm_dims() expects fp32 x by default: a bf16 o of the layer is not read as fp32."""
+    o, y = OnGpu(torch.zeros(5, 4, 32, dtype=BF16)), OnGpu(torch.zeros(5, 128, dtype=BF16))
+    with pytest.raises(ValueError, match="x must be"):
+        gdn.group_norm(gdn.make_norm_dims(4, 32), o, None, y)
+    gdn.group_norm(gdn.make_norm_dims(4, 32, in_dtype=gdn.GDN_BF16), o, None, y)
+    assert len(launches) == 1
+
+
+def test_group_norm_layouts(launches):
+    """Rows apart, three axes, axes of length 1 whatever stride they carry, no rows."""
+    d = gdn.make_norm_dims(4, 32, gate_dtype=gdn.GDN_F32, out_dtype=gdn.GDN_F32)
+    one = gdn.make_norm_dims(1, 32, out_dtype=gdn.GDN_F32)
+    ones = gdn.make_norm_dims(4, 1, out_dtype=gdn.GDN_F32, shared_params=False)
+    wide = torch.zeros(5, 160)
+    fine = [(d, wide[:, :128], wide[:, 32:]), (d, torch.zeros(5, 4, 32), wide[:, :128].view(5, 4, 32)),
+            (d, torch.zeros(0, 128), torch.zeros(0, 4, 32)), (d, wide[1:2, 3:131], torch.zeros(1, 4, 32)),
+            (one, torch.zeros(5, 4, 32)[:, 2:3], torch.zeros(5, 32)), (one, torch.zeros(5, 32, 4).transpose(1, 2)[:, :1].contiguous(),
+                                                                       torch.zeros(5, 1, 32)),
+            (ones, torch.zeros(5, 4).as_strided((5, 4, 1), (4, 1, 7)), torch.zeros(5, 4))]
+    for dims, x, y in fine:
+        gdn.group_norm(dims, OnGpu(x), None, OnGpu(y))
+    assert len(launches) == len(fine)
+    for bad in (torch.zeros(5, 256)[:, ::2], torch.zeros(5, 8, 32)[:, ::2], torch.zeros(128, 5).t(), torch.zeros(640),
+                torch.zeros(5, 2, 2, 32), torch.zeros(4, 160), torch.zeros(5, 4, 64)[..., :32]):
+        with pytest.raises(ValueError):
+            gdn.group_norm(d, OnGpu(bad), None, OnGpu(torch.zeros(5, 128)))
+    assert len(launches) == len(fine)
