@@ -239,21 +239,21 @@ def tree_accept(dims: gdn_dims, x: torch.Tensor, record, parents, cu_nodes: torc
 
 def _block_operands(fn: str, state_ptrs: torch.Tensor, conv_state_ptrs, packed_ptrs: torch.Tensor):
     n, at = state_ptrs.numel(), state_ptrs.get_device()
-    _at(fn, "state_ptrs", state_ptrs, _I64, n, at)
-    return (None if conv_state_ptrs is None else _at(fn, "conv_state_ptrs", conv_state_ptrs, _I64, n, at),
+    return (_at(fn, "state_ptrs", state_ptrs, _I64, n, at),
+            None if conv_state_ptrs is None else _at(fn, "conv_state_ptrs", conv_state_ptrs, _I64, n, at),
             _at(fn, "packed_ptrs", packed_ptrs, _I64, n, at), n)
 
 
 def slot_pack(dims: gdn_dims, fmt: int, state_ptrs: torch.Tensor, conv_state_ptrs, packed_ptrs: torch.Tensor,
               stream=None) -> None:
-    cp, bp, n = _block_operands("slot_pack", state_ptrs, conv_state_ptrs, packed_ptrs)
-    _lib.gdn_slot_pack(dims, fmt, state_ptrs, cp, bp, n, stream)
+    sp, cp, bp, n = _block_operands("slot_pack", state_ptrs, conv_state_ptrs, packed_ptrs)
+    _lib._launch("gdn_slot_pack", _lib._LIB.gdn_slot_pack, stream, state_ptrs, ctypes.byref(dims), fmt, sp, cp, bp, n)
 
 
 def slot_unpack(dims: gdn_dims, fmt: int, packed_ptrs: torch.Tensor, state_ptrs: torch.Tensor, conv_state_ptrs,
                 stream=None) -> None:
-    cp, bp, n = _block_operands("slot_unpack", state_ptrs, conv_state_ptrs, packed_ptrs)
-    _lib.gdn_slot_unpack(dims, fmt, bp, state_ptrs, cp, n, stream)
+    sp, cp, bp, n = _block_operands("slot_unpack", state_ptrs, conv_state_ptrs, packed_ptrs)
+    _lib._launch("gdn_slot_unpack", _lib._LIB.gdn_slot_unpack, stream, state_ptrs, ctypes.byref(dims), fmt, bp, sp, cp, n)
 
 
 def group_norm(dims, x: torch.Tensor, weight, y: torch.Tensor, gate=None, bias=None, stream=None) -> None:
