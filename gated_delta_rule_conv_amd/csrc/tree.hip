@@ -89,7 +89,7 @@ __device__ __forceinline__ int xcd_head() {
 // (exact) that puts its norm (or largest value) at 2^12 .. 2^13, and the result by its inverse. A value far
 // below its row's norm is so held to 2^-37 of the norm, not to 2^-22 of itself: what a sum loses is small beside
 // the rows' norms, but not always beside the sum, which is why fp32 inputs do not take this form by default.
-// 64 slots x 64 nodes of bf16 x take 123 us with pairs and 169 us in fp32, x 16 nodes 44 and 48 us.
+// 64 slots x 64 nodes of bf16 x take 121 us with pairs and 162 us in fp32, x 16 nodes 44 and 48 us.
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 typedef _Float16 f16x4 __attribute__((ext_vector_type(4)));
 
@@ -307,20 +307,21 @@ __device__ __forceinline__ constexpr int place(int k) {
   return (k / 32) * 32 + ((k % 16) / 4) * 8 + ((k % 32) / 16) * 4 + k % 4;
 }
 
-// Heads of a workgroup (HP); how many of them side by side on waves of their own (PAR) and how many
-// together on the same waves (JOIN), the rest one after the other. Together, a fragment of K or Q read from
-// LDS serves both heads and both states are in flight from the start, at 64 more registers: 64 slots x 64
-// nodes take 129 us against 131 us one after the other, but 64 slots x 16 nodes 49 us against 44 us (their
-// 128-register budget, which keeps two workgroups on a CU, spills). Side by side is for the smaller head
-// dims' larger trees, whose four or two waves a head would convolve the tokens alone.
+// Heads of a workgroup (HP) and how many of them side by side on waves of their own (PAR), the rest one after
+// the other. Side by side is for the smaller head dims' larger trees, whose four or two waves a head would convolve
+// the tokens alone: 64 slots x 64 nodes take 65 us against 107 (d = 32), 66 against 97 (d = 64, bf16 x) and 81 against
+// 107 (fp32 x), one slot 15 to 17 against 18 to 21.
+// JOIN, the heads that a wave takes together, is 1. Two spare LDS reads at 64 more registers, and lose everywhere:
+// 64 slots x 64 nodes of d = 128 take 121 us one after the other and 124 together (fp32 products 161 and 169), one
+// slot 21.5 and 22.9. The loops over it stay all the same: without them the compiler lays the blocks out so that
+// the larger trees spill (129 us, fp32 products 247).
 constexpr int kVerifyHeads = 2;
 constexpr int verify_par(int nb, int d) { return nb > 2 && d < 128 ? 2 : 1; }
-constexpr int verify_join(int nb, int d) { return nb > 2 && d == 128 ? 2 : 1; }
 
 template <typename MMA, typename T, int K, int D, int NB, int SILU>  // (SILU -1: as the arguments say)
 __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ? 4 : 2)) void tree_verify_kernel(
     TreeArgs a, int32_t heads, int32_t chunks) {
-  constexpr int HP = kVerifyHeads, PAR = verify_par(NB, D), SEQ = HP / PAR, JOIN = verify_join(NB, D);
+  constexpr int HP = kVerifyHeads, PAR = verify_par(NB, D), SEQ = HP / PAR, JOIN = 1;
   using Lds = VerifyLds<MMA, T, K, D, NB, HP>;
   const bool silu_on = SILU < 0 ? a.silu != 0 : SILU != 0;
   constexpr int WH = D / 16;         // waves of a head
@@ -412,12 +413,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
   };
 #pragma unroll
   for (int t = 0; t < JOIN; ++t) {
-    if (t * PAR + hw < nh) {
-      load_state(s[t], t * PAR + hw);
-    } else {
-#pragma unroll
-      for (int e = 0; e < D / 16; ++e) s[t][e] = f32x4{0.f, 0.f, 0.f, 0.f};  // (an odd group's last head alone)
-    }
+    if (t * PAR + hw < nh) load_state(s[t], t * PAR + hw);
   }
   __builtin_amdgcn_sched_barrier(0);  // every load above is issued before the first wait
   if (tid < 2) {
@@ -706,9 +702,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
           }
         if (MMA::kFull && NB <= 2 && e % 2) __builtin_amdgcn_sched_barrier(0);
       }
-      if constexpr (JOIN == 1) {
-        if (head(1) < nh) load_state(s[0], head(1));
-      }
+      if (head(1) < nh) load_state(s[0], head(1));
     }
     if (sq == 0) barrier_lds();  // A, P and the inverses of every head
     if (head(0) >= nh) break;
@@ -806,7 +800,9 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
 
 template <typename T, int K, int D, int NB>
 hipError_t verify_nb(const TreeArgs& a, int32_t m, hipStream_t s) {
-  // both heads of a pair on one workgroup once that leaves a workgroup for every CU
+  // Both heads of a pair on one workgroup once that leaves a workgroup for every CU. 16/32 heads of d = 128, trees of
+  // 16 / 32 / 64 nodes, one head against two: 8 slots 10 / 14 / 26 us against 12 / 18 / 33, 16 slots (256 workgroups
+  // of two) 15 / 22 / 48 against 13 / 20 / 36, 64 slots 48 / 64 / 169 against 42 / 57 / 124.
   const int32_t pairs = (a.r.group + kVerifyHeads - 1) / kVerifyHeads;
   const int32_t heads = static_cast<int64_t>(m) * a.r.hk * pairs >= 256 ? kVerifyHeads : 1;
   const int32_t chunks = heads == 1 ? a.r.group : pairs;  // workgroups of a k-head
