@@ -5,7 +5,8 @@
 // Bound by HBM, with the vector units close behind: x, gate and y move once (8 bytes a value for fp32 x and
 // bf16 gate and y: 515 MB of a 15717-token, 32-head, d = 128 layer in 95 us, 5.4 TB/s), and a value takes
 // about 12 VALU operations besides the exponential and the reciprocal of SiLU, which cost four times one;
-// so the divisions by the group count and size are products with numbers the host prepared. A group lives in the registers of LPG adjacent lanes, each
+// so the divisions by the group count and size are products with numbers the host prepared (the mean is then good to
+// an ulp), and the root is the hardware's reciprocal square root (an ulp as well). A group lives in the registers of LPG adjacent lanes, each
 // holding V vectors of 4 consecutive values (lane c: values 4 (c + LPG t), t < V), so the mean
 // and the sum of squares are one pass over memory and two over registers, in fp32; sums over lanes
 // are fixed butterflies. Rows and groups may start at any multiple of the element: gfx950's vector

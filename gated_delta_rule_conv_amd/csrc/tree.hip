@@ -233,8 +233,8 @@ __device__ __forceinline__ void barrier_lds() {
 //   M = K S^T, W = Q S^T               [N][16]
 //   A_ij = -beta_i e^(G_i - G_j) k_i.k_j for j above i, else 0;   P_ij = e^(G_i - G_j) q_i.k_j, j above or at i
 //   U = (I - A)^-1 (beta (V - e^G M)), O = e^G W + P U
-// (I - A) is unit lower triangular (parents come first): its 16x16 diagonal blocks are inverted by
-// substitution, the rest is block substitution. The products with d terms (M, W, A, P) run in the call's
+// (I - A) is unit lower triangular (parents come first): its 16x16 diagonal blocks are inverted by five
+// products (unit_lower_inverse), the rest is block substitution. The products with d terms (M, W, A, P) run in the call's
 // policy (MMA), the others on fp32 MFMA with the contraction index dealt as 4 (l / 16) + r, so that a result
 // tile (lane l: rows 4 (l / 16) + r of column l % 16) is the right operand of the next product as it stands.
 //
@@ -244,14 +244,16 @@ __device__ __forceinline__ void barrier_lds() {
 // rows stay in flight across them.
 //
 // What bounds it. At 16/32 heads, d = 128, bf16, 64 slots read 134 MB of states: 16-node trees take 42 us (182 MB
-// in all, 4.3 TB/s), 64-node trees 129 us (290 MB and 8.6 GFLOP, of which the products with d terms are issued
-// three times). HBM is busy at its streaming rate while the workgroups of a round load, and mostly idle while
-// they compute: the two workgroups that a CU holds (one, for the largest trees, whose K and Q fill half of the
-// LDS) start together and stay in step. Neither the vector units (34% of the time) nor MFMA (14%; 22% for
-// the largest trees) is the limit there, LDS fragment reads and the substitution's dependent products are.
+// in all, 4.3 TB/s), 64-node trees 121 to 126 us (290 MB and 8.6 GFLOP, of which the products with d terms are
+// issued three times). HBM is busy at its streaming rate while the workgroups of a round load, and mostly idle
+// while they compute: the two workgroups that a CU holds (one, for the largest trees: of its 157 KB of LDS
+// the two heads' A, P and inverses take 80, K and Q 74) start together and stay in step. Neither the
+// vector units (36% of the time) nor MFMA (14%; 23% for the largest trees) is the limit there, LDS
+// fragment reads and the substitution's dependent products are.
 // A workgroup that took several items in turn and loaded the next one's state and x during the
-// substitution needed 130 to 300 bytes of spilled registers a lane. One slot with 4 nodes takes 8.3 us, a chain
+// substitution needed 130 to 300 bytes of spilled registers a lane. One slot with 4 nodes takes 8.4 us, a chain
 // of about 17k cycles: two dependent memory round trips, the conv, A's diagonal blocks, M and W, the substitution.
+// Part of it is work that a single head does not need: v's conv runs for two heads, whether or not there is a second.
 //
 // A zero of A or P times an infinity or a NaN would carry a broken token into branches that do not
 // see it. So such values never enter the products: a k that is not finite marks its node, a row of A that is
@@ -259,6 +261,7 @@ __device__ __forceinline__ void barrier_lds() {
 // state row, zeros go in their place, and the results of the marked nodes and their descendants are set to
 // NaN at the end. An inverse that is not finite (a path of unnormalised keys that diverges) is formed
 // again without products by zeros; its rows are then not finite on that path alone, and so u's.
+
 // q and k in LDS: fp32 rows, or hi and lo rows of halves (inside a row see place()).
 template <typename MMA, int N, int D>
 struct QkRows {

@@ -9,7 +9,8 @@ the slot index on the launch grid and hands the kernels one address per slot.)
 
 ``conv_update``, ``prefill``, ``decode``, ``decode_fused``, ``tree_verify``, ``tree_accept``,
 ``slot_pack``, ``slot_unpack`` and ``group_norm`` derive pointers, strides and views from torch
-tensors and call the library; all arithmetic happens in the HIP kernels.
+tensors and call the library; all arithmetic happens in the HIP kernels. The last five check the type,
+size, layout and device of every operand first (ValueError): the kernels see addresses alone.
 """
 
 from __future__ import annotations

@@ -10,9 +10,10 @@ from tests.test_gpu_tree import accept, check_o, device, make_case, make_dims, o
 
 pytestmark = pytest.mark.gpu
 
-# one shape a form of the kernel: 16, 32 and 64 nodes, heads after each other, side by side and joined
+# one shape a form of the kernel: 16, 32 and 64 nodes, heads after each other and side by side, fp32 products (fp32
+# input) and pairs of halves (bf16 input)
 FORMS = [(1, 2, 32, "f32", 16), (2, 4, 32, "bf16", 31), (1, 3, 64, "f32", 64), (1, 2, 128, "bf16", 16), (1, 2, 128, "f32", 30),
-         (2, 4, 128, "bf16", 64)]
+         (2, 4, 128, "bf16", 64), (1, 2, 64, "bf16", 50), (2, 2, 32, "bf16", 64), (1, 3, 128, "f32", 64)]
 
 
 def descendants(c, tree, node):
