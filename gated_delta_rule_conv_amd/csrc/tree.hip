@@ -63,15 +63,19 @@ __device__ __forceinline__ int parent_of(const int32_t* parents, int first, int 
 // The record's G holds one fp32 number, whose steps grow with it. So where a parent's is below -128 and the
 // node's own g above that, the sum starts again from the node: G = g. Such a parent is at the end of a
 // path whose sum of g is below -128, and no other node's G behind it rises above its parent's, which is how the
-// reader knows. Lane t: sum = the path's sum (used while above -128), g and parent of node t.
-__device__ __forceinline__ float restarted_sum(float sum, float g, int par, int n) {
-  float rec = sum;
+// reader knows. Lane t: sum = the path's sum (used while above -128), g and parent of node t. In two halves here
+// as well, so that an entry is rounded once and not once a node of its path.
+__device__ __forceinline__ float restarted_sum(Gamma sum, float g, int par, int n) {
+  Gamma rec = sum;
   for (int s = 0; s < n; ++s) {  // (after s rounds right down to depth s)
-    const float above = __shfl(rec, par >= 0 ? par : 0);
-    const bool past = par >= 0 && above < kForget;
-    if (past || sum <= kForget) rec = par < 0 || (past && g > above) ? g : above + g;
+    const Gamma above = {__shfl(rec.hi, par >= 0 ? par : 0), __shfl(rec.lo, par >= 0 ? par : 0)};
+    const bool past = par >= 0 && above.hi < kForget;
+    if (past || sum.hi <= kForget) {
+      rec = par < 0 || (past && g > above.hi) ? Gamma{g, 0.f} : above + Gamma{g, 0.f};
+      if (!(fabsf(rec.lo) < __builtin_inff())) rec.lo = 0.f, rec.hi = above.hi + g;  // (a sum beyond fp32's range)
+    }
   }
-  return rec;
+  return rec.hi;
 }
 
 // Renumbers grid.x so that consecutive k-heads, which read and write neighbouring bytes, share an
@@ -454,7 +458,7 @@ __global__ __launch_bounds__(D * 4 * verify_par(NB, D), (D < 128 ? 1 : NB <= 2 ?
       }
     }
     float rec = gam.hi;
-    if (a.gamma_rec && __any(gam.hi <= kForget)) rec = restarted_sum(gam.hi, gval, par, n);
+    if (a.gamma_rec && __any(gam.hi <= kForget)) rec = restarted_sum(gam, gval, par, n);
     if (lane < N) {
       if (w == 0) {
         lds.anc[lane][0] = lo;

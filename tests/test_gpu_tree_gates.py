@@ -86,3 +86,15 @@ def test_the_record_of_ordinary_gates_is_the_path_sum():
     want = np.concatenate([np.cumsum(g[:64], 0), np.cumsum(g[64:], 0)])
     got = e["rec"][2].cpu().numpy().astype(np.float64)
     assert (np.abs(got - want) <= 2.0 ** -24 * 1.001 * np.abs(want)).all()
+
+
+@pytest.mark.parametrize("first", [-1e9, -150.0])
+def test_many_equal_steps_after_a_restart(first):
+    """A sum that starts again, falls to -100 at once and then by 0.01 sixty times: each entry is rounded once, not
+    once a node on its path."""
+    announce(f"tree: g = {first}, -100, then -0.01 sixty times")
+    sh = LayerShape(1, 2, 32, in_dtype="f32")
+    c = make_case(sh, [64, 9], "chain", seed=14)
+    c["g"][:] = -0.01
+    c["g"][1], c["g"][2] = first, -100.0
+    run(c)
