@@ -316,9 +316,9 @@ def gdn_hbm_probe(buf, nbytes: int, salt: int = 0, stream=None) -> None:
 
 def gdn_slot_pointers(pool_base: int, slot_bytes: int, pool_slots: int, slot_idx, m: int, out_ptrs,
                       stream=None) -> None:
-    st = _LIB.gdn_slot_pointers(ctypes.c_uint64(pool_base), slot_bytes, pool_slots, _ptr(slot_idx), m,
-                                _ptr(out_ptrs), _stream(stream, slot_idx, out_ptrs))
-    _check("gdn_slot_pointers", st)
+    _launch("gdn_slot_pointers", _LIB.gdn_slot_pointers, stream,
+            out_ptrs if slot_idx is None or isinstance(slot_idx, int) else slot_idx, ctypes.c_uint64(pool_base), slot_bytes,
+            pool_slots, _ptr(slot_idx), m, _ptr(out_ptrs))
 
 
 def gdn_tree_verify(dims: gdn_dims, x, x_stride: int, conv_w, conv_b, g, beta, o, parents, cu_nodes, m: int,

@@ -19,6 +19,9 @@ class OnGpu:
     def __getattr__(self, name):
         return getattr(self._t, name)
 
+    def __getitem__(self, i):
+        return OnGpu(self._t[i], self._index)
+
     def get_device(self):
         return self._index
 
@@ -224,3 +227,39 @@ def test_group_norm_layouts(launches):
         with pytest.raises(ValueError):
             gdn.group_norm(d, OnGpu(bad), None, OnGpu(torch.zeros(5, 128)))
     assert len(launches) == len(fine)
+
+
+def test_a_pool_on_another_gpu_than_the_current_one(monkeypatch):
+    """pack_slots and unpack_slots: the pointer arrays are built on the pool's device, as the blocks are moved."""
+    current, where = [0], []
+
+    class Guard:
+        def __init__(self, device):
+            self.device = device
+
+        def __enter__(self):
+            self.before, current[0] = current[0], self.device
+
+        def __exit__(self, *a):
+            current[0] = self.before
+
+    class Lib:
+        def __getattr__(self, name):
+            return lambda *a: where.append((name, current[0], a[-1])) or 0
+
+    size = gdn.gdn_slot_packed_size(gdn.make_dims(1, 2, 32), gdn.GDN_PACK_INT8)
+    monkeypatch.setattr(_lib, "_LIB", Lib())
+    monkeypatch.setattr(_lib, "gdn_slot_packed_size", lambda *a: size)
+    monkeypatch.setattr(_lib, "_current_device", lambda: current[0])
+    monkeypatch.setattr(_lib, "_device_guard", Guard)
+    monkeypatch.setattr(_lib, "_raw_stream", lambda device: 1000 + device)
+    empty, arange = torch.empty, torch.arange
+    monkeypatch.setattr(torch, "empty", lambda *a, device=None, **k: OnGpu(empty(*a, **k), device.index))
+    monkeypatch.setattr(torch, "arange", lambda *a, device=None, **k: OnGpu(arange(*a, **k), device.index))
+    pool = gdn.SlotPool(gdn.make_dims(1, 2, 32), 4, device="cpu")
+    pool.state, pool.conv_state = OnGpu(pool.state, 1), OnGpu(pool.conv_state, 1)
+    idx, store = OnGpu(torch.zeros(2, dtype=I32), 1), OnGpu(torch.zeros(2, size, dtype=torch.uint8), 1)
+    pool.pack_slots(idx, store, gdn.GDN_PACK_INT8)
+    pool.unpack_slots(store, idx, idx, gdn.GDN_PACK_INT8)
+    assert [w[0] for w in where] == (["gdn_slot_pointers"] * 3 + ["gdn_slot_pack"]) + (["gdn_slot_pointers"] * 3 + ["gdn_slot_unpack"])
+    assert all(w[1:] == (1, 1001) for w in where) and current == [0]
