@@ -19,17 +19,20 @@ GDN_OK, GDN_ERR_NULL, GDN_ERR_SHAPE, GDN_ERR_DTYPE, GDN_ERR_ALIGN, GDN_ERR_WORKS
 STATUS_NAMES = {0: "GDN_OK", 1: "GDN_ERR_NULL", 2: "GDN_ERR_SHAPE", 3: "GDN_ERR_DTYPE", 4: "GDN_ERR_ALIGN",
                 5: "GDN_ERR_WORKSPACE", 6: "GDN_ERR_UNSUPPORTED", 7: "GDN_ERR_HIP"}
 GDN_F32, GDN_BF16 = 0, 1
-GDN_ACT_NONE, GDN_ACT_SILU = 0, 1
+GDN_ACT_NONE, GDN_ACT_SILU, GDN_ACT_SIGMOID = 0, 1, 2
 GDN_MMA_AUTO, GDN_MMA_FP32, GDN_MMA_BF16X3 = 0, 1, 2
 GDN_PREFILL_AUTO, GDN_PREFILL_WHOLE, GDN_PREFILL_SEGMENTS = 0, 1, 2
 GDN_PACK_INT8, GDN_PACK_E4M3 = 0, 1
 GDN_TREE_MAX_NODES = 64
+GDN_BLOCK_NORM_MAX_WIDTH = 32768
 
 EXPORTED = ("gdn_dims_init", "gdn_conv_update", "gdn_prefill_workspace_size", "gdn_prefill_chunked",
             "gdn_prefill_fused_workspace_size", "gdn_prefill_fused", "gdn_prefill_fused_static", "gdn_decode_batched",
             "gdn_decode_fused",
             "gdn_slot_copy", "gdn_slot_pointers", "gdn_tree_verify", "gdn_tree_accept", "gdn_slot_packed_size",
-            "gdn_slot_pack", "gdn_slot_unpack", "gdn_group_norm", "gdn_last_error", "gdn_abi_version", "gdn_hbm_probe")
+            "gdn_slot_pack", "gdn_slot_unpack", "gdn_group_norm", "gdn_linear_workspace_size", "gdn_linear_prefill",
+            "gdn_linear_decode", "gdn_block_norm", "gdn_sample_workspace_size", "gdn_sample", "gdn_tree_follow",
+            "gdn_last_error", "gdn_abi_version", "gdn_hbm_probe")
 
 
 class gdn_dims(ctypes.Structure):
@@ -60,6 +63,14 @@ def make_dims(num_k_heads: int, num_v_heads: int, head_dim: int, conv_width: int
                     activation, in_dtype, mma, l2_eps, scale, prefill_form, out_dtype, 0 if qk_l2norm else 1)
 
 
+def make_linear_dims(num_k_heads: int, num_v_heads: int, head_dim: int, in_dtype: int = GDN_BF16,
+                     out_dtype: int = GDN_F32, scale: float = 1.0, mma: int = GDN_MMA_AUTO,
+                     prefill_form: int = GDN_PREFILL_AUTO) -> gdn_dims:
+    """gdn_dims of a linear attention layer: q and k used as given."""
+    return make_dims(num_k_heads, num_v_heads, head_dim, in_dtype=in_dtype, out_dtype=out_dtype, scale=scale, mma=mma,
+                     prefill_form=prefill_form, qk_l2norm=False)
+
+
 class gdn_norm_dims(ctypes.Structure):
     _fields_ = [
         ("struct_size", ctypes.c_int32),
@@ -85,6 +96,33 @@ def make_norm_dims(groups: int, group_size: int, in_dtype: int = GDN_F32, gate_d
     bf16 gate, weight and result, SiLU gate after a root-mean-square norm per v-head)."""
     return gdn_norm_dims(ctypes.sizeof(gdn_norm_dims), groups, group_size, in_dtype, gate_dtype, param_dtype,
                          out_dtype, activation, int(centered), int(gate_first), int(shared_params), eps)
+
+
+class gdn_block_norm_dims(ctypes.Structure):
+    _fields_ = [
+        ("struct_size", ctypes.c_int32),
+        ("width", ctypes.c_int32),
+        ("in_dtype", ctypes.c_int32),
+        ("residual_dtype", ctypes.c_int32),
+        ("gate_dtype", ctypes.c_int32),
+        ("param_dtype", ctypes.c_int32),
+        ("out_dtype", ctypes.c_int32),
+        ("activation", ctypes.c_int32),
+        ("post_norm", ctypes.c_int32),
+        ("centered", ctypes.c_int32),
+        ("scale", ctypes.c_float),
+        ("eps", ctypes.c_float),
+    ]
+
+
+def make_block_norm_dims(width: int, in_dtype: int = GDN_BF16, residual_dtype: int = GDN_BF16, gate_dtype: int = GDN_BF16,
+                         param_dtype: int = GDN_BF16, out_dtype: int = GDN_BF16, activation: int = GDN_ACT_NONE,
+                         post_norm: bool = False, centered: bool = False, scale: float = 1.0,
+                         eps: float = 1e-6) -> gdn_block_norm_dims:
+    """gdn_block_norm_dims with struct_size set; the defaults are a plain residual sum of bf16 rows
+    and the root-mean-square norm after it."""
+    return gdn_block_norm_dims(ctypes.sizeof(gdn_block_norm_dims), width, in_dtype, residual_dtype, gate_dtype, param_dtype,
+                               out_dtype, activation, int(post_norm), int(centered), scale, eps)
 
 
 class GDNError(RuntimeError):
@@ -136,10 +174,20 @@ def _load() -> ctypes.CDLL:
     lib.gdn_slot_pack.argtypes = [D, I32, P, P, P, I32, P]
     lib.gdn_slot_unpack.argtypes = [D, I32, P, P, P, I32, P]
     lib.gdn_group_norm.argtypes = [ctypes.POINTER(gdn_norm_dims), P, I64, P, I64, P, P, P, I64, I32, P]
+    lib.gdn_linear_workspace_size.argtypes = [D, I32, I32, ctypes.POINTER(SZ)]
+    lib.gdn_linear_prefill.argtypes = [D, P, I64, P, I64, P, I64, P, I64, P, P, I32, I32, P, P, SZ, P]
+    lib.gdn_linear_decode.argtypes = [D, P, I64, P, I64, P, I64, P, I64, P, P, I32, P]
+    lib.gdn_block_norm.argtypes = [ctypes.POINTER(gdn_block_norm_dims), P, I64, P, I64, P, I64, P, P, P, P, P, I64, P, I64,
+                                   I32, P]
+    lib.gdn_sample_workspace_size.argtypes = [I32, I32, ctypes.POINTER(SZ)]
+    lib.gdn_sample.argtypes = [P, I64, I32, I32, I32, P, P, P, P, P, P, P, P, SZ, P]
+    lib.gdn_tree_follow.argtypes = [P, P, P, P, P, I32, I32, I32, P, P, P, P]
     for fn in ("gdn_dims_init", "gdn_conv_update", "gdn_prefill_workspace_size", "gdn_prefill_chunked",
                "gdn_prefill_fused_workspace_size", "gdn_prefill_fused", "gdn_prefill_fused_static", "gdn_decode_batched",
                "gdn_decode_fused", "gdn_slot_copy", "gdn_slot_pointers", "gdn_tree_verify", "gdn_tree_accept",
-               "gdn_slot_packed_size", "gdn_slot_pack", "gdn_slot_unpack", "gdn_group_norm"):
+               "gdn_slot_packed_size", "gdn_slot_pack", "gdn_slot_unpack", "gdn_group_norm", "gdn_linear_workspace_size",
+               "gdn_linear_prefill", "gdn_linear_decode", "gdn_block_norm", "gdn_sample_workspace_size", "gdn_sample",
+               "gdn_tree_follow"):
         getattr(lib, fn).restype = ctypes.c_int
     lib.gdn_hbm_probe.argtypes = [P, SZ, ctypes.c_uint32, P]
     lib.gdn_hbm_probe.restype = ctypes.c_int
@@ -356,3 +404,50 @@ def gdn_group_norm(dims: gdn_norm_dims, x, x_stride: int, gate, gate_stride: int
                    rows: int, stream=None) -> None:
     _launch("gdn_group_norm", _LIB.gdn_group_norm, stream, x, ctypes.byref(dims), _ptr(x), x_stride, _ptr(gate),
             gate_stride, _ptr(weight), _ptr(bias), _ptr(y), y_stride, rows)
+
+
+def gdn_linear_workspace_size(dims: gdn_dims, num_seqs: int, total_tokens: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("gdn_linear_workspace_size",
+           _LIB.gdn_linear_workspace_size(ctypes.byref(dims), num_seqs, total_tokens, ctypes.byref(out)))
+    return int(out.value)
+
+
+def gdn_linear_prefill(dims: gdn_dims, q, q_stride: int, k, k_stride: int, v, v_stride: int, g, g_stride: int, o,
+                       cu_seqlens, num_seqs: int, total_tokens: int, state_ptrs, workspace, workspace_bytes: int,
+                       stream=None) -> None:
+    _launch("gdn_linear_prefill", _LIB.gdn_linear_prefill, stream, q, ctypes.byref(dims), _ptr(q), q_stride, _ptr(k), k_stride,
+            _ptr(v), v_stride, _ptr(g), g_stride, _ptr(o), _ptr(cu_seqlens), num_seqs, total_tokens, _ptr(state_ptrs),
+            _ptr(workspace), workspace_bytes)
+
+
+def gdn_linear_decode(dims: gdn_dims, q, q_stride: int, k, k_stride: int, v, v_stride: int, g, g_stride: int, o, state_ptrs,
+                      m: int, stream=None) -> None:
+    _launch("gdn_linear_decode", _LIB.gdn_linear_decode, stream, q, ctypes.byref(dims), _ptr(q), q_stride, _ptr(k), k_stride,
+            _ptr(v), v_stride, _ptr(g), g_stride, _ptr(o), _ptr(state_ptrs), m)
+
+
+def gdn_block_norm(dims: gdn_block_norm_dims, x, x_stride: int, residual, residual_stride: int, gate, gate_stride: int,
+                   post_weight, post_bias, pre_weight, pre_bias, residual_out, residual_out_stride: int, y, y_stride: int,
+                   rows: int, stream=None) -> None:
+    _launch("gdn_block_norm", _LIB.gdn_block_norm, stream, x, ctypes.byref(dims), _ptr(x), x_stride, _ptr(residual),
+            residual_stride, _ptr(gate), gate_stride, _ptr(post_weight), _ptr(post_bias), _ptr(pre_weight), _ptr(pre_bias),
+            _ptr(residual_out), residual_out_stride, _ptr(y), y_stride, rows)
+
+
+def gdn_sample_workspace_size(rows: int, vocab: int) -> int:
+    out = ctypes.c_size_t(0)
+    _check("gdn_sample_workspace_size", _LIB.gdn_sample_workspace_size(rows, vocab, ctypes.byref(out)))
+    return int(out.value)
+
+
+def gdn_sample(logits, stride: int, dtype: int, rows: int, vocab: int, temperature, top_k, top_p, min_p, uniform, tokens,
+               prob, workspace, workspace_bytes: int, stream=None) -> None:
+    _launch("gdn_sample", _LIB.gdn_sample, stream, logits, _ptr(logits), stride, dtype, rows, vocab, _ptr(temperature),
+            _ptr(top_k), _ptr(top_p), _ptr(min_p), _ptr(uniform), _ptr(tokens), _ptr(prob), _ptr(workspace), workspace_bytes)
+
+
+def gdn_tree_follow(drafted, sampled, pending, parents, cu_nodes, m: int, total_nodes: int, max_nodes: int, accepted,
+                    next, path, stream=None) -> None:
+    _launch("gdn_tree_follow", _LIB.gdn_tree_follow, stream, pending, _ptr(drafted), _ptr(sampled), _ptr(pending),
+            _ptr(parents), _ptr(cu_nodes), m, total_nodes, max_nodes, _ptr(accepted), _ptr(next), _ptr(path))

@@ -16,7 +16,8 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libgdn.so")
-SOURCES = ["gdn_api.cpp", "conv.hip", "decode.hip", "prefill.hip", "probe.hip", "tree.hip", "snapshot.hip", "norm.hip"]
+SOURCES = ["gdn_api.cpp", "conv.hip", "decode.hip", "prefill.hip", "probe.hip", "tree.hip", "snapshot.hip", "norm.hip",
+           "linear.hip", "block_norm.hip", "sample.hip"]
 ARCH = "gfx950"
 
 FLAGS = [

@@ -269,6 +269,34 @@ gdn_status pack_impl(const char* fn, const gdn_dims* dims, int32_t format, const
   return hip_status(unpack ? gdn::launch_slot_unpack(a, n, s) : gdn::launch_slot_pack(a, n, s), fn);
 }
 
+// Checks of the linear attention entry points, and what both hand to the kernels.
+gdn_status check_linear(const gdn_dims* d, const char* fn) {
+  if (gdn_status st = check_dims(d, fn)) return st;
+  if (!d->qk_l2norm_off)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: q and k are used as given: qk_l2norm_off must be 1", fn);
+  return GDN_OK;
+}
+
+gdn_status linear_args(const gdn_dims* d, const char* fn, const void* q, int64_t qs, const void* k, int64_t ks,
+                       const void* v, int64_t vs, const float* g, int64_t gs, void* o, const uint64_t* state_ptrs,
+                       int32_t rows, gdn::LinearArgs* a) {
+  if (!q || !k || !v || !g || !o) return fail(GDN_ERR_NULL, "%s: q, k, v, g and o are required", fn);
+  const int64_t qk_w = static_cast<int64_t>(d->num_k_heads) * d->head_dim;
+  const int64_t v_w = static_cast<int64_t>(d->num_v_heads) * d->head_dim;
+  if (qs < 0 || ks < 0 || vs < 0 || gs < 0) return fail(GDN_ERR_SHAPE, "%s: negative stride", fn);
+  if (rows > 1 && (qs < qk_w || ks < qk_w || vs < v_w || (gs != 0 && gs < d->num_v_heads)))
+    return fail(GDN_ERR_SHAPE, "%s: row strides (q %lld, k %lld, v %lld, g %lld) below row widths (%lld, %lld, %d)", fn,
+                static_cast<long long>(qs), static_cast<long long>(ks), static_cast<long long>(vs),
+                static_cast<long long>(gs), static_cast<long long>(qk_w), static_cast<long long>(v_w), d->num_v_heads);
+  const int64_t per = d->in_dtype == GDN_BF16 ? 8 : 4;  // elements in 16 bytes
+  if (!aligned16(q) || !aligned16(k) || !aligned16(v) || qs % per || ks % per || vs % per)
+    return fail(GDN_ERR_ALIGN, "%s: q, k, v must be 16-byte aligned with strides a multiple of 16 bytes", fn);
+  *a = gdn::LinearArgs{q, qs, k, ks, v, vs, g, gs, o, state_ptrs, d->num_k_heads, d->num_v_heads, d->head_dim,
+                       d->num_v_heads / d->num_k_heads, d->scale, d->in_dtype == GDN_BF16, d->out_dtype == GDN_BF16,
+                       resolve_mma(d), d->prefill_form};
+  return GDN_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -681,6 +709,169 @@ gdn_status gdn_group_norm(const gdn_norm_dims* dims, const void* x, int64_t x_st
   a.shared = dims->shared_params;
   a.eps = dims->eps;
   return hip_status(gdn::launch_group_norm(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+gdn_status gdn_linear_workspace_size(const gdn_dims* dims, int32_t num_seqs, int32_t total_tokens, size_t* bytes) {
+  const char* fn = "gdn_linear_workspace_size";
+  if (gdn_status st = check_linear(dims, fn)) return st;
+  if (!bytes) return fail(GDN_ERR_NULL, "%s: bytes is NULL", fn);
+  if (num_seqs < 0 || total_tokens < 0) return fail(GDN_ERR_SHAPE, "%s: negative count", fn);
+  *bytes = gdn::linear_workspace_bytes(dims->num_v_heads, dims->head_dim, num_seqs, total_tokens, dims->prefill_form);
+  return GDN_OK;
+}
+
+gdn_status gdn_linear_prefill(const gdn_dims* dims, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const float* g, int64_t g_stride, void* o,
+                              const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                              const uint64_t* state_ptrs, void* workspace, size_t workspace_bytes, void* stream) {
+  const char* fn = "gdn_linear_prefill";
+  if (gdn_status st = check_linear(dims, fn)) return st;
+  if (num_seqs < 0 || total_tokens < 0) return fail(GDN_ERR_SHAPE, "%s: negative count", fn);
+  if (num_seqs == 0 && total_tokens != 0) return fail(GDN_ERR_SHAPE, "%s: tokens without sequences", fn);
+  if (total_tokens == 0) return GDN_OK;
+  if (!cu_seqlens || !state_ptrs) return fail(GDN_ERR_NULL, "%s: cu_seqlens and state_ptrs are required", fn);
+  gdn::LinearArgs a;
+  if (gdn_status st = linear_args(dims, fn, q, q_stride, k, k_stride, v, v_stride, g, g_stride, o, state_ptrs,
+                                  total_tokens, &a))
+    return st;
+  const size_t need =
+      gdn::linear_workspace_bytes(dims->num_v_heads, dims->head_dim, num_seqs, total_tokens, dims->prefill_form);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(GDN_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", fn, need, workspace_bytes,
+                workspace ? "" : " (NULL)");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(GDN_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
+  return hip_status(gdn::launch_linear_prefill(a, cu_seqlens, num_seqs, total_tokens, workspace,
+                                               static_cast<hipStream_t>(stream)),
+                    fn);
+}
+
+gdn_status gdn_linear_decode(const gdn_dims* dims, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const float* g, int64_t g_stride, void* o,
+                             const uint64_t* state_ptrs, int32_t m, void* stream) {
+  const char* fn = "gdn_linear_decode";
+  if (gdn_status st = check_linear(dims, fn)) return st;
+  if (m < 0) return fail(GDN_ERR_SHAPE, "%s: negative m", fn);
+  if (m == 0) return GDN_OK;
+  if (m > 65535) return fail(GDN_ERR_SHAPE, "%s: m = %d above the grid limit 65535", fn, m);
+  if (!state_ptrs) return fail(GDN_ERR_NULL, "%s: state_ptrs is required", fn);
+  gdn::LinearArgs a;
+  if (gdn_status st = linear_args(dims, fn, q, q_stride, k, k_stride, v, v_stride, g, g_stride, o, state_ptrs, m, &a))
+    return st;
+  return hip_status(gdn::launch_linear_decode(a, m, static_cast<hipStream_t>(stream)), fn);
+}
+
+gdn_status gdn_block_norm(const gdn_block_norm_dims* dims, const void* x, int64_t x_stride, const void* residual,
+                          int64_t residual_stride, const void* gate, int64_t gate_stride, const void* post_weight,
+                          const void* post_bias, const void* pre_weight, const void* pre_bias, void* residual_out,
+                          int64_t residual_out_stride, void* y, int64_t y_stride, int32_t rows, void* stream) {
+  const char* fn = "gdn_block_norm";
+  if (!dims) return fail(GDN_ERR_NULL, "%s: dims is NULL", fn);
+  if (dims->struct_size != static_cast<int32_t>(sizeof(gdn_block_norm_dims)))
+    return fail(GDN_ERR_SHAPE, "%s: dims->struct_size is %d, expected %d", fn, dims->struct_size,
+                static_cast<int>(sizeof(gdn_block_norm_dims)));
+  const int64_t width = dims->width;
+  if (width < 1) return fail(GDN_ERR_SHAPE, "%s: width must be >= 1 (got %d)", fn, dims->width);
+  if (width > GDN_BLOCK_NORM_MAX_WIDTH)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: rows of %d values not built (at most %d)", fn, dims->width,
+                GDN_BLOCK_NORM_MAX_WIDTH);
+  for (int32_t t : {dims->in_dtype, dims->residual_dtype, dims->gate_dtype, dims->param_dtype, dims->out_dtype})
+    if (t != GDN_F32 && t != GDN_BF16) return fail(GDN_ERR_DTYPE, "%s: unknown dtype %d", fn, t);
+  if (dims->activation != GDN_ACT_NONE && dims->activation != GDN_ACT_SILU && dims->activation != GDN_ACT_SIGMOID)
+    return fail(GDN_ERR_DTYPE, "%s: unknown activation %d", fn, dims->activation);
+  for (int32_t f : {dims->post_norm, dims->centered})
+    if (f != 0 && f != 1) return fail(GDN_ERR_DTYPE, "%s: a switch must be 0 or 1 (got %d)", fn, f);
+  if (!(dims->eps >= 0.0f) || !(dims->eps < 1e30f)) return fail(GDN_ERR_SHAPE, "%s: eps must be finite and >= 0", fn);
+  if (!(dims->scale >= -1e30f) || !(dims->scale <= 1e30f)) return fail(GDN_ERR_SHAPE, "%s: scale must be finite", fn);
+  if (rows < 0) return fail(GDN_ERR_SHAPE, "%s: negative rows", fn);
+  if (!dims->post_norm && (post_weight || post_bias))
+    return fail(GDN_ERR_SHAPE, "%s: post_weight and post_bias without post_norm", fn);
+  if (rows == 0) return GDN_OK;
+  if (!x || (!residual_out && !y)) return fail(GDN_ERR_NULL, "%s: x and one of residual_out and y are required", fn);
+  if (!y && (pre_weight || pre_bias)) return fail(GDN_ERR_NULL, "%s: pre_weight and pre_bias without y", fn);
+  const struct {
+    const void* p;
+    int64_t stride;
+    int32_t dtype;
+    bool broadcast;
+  } rows_of[] = {{x, x_stride, dims->in_dtype, false},
+                 {residual, residual_stride, dims->residual_dtype, false},
+                 {gate, gate_stride, dims->gate_dtype, true},
+                 {residual_out, residual_out_stride, dims->residual_dtype, false},
+                 {y, y_stride, dims->out_dtype, false}};
+  for (const auto& t : rows_of) {
+    if (!t.p) continue;
+    if (t.stride < 0 || (rows > 1 && t.stride < width && !(t.broadcast && t.stride == 0)))
+      return fail(GDN_ERR_SHAPE, "%s: a row stride of %lld is below the row width %lld", fn,
+                  static_cast<long long>(t.stride), static_cast<long long>(width));
+    if (reinterpret_cast<uintptr_t>(t.p) & (t.dtype == GDN_BF16 ? 1u : 3u))
+      return fail(GDN_ERR_ALIGN, "%s: a pointer is not aligned to its type", fn);
+  }
+  for (const void* p : {post_weight, post_bias, pre_weight, pre_bias})
+    if (reinterpret_cast<uintptr_t>(p) & (dims->param_dtype == GDN_BF16 ? 1u : 3u))
+      return fail(GDN_ERR_ALIGN, "%s: a pointer is not aligned to its type", fn);
+  if (residual_out && residual_out == residual && rows > 1 && residual_out_stride != residual_stride)
+    return fail(GDN_ERR_SHAPE, "%s: residual_out on top of residual needs its stride", fn);
+  const gdn::BlockNormArgs a{x, x_stride, residual, residual_stride, gate, gate_stride, post_weight, post_bias,
+                             pre_weight, pre_bias, residual_out, residual_out_stride, y, y_stride, rows, dims->width,
+                             dims->in_dtype == GDN_BF16, dims->residual_dtype == GDN_BF16,
+                             dims->gate_dtype == GDN_BF16, dims->param_dtype == GDN_BF16, dims->out_dtype == GDN_BF16,
+                             dims->activation, dims->post_norm, dims->centered, dims->scale, dims->eps};
+  return hip_status(gdn::launch_block_norm(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+static gdn_status check_sample(const char* fn, int32_t rows, int32_t vocab) {
+  if (rows < 0) return fail(GDN_ERR_SHAPE, "%s: negative rows", fn);
+  if (vocab < 1 || vocab > (1 << 24)) return fail(GDN_ERR_SHAPE, "%s: vocab %d outside 1 .. 2^24", fn, vocab);
+  return GDN_OK;
+}
+
+gdn_status gdn_sample_workspace_size(int32_t rows, int32_t vocab, size_t* bytes) {
+  const char* fn = "gdn_sample_workspace_size";
+  if (!bytes) return fail(GDN_ERR_NULL, "%s: bytes is NULL", fn);
+  if (gdn_status st = check_sample(fn, rows, vocab)) return st;
+  *bytes = gdn::sample_workspace_bytes(rows, vocab);
+  return GDN_OK;
+}
+
+gdn_status gdn_sample(const void* logits, int64_t stride, int32_t dtype, int32_t rows, int32_t vocab,
+                      const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                      const float* uniform, int32_t* tokens, float* prob, void* workspace, size_t workspace_bytes,
+                      void* stream) {
+  const char* fn = "gdn_sample";
+  if (gdn_status st = check_sample(fn, rows, vocab)) return st;
+  if (dtype != GDN_F32 && dtype != GDN_BF16) return fail(GDN_ERR_DTYPE, "%s: unknown dtype %d", fn, dtype);
+  if (rows == 0) return GDN_OK;
+  if (!logits || !uniform || !tokens) return fail(GDN_ERR_NULL, "%s: logits, uniform and tokens are required", fn);
+  if (stride < 0 || (rows > 1 && stride < vocab))
+    return fail(GDN_ERR_SHAPE, "%s: row stride %lld below the vocabulary %d", fn, static_cast<long long>(stride), vocab);
+  if (reinterpret_cast<uintptr_t>(logits) & (dtype == GDN_BF16 ? 1u : 3u))
+    return fail(GDN_ERR_ALIGN, "%s: logits are not aligned to their type", fn);
+  const size_t need = gdn::sample_workspace_bytes(rows, vocab);
+  if (need > 0 && (!workspace || workspace_bytes < need))
+    return fail(GDN_ERR_WORKSPACE, "%s: workspace of %zu bytes needed, %zu given%s", fn, need, workspace_bytes,
+                workspace ? "" : " (NULL)");
+  if (reinterpret_cast<uintptr_t>(workspace) & 255u)
+    return fail(GDN_ERR_ALIGN, "%s: workspace must be 256-byte aligned", fn);
+  const gdn::SampleArgs a{logits, stride, dtype == GDN_BF16, rows, vocab, temperature, top_k, top_p,
+                          min_p, uniform, tokens, prob, workspace};
+  return hip_status(gdn::launch_sample(a, static_cast<hipStream_t>(stream)), fn);
+}
+
+gdn_status gdn_tree_follow(const int32_t* drafted, const int32_t* sampled, const int32_t* pending, const int32_t* parents,
+                           const int32_t* cu_nodes, int32_t m, int32_t total_nodes, int32_t max_nodes, int32_t* accepted,
+                           int32_t* next, int32_t* path, void* stream) {
+  const char* fn = "gdn_tree_follow";
+  if (m < 0 || total_nodes < 0) return fail(GDN_ERR_SHAPE, "%s: negative m or total_nodes", fn);
+  if (m == 0 && total_nodes != 0) return fail(GDN_ERR_SHAPE, "%s: nodes without slots", fn);
+  if (max_nodes < 1) return fail(GDN_ERR_SHAPE, "%s: max_nodes must be >= 1 (got %d)", fn, max_nodes);
+  if (max_nodes > GDN_TREE_MAX_NODES)
+    return fail(GDN_ERR_UNSUPPORTED, "%s: trees of %d nodes not built (at most %d)", fn, max_nodes, GDN_TREE_MAX_NODES);
+  if (m == 0) return GDN_OK;
+  if (!pending || !cu_nodes || !accepted || !next || (total_nodes > 0 && (!drafted || !sampled)))
+    return fail(GDN_ERR_NULL, "%s: drafted, sampled, pending, cu_nodes, accepted and next are required", fn);
+  const gdn::FollowArgs a{drafted, sampled, pending, parents, cu_nodes, accepted, next, path, m, total_nodes, max_nodes};
+  return hip_status(gdn::launch_tree_follow(a, static_cast<hipStream_t>(stream)), fn);
 }
 
 }  // extern "C"

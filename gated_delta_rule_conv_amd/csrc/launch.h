@@ -202,4 +202,98 @@ struct NormArgs {
 
 hipError_t launch_group_norm(const NormArgs& a, hipStream_t s);
 
+// Linear attention with a decay for each head.
+struct LinearArgs {
+  const void* q;
+  int64_t q_stride;
+  const void* k;
+  int64_t k_stride;
+  const void* v;
+  int64_t v_stride;
+  const float* g;
+  int64_t g_stride;  // 0: one decay a head for all tokens
+  void* o;
+  const uint64_t* state_ptrs;
+  int32_t hk;
+  int32_t hv;
+  int32_t d;
+  int32_t group;  // hv / hk
+  float scale;
+  int32_t bf16;  // q, k and v
+  int32_t o_bf16;
+  int32_t mma;  // 1 = fp32, 2 = bf16x3's place: exact bf16 thirds (resolved)
+  int32_t form;  // gdn_prefill_form
+};
+
+hipError_t launch_linear_decode(const LinearArgs& a, int32_t m, hipStream_t s);
+size_t linear_workspace_bytes(int32_t hv, int32_t d, int32_t num_seqs, int32_t total_tokens, int32_t form);
+hipError_t launch_linear_prefill(const LinearArgs& a, const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                                 void* workspace, hipStream_t s);
+
+struct BlockNormArgs {
+  const void* x;
+  int64_t x_stride;
+  const void* residual;  // nullable
+  int64_t residual_stride;
+  const void* gate;  // nullable
+  int64_t gate_stride;  // 0: one row for all
+  const void* post_weight;  // nullable, as the next three
+  const void* post_bias;
+  const void* pre_weight;
+  const void* pre_bias;
+  void* h;  // nullable, as y
+  int64_t h_stride;
+  void* y;
+  int64_t y_stride;
+  int32_t rows;
+  int32_t width;
+  int32_t x_bf16;
+  int32_t residual_bf16;  // of h too
+  int32_t gate_bf16;
+  int32_t param_bf16;
+  int32_t y_bf16;
+  int32_t activation;  // gdn_activation
+  int32_t post;
+  int32_t centered;
+  float scale;
+  float eps;
+};
+
+hipError_t launch_block_norm(const BlockNormArgs& a, hipStream_t s);
+
+struct SampleArgs {
+  const void* logits;
+  int64_t stride;
+  int32_t bf16;
+  int32_t rows;
+  int32_t vocab;
+  const float* temperature;  // nullable, as the next three
+  const int32_t* top_k;
+  const float* top_p;
+  const float* min_p;
+  const float* uniform;
+  int32_t* tokens;
+  float* prob;  // nullable
+  void* workspace;
+};
+
+size_t sample_workspace_bytes(int32_t rows, int32_t vocab);
+hipError_t launch_sample(const SampleArgs& a, hipStream_t s);
+
+struct FollowArgs {
+  const int32_t* drafted;
+  const int32_t* sampled;
+  const int32_t* pending;
+  const int32_t* parents;  // nullable (chains)
+  const int32_t* cu_nodes;
+  int32_t* accepted;
+  int32_t* next;
+  int32_t* path;  // nullable
+  int32_t m;
+  int32_t total_nodes;
+  int32_t max_nodes;
+};
+
+hipError_t launch_tree_follow(const FollowArgs& a, hipStream_t s);
+
 }  // namespace gdn

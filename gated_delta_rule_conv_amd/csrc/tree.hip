@@ -1017,6 +1017,38 @@ hipError_t accept_t(const AcceptArgs& a, int32_t m, hipStream_t s) {
   }
 }
 
+// ------------------------------------------------------------------------------ follow
+// A wave a slot, a lane a node: from the slot down, the first child whose drafted token is the one that was sampled at the
+// node above (gdn_tree_follow). A step is a ballot and two reads of a lane; numbers rise along a path, so it ends.
+constexpr int kFollowWaves = 4;
+
+__global__ __launch_bounds__(kFollowWaves* kWave) void tree_follow_kernel(FollowArgs a) {
+  const int i = blockIdx.x * kFollowWaves + __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = threadIdx.x & (kWave - 1);
+  if (i >= a.m) return;
+  int first, n;
+  tree_span(a.cu_nodes, i, a.total_nodes, a.max_nodes, first, n);
+  int want = ((ci32*)a.pending)[i];
+  const bool live = lane < n;
+  const int up = live ? parent_of(a.parents, first, lane) : -2;
+  const int draft = live ? a.drafted[first + lane] : -1;
+  const int said = live ? a.sampled[first + lane] : -1;
+  int at = -1, steps = 0, path = -1;
+  while (true) {
+    const uint64_t fits = __ballot(up == at && draft == want && draft >= 0);
+    if (fits == 0) break;
+    at = __builtin_ctzll(fits);
+    want = __builtin_amdgcn_readlane(said, at);
+    if (lane == steps) path = at;
+    ++steps;
+  }
+  if (lane == 0) {
+    a.accepted[i] = at;
+    a.next[i] = want;
+  }
+  if (a.path && lane < a.max_nodes) a.path[static_cast<int64_t>(i) * a.max_nodes + lane] = path;
+}
+
 }  // namespace
 
 hipError_t launch_tree_verify(const TreeArgs& a, int32_t m, hipStream_t s) {
@@ -1027,6 +1059,11 @@ hipError_t launch_tree_verify(const TreeArgs& a, int32_t m, hipStream_t s) {
 hipError_t launch_tree_accept(const AcceptArgs& a, int32_t m, hipStream_t s) {
   if (m == 0) return hipSuccess;
   return a.bf16 ? accept_t<uint16_t>(a, m, s) : accept_t<float>(a, m, s);
+}
+
+hipError_t launch_tree_follow(const FollowArgs& a, hipStream_t s) {
+  tree_follow_kernel<<<static_cast<unsigned>((a.m + kFollowWaves - 1) / kFollowWaves), kFollowWaves * kWave, 0, s>>>(a);
+  return hipGetLastError();
 }
 
 }  // namespace gdn

@@ -8,9 +8,10 @@ and conv state in such a pool of slots; aprender #5279, "Phase plan", phase P5, 
 the slot index on the launch grid and hands the kernels one address per slot.)
 
 ``conv_update``, ``prefill``, ``decode``, ``decode_fused``, ``tree_verify``, ``tree_accept``,
-``slot_pack``, ``slot_unpack`` and ``group_norm`` derive pointers, strides and views from torch
-tensors and call the library; all arithmetic happens in the HIP kernels. The last five check the type,
-size, layout and device of every operand first (ValueError): the kernels see addresses alone.
+``slot_pack``, ``slot_unpack``, ``group_norm``, ``linear_prefill``, ``linear_decode``, ``block_norm``, ``sample`` and
+``tree_follow`` derive pointers, strides and views from torch tensors and call the library; all arithmetic happens in
+the HIP kernels. From ``tree_verify`` on they check the type, size, layout and device of every operand first
+(ValueError): the kernels see addresses alone.
 """
 
 from __future__ import annotations
@@ -180,6 +181,7 @@ def tree_record(dims: gdn_dims, total_nodes: int, device="cuda"):
 
 _F32, _I32, _I64 = torch.float32, torch.int32, torch.int64
 _DTYPES = {GDN_F32: torch.float32, GDN_BF16: torch.bfloat16}
+_KINDS = {torch.float32: GDN_F32, torch.bfloat16: GDN_BF16}
 
 
 def _at(fn: str, name: str, t: torch.Tensor, dtype, n: int, device: int) -> int:
@@ -274,7 +276,7 @@ def group_norm(dims, x: torch.Tensor, weight, y: torch.Tensor, gate=None, bias=N
         _row_stride("y", y, _DTYPES.get(dims.out_dtype), rows, n, at), rows)
 
 
-def _row_stride(name: str, t: torch.Tensor, dtype, rows: int, n: int, device: int) -> int:
+def _row_stride(name: str, t: torch.Tensor, dtype, rows: int, n: int, device: int, fn: str = "group_norm") -> int:
     """Row stride of t, which holds n values in `rows` contiguous rows, [rows, width] or [rows, a, b] (an axis of
     length 1 has no stride to speak of)."""
     s, shape = t.stride(), t.shape
@@ -282,9 +284,120 @@ def _row_stride(name: str, t: torch.Tensor, dtype, rows: int, n: int, device: in
             len(s) == 2 and (s[1] == 1 or shape[1] == 1)
             or len(s) == 3 and (s[2] == 1 or shape[2] == 1) and (s[1] == shape[2] or shape[1] == 1) or n == 0):
         return s[0]
-    raise ValueError(f"group_norm: {name} must be {rows} rows of {n // rows if rows else 0} adjacent values of {dtype}, [rows, "
+    raise ValueError(f"{fn}: {name} must be {rows} rows of {n // rows if rows else 0} adjacent values of {dtype}, [rows, "
                      f"width] or [rows, a, b], on the device of x (got {t.dtype}, shape {tuple(shape)}, strides {s}, "
                      f"device {t.device})")
+
+
+def _linear_operands(fn: str, dims: gdn_dims, q, k, v, g, o, state_ptrs):
+    """q, k, v and g with their strides, and o's and the pointers' addresses."""
+    rows, at, dtype = q.shape[0], q.get_device(), _DTYPES.get(dims.in_dtype)
+    wide, values = rows * dims.num_k_heads * dims.head_dim, rows * dims.num_v_heads * dims.head_dim
+    if g.dim() == 1:
+        gp, gs = _at(fn, "g", g, _F32, dims.num_v_heads, at), 0
+    else:
+        gp, gs = g.data_ptr(), _row_stride("g", g, _F32, rows, rows * dims.num_v_heads, at, fn)
+        if gs < dims.num_v_heads and rows > 1:  # (a stride of 0 would be read as one row of decays for all tokens)
+            raise ValueError(f"{fn}: the rows of g overlap (strides {g.stride()}); one row of decays for all tokens is given as "
+                             f"[{dims.num_v_heads}]")
+        gs = max(gs, dims.num_v_heads)
+    return (q.data_ptr(), _row_stride("q", q, dtype, rows, wide, at, fn), k.data_ptr(), _row_stride("k", k, dtype, rows, wide, at, fn),
+            v.data_ptr(), _row_stride("v", v, dtype, rows, values, at, fn), gp, gs,
+            _at(fn, "o", o, _DTYPES.get(dims.out_dtype), values, at), _at(fn, "state_ptrs", state_ptrs, _I64, state_ptrs.numel(), at))
+
+
+def linear_prefill(dims: gdn_dims, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, o: torch.Tensor,
+                   cu_seqlens: torch.Tensor, state_ptrs: torch.Tensor, workspace, stream=None) -> None:
+    """Linear attention with a decay for each head over packed prompts, the slots' states in place (dims from
+    make_linear_dims(), workspace from linear_workspace()). q, k: [T, Hk * d] or [T, Hk, d], v likewise, rows
+    of a wider tensor allowed; g: fp32 [T, Hv], or [Hv] for one decay a head."""
+    fn, n, rows = "linear_prefill", state_ptrs.numel(), q.shape[0]
+    qp, qs, kp, ks, vp, vs, gp, gs, op, sp = _linear_operands(fn, dims, q, k, v, g, o, state_ptrs)
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _lib._launch("gdn_linear_prefill", _lib._LIB.gdn_linear_prefill, stream, q, ctypes.byref(dims), qp, qs, kp, ks, vp, vs, gp, gs, op,
+                 _at(fn, "cu_seqlens", cu_seqlens, _I32, n + 1, q.get_device()), n, rows, sp,
+                 None if workspace is None else _at(fn, "workspace", workspace, workspace.dtype, workspace.numel(), q.get_device()), size)
+
+
+def linear_decode(dims: gdn_dims, q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, g: torch.Tensor, o: torch.Tensor,
+                  state_ptrs: torch.Tensor, stream=None) -> None:
+    """linear_prefill for one token of each of m slots: row i of q, k, v, g and o is slot i's."""
+    fn, m = "linear_decode", state_ptrs.numel()
+    qp, qs, kp, ks, vp, vs, gp, gs, op, sp = _linear_operands(fn, dims, q, k, v, g, o, state_ptrs)
+    if q.shape[0] != m:
+        raise ValueError(f"{fn}: {q.shape[0]} rows for {m} slots")
+    _lib._launch("gdn_linear_decode", _lib._LIB.gdn_linear_decode, stream, q, ctypes.byref(dims), qp, qs, kp, ks, vp, vs, gp, gs, op, sp, m)
+
+
+def block_norm(dims, x: torch.Tensor, residual, y, residual_out=None, gate=None, post_weight=None, post_bias=None,
+               pre_weight=None, pre_bias=None, stream=None) -> None:
+    """h = residual + scale act(gate) a with a = x or its norm, and y the norm of h (dims from make_block_norm_dims(), all
+    operands' types among them). h goes to residual_out (may be residual itself; None: not stored); y None: no
+    second norm; residual None: 0. x, residual, residual_out, y: [rows, width]; gate: the same, or [width] for all rows; weights and
+    biases [width]."""
+    fn, rows, width, at = "block_norm", x.shape[0], dims.width, x.get_device()
+    n, stream_t, param = rows * width, _DTYPES.get(dims.residual_dtype), _DTYPES.get(dims.param_dtype)
+
+    def of(name, t, dtype):
+        return (None, 0) if t is None else (t.data_ptr(), _row_stride(name, t, dtype, rows, n, at, fn))
+
+    def vector(name, t):
+        return None if t is None else _at(fn, name, t, param, width, at)
+
+    gate_t = _DTYPES.get(dims.gate_dtype)
+    one = gate is not None and gate.dim() == 1
+    gp, gs = (_at(fn, "gate", gate, gate_t, width, at), 0) if one else of("gate", gate, gate_t)
+    if not one and gate is not None and gs < width and rows > 1:
+        raise ValueError(f"{fn}: the rows of gate overlap (strides {gate.stride()}); one row for all is given as [{width}]")
+    if gate is not None and not one:
+        gs = max(gs, width)
+    _lib._launch("gdn_block_norm", _lib._LIB.gdn_block_norm, stream, x, ctypes.byref(dims), *of("x", x, _DTYPES.get(dims.in_dtype)),
+                 *of("residual", residual, stream_t), gp, gs, vector("post_weight", post_weight), vector("post_bias", post_bias),
+                 vector("pre_weight", pre_weight), vector("pre_bias", pre_bias), *of("residual_out", residual_out, stream_t),
+                 *of("y", y, _DTYPES.get(dims.out_dtype)), rows)
+
+
+def sample(logits: torch.Tensor, uniform: torch.Tensor, tokens: torch.Tensor, workspace, temperature=None, top_k=None,
+           top_p=None, min_p=None, prob=None, stream=None) -> None:
+    """tokens[r] (int32) drawn from row r of logits [rows, vocab] by the random number uniform[r] in [0, 1): softmax at
+    temperature[r] (0: the likeliest token), cut by top_k[r] (int32), top_p[r] and min_p[r]; prob[r]: its
+    probability there. fp32 where not said; None leaves a filter out. workspace from sample_workspace()."""
+    fn, at = "sample", logits.get_device()
+    if logits.dim() != 2 or logits.dtype not in _KINDS:
+        raise ValueError(f"{fn}: logits must be fp32 or bf16 [rows, vocab] (got {logits.dtype}, shape {tuple(logits.shape)})")
+    rows, vocab = logits.shape
+
+    def of(name, t, dtype=_F32):
+        return None if t is None else _at(fn, name, t, dtype, rows, at)
+
+    size = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _lib._launch("gdn_sample", _lib._LIB.gdn_sample, stream, logits, logits.data_ptr(),
+                 _row_stride("logits", logits, logits.dtype, rows, rows * vocab, at, fn), _KINDS[logits.dtype], rows, vocab,
+                 of("temperature", temperature), of("top_k", top_k, _I32), of("top_p", top_p), of("min_p", min_p),
+                 _at(fn, "uniform", uniform, _F32, rows, at), _at(fn, "tokens", tokens, _I32, rows, at), of("prob", prob),
+                 None if workspace is None else _at(fn, "workspace", workspace, workspace.dtype, workspace.numel(), at), size)
+
+
+def tree_follow(drafted: torch.Tensor, sampled: torch.Tensor, pending: torch.Tensor, parents, cu_nodes: torch.Tensor,
+                max_nodes: int, accepted: torch.Tensor, next: torch.Tensor, path=None, stream=None) -> None:
+    """The path that the sampled tokens take through each slot's drafted tree: its last node in accepted (tree_accept's
+    operand), the token after it in next (may be pending itself), its nodes in path [m, max_nodes]. All int32."""
+    fn, m, rows, at = "tree_follow", pending.numel(), drafted.numel(), pending.get_device()
+    _lib._launch("gdn_tree_follow", _lib._LIB.gdn_tree_follow, stream, pending, _at(fn, "drafted", drafted, _I32, rows, at),
+                 _at(fn, "sampled", sampled, _I32, rows, at), _at(fn, "pending", pending, _I32, m, at),
+                 None if parents is None else _at(fn, "parents", parents, _I32, rows, at), _at(fn, "cu_nodes", cu_nodes, _I32, m + 1, at),
+                 m, rows, max_nodes, _at(fn, "accepted", accepted, _I32, m, at), _at(fn, "next", next, _I32, m, at),
+                 None if path is None else _at(fn, "path", path, _I32, m * max_nodes, at))
+
+
+def linear_workspace(dims: gdn_dims, num_seqs: int, total_tokens: int, device="cuda") -> torch.Tensor:
+    nbytes = _lib.gdn_linear_workspace_size(dims, num_seqs, total_tokens)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
+
+
+def sample_workspace(rows: int, vocab: int, device="cuda") -> torch.Tensor:
+    nbytes = _lib.gdn_sample_workspace_size(rows, vocab)
+    return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
 def prefill_workspace(dims: gdn_dims, num_seqs: int, total_tokens: int, device="cuda") -> torch.Tensor:
@@ -297,7 +410,8 @@ def prefill_fused_workspace(dims: gdn_dims, num_seqs: int, total_tokens: int, de
     return torch.empty(max(nbytes, 256), dtype=torch.uint8, device=device)
 
 
-__all__ = ["SlotPool", "channels", "conv_update", "decode", "decode_fused", "group_norm", "packed_slots", "prefill",
-           "prefill_fused", "prefill_fused_static", "prefill_fused_workspace", "prefill_workspace", "qkv_views",
-           "slot_pack", "slot_unpack", "torch_in_dtype", "tree_accept", "tree_record", "tree_verify",
+__all__ = ["SlotPool", "block_norm", "channels", "conv_update", "decode", "decode_fused", "group_norm", "linear_decode",
+           "linear_prefill", "linear_workspace", "packed_slots", "prefill", "prefill_fused", "prefill_fused_static",
+           "prefill_fused_workspace", "prefill_workspace", "qkv_views", "sample", "sample_workspace", "slot_pack",
+           "slot_unpack", "torch_in_dtype", "tree_accept", "tree_follow", "tree_record", "tree_verify",
            "GDN_F32", "GDN_BF16"]

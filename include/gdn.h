@@ -18,7 +18,10 @@
  * conv and SSM state (same issue, comment "Where concurrency is lost", item 3).
  *
  * Around it, over the same slots: gdn_tree_verify / gdn_tree_accept (speculative decoding),
- * gdn_slot_pack / gdn_slot_unpack (8-bit snapshots) and gdn_group_norm (the norm of o).
+ * gdn_slot_pack / gdn_slot_unpack (8-bit snapshots) and gdn_group_norm (the norm of o). For the
+ * other layers of a hybrid model and the end of its step: gdn_linear_prefill / gdn_linear_decode (linear
+ * attention with a decay for each head, over the same slots), gdn_block_norm (the norms around a block),
+ * gdn_sample (a token from logits) and gdn_tree_follow (the path of sampled tokens through a drafted tree).
  *
  * Conventions for every entry point
  *  - Every pointer argument except `dims`, `bytes` and `stream` is a DEVICE pointer
@@ -63,7 +66,11 @@ typedef enum gdn_dtype { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
 
 /* Activation applied to the conv output. The pages name the conv only as a depthwise
  * causal Conv1d, so the default is the identity; SiLU is offered as an option. */
-typedef enum gdn_activation { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1 } gdn_activation;
+typedef enum gdn_activation {
+  GDN_ACT_NONE = 0,
+  GDN_ACT_SILU = 1,
+  GDN_ACT_SIGMOID = 2 /* of gdn_block_norm's gate alone */
+} gdn_activation;
 
 /* Matrix-core precision of the prefill contractions (decode is plain fp32 FMA), and of
  * gdn_tree_verify's products over d, for which BF16X3 is closer than its name: see there.
@@ -478,6 +485,127 @@ typedef struct gdn_norm_dims {
 gdn_status gdn_group_norm(const gdn_norm_dims* dims, const void* x, int64_t x_stride, const void* gate,
                           int64_t gate_stride, const void* weight, const void* bias, void* y, int64_t y_stride,
                           int32_t rows, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * Linear attention with a decay for each head, over the slots of the layer core (a SlotPool's states,
+ * their pointer arrays, copies and snapshots serve both kinds of layer):
+ *   S_t = exp(g_t) S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t.
+ * dims: num_k_heads, num_v_heads (v-head j reads k-head j / (Hv / Hk)), head_dim, in_dtype (of q, k, v), out_dtype,
+ * scale, mma and prefill_form. q and k are used as given: qk_l2norm_off must be 1 (else GDN_ERR_UNSUPPORTED), so
+ * that dims of the layer core are not taken by mistake. No conv state is touched.
+ *
+ *  q, k       [rows][Hk*d], v [rows][Hv*d] in dims->in_dtype, row strides in elements.
+ *  g          [rows][Hv] fp32, row stride g_stride (>= Hv); g_stride 0: one row of Hv decays for all tokens.
+ *             exp(g) is the share of the state that a token keeps: g <= 0, minus infinity included (nothing is
+ *             kept: a new document inside a sequence). In the prefill a g below -128 counts as -128, which is 0 too.
+ *  o          [rows][Hv][d] contiguous in dims->out_dtype.
+ *  state_ptrs device u64, fp32 [Hv][d_v][d_k] states, 16-byte aligned, updated in place. An entry of 0 marks an
+ *             inactive slot (nothing read or written for it, its o rows untouched). Distinct slots.
+ *  Alignment: q, k, v 16-byte aligned, their strides multiples of 16 bytes.
+ *
+ * gdn_linear_prefill: packed ragged sequences, cu_seqlens device int32 [num_seqs+1] as for gdn_prefill_chunked;
+ * zero-length sequences keep their state; rows outside [0, total_tokens) are not touched. A token's o depends on no
+ * later token, whatever that holds (an infinity or a NaN among its values included).
+ *  workspace  gdn_linear_workspace_size(dims, num_seqs, total_tokens) bytes, 256-byte aligned, contents ignored;
+ *             may be NULL where that is 0.
+ * gdn_linear_decode: one token for each of m slots; a slot's bits do not depend on the rest of the call.
+ */
+gdn_status gdn_linear_workspace_size(const gdn_dims* dims, int32_t num_seqs, int32_t total_tokens, size_t* bytes);
+gdn_status gdn_linear_prefill(const gdn_dims* dims, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                              const void* v, int64_t v_stride, const float* g, int64_t g_stride, void* o,
+                              const int32_t* cu_seqlens, int32_t num_seqs, int32_t total_tokens,
+                              const uint64_t* state_ptrs, void* workspace, size_t workspace_bytes, void* stream);
+gdn_status gdn_linear_decode(const gdn_dims* dims, const void* q, int64_t q_stride, const void* k, int64_t k_stride,
+                             const void* v, int64_t v_stride, const float* g, int64_t g_stride, void* o,
+                             const uint64_t* state_ptrs, int32_t m, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * gdn_block_norm -- between two blocks of a residual stream, for every row: the norm after the block that gave x, its
+ * gate and scale, the residual sum, and the norm before the next block:
+ *   a = post_norm ? N(x) post_weight + post_bias : x
+ *   h = residual + scale act(gate) a
+ *   y = N(h) pre_weight + pre_bias
+ * with N(x) = x / sqrt(mean(x^2) + eps), or, centered, (x - mean(x)) / sqrt(var(x) + eps), over the whole row. h is
+ * rounded to residual_dtype where it is stored; y is the norm of h before that. Sums are fp32, under a power of two
+ * where the squares leave its range (any finite x and h will do). A row of zeros with eps = 0 is 0 / 0: NaN.
+ */
+typedef struct gdn_block_norm_dims {
+  int32_t struct_size;    /* sizeof(gdn_block_norm_dims) as compiled by the caller */
+  int32_t width;          /* 1 .. GDN_BLOCK_NORM_MAX_WIDTH */
+  int32_t in_dtype;       /* gdn_dtype of x */
+  int32_t residual_dtype; /* gdn_dtype of residual and residual_out */
+  int32_t gate_dtype;     /* gdn_dtype of gate */
+  int32_t param_dtype;    /* gdn_dtype of the weights and biases */
+  int32_t out_dtype;      /* gdn_dtype of y (bf16: rounded to nearest even) */
+  int32_t activation;     /* gdn_activation of the gate */
+  int32_t post_norm;      /* 0: a = x (post_weight and post_bias must be NULL); 1: the norm after the block */
+  int32_t centered;       /* of both norms: 0 root mean square; 1 mean taken off first */
+  float scale;            /* finite; 1 for a plain sum */
+  float eps;              /* finite, >= 0 */
+} gdn_block_norm_dims;
+
+/*  x, residual, gate, residual_out, y  [rows][width] with row strides (elements), any alignment of their type.
+ *              residual NULL: 0 (a stream's first block).   gate NULL: 1; gate_stride 0: one row for all rows.
+ *              residual_out may be residual itself (with its stride), or NULL: h is not stored.   y NULL: no second
+ *              norm. One of the two is required. Otherwise no output overlaps an input or the other output.
+ *  the weights [width], NULL: 1; the biases [width], NULL: 0.
+ *  Errors: GDN_ERR_UNSUPPORTED for a width above GDN_BLOCK_NORM_MAX_WIDTH.
+ */
+#define GDN_BLOCK_NORM_MAX_WIDTH 32768
+gdn_status gdn_block_norm(const gdn_block_norm_dims* dims, const void* x, int64_t x_stride, const void* residual,
+                          int64_t residual_stride, const void* gate, int64_t gate_stride, const void* post_weight,
+                          const void* post_bias, const void* pre_weight, const void* pre_bias, void* residual_out,
+                          int64_t residual_out_stride, void* y, int64_t y_stride, int32_t rows, void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * gdn_sample -- one token for every row of logits x, from a random number u the caller gives. Per row, with m the
+ * largest x and T its temperature:
+ *   weights  w_i = e^((x_i - m) / T); the order is by x, the lower index first among equals
+ *   top_k    the first k of the order stay
+ *   top_p    of those the shortest beginning whose weight reaches p times the weight of all of them stays: a token stays
+ *            while the weight before it is below that
+ *   min_p    of those the ones with w_i >= min_p (w_i >= 1 for a min_p above 1) stay
+ *   token    the lowest index i at which the stayers' weights up to i, in index order, pass u times their sum
+ *   prob     w_token / that sum
+ * T <= 0 (or NaN): the lowest index that has m, prob 1. A NaN logit counts as minus infinity; a row with nothing above
+ * minus infinity gives token -1, prob 0. Beside an x of plus infinity only others like it weigh anything.
+ * Weights are whole multiples of 2^-S with S = min(52, 62 - ceil(log2 vocab)): smaller ones are 0, sums are exact, and a row's
+ * token depends on nothing else in the call.
+ *
+ *  logits     [rows][vocab] in dtype (a gdn_dtype), row stride in elements, any alignment of the type.
+ *  temperature, top_p, min_p  device fp32 [rows], top_k device int32 [rows]; NULL, or an entry that filters nothing
+ *             (k <= 0 or k >= vocab; p >= 1 or NaN; min_p <= 0 or NaN), leaves the filter out; NULL temperature: 1.
+ *             p <= 0 keeps the first of the order alone.
+ *  uniform    device fp32 [rows] in [0, 1); others count as the nearest number there, NaN as 0.
+ *  tokens     device int32 [rows].   prob: device fp32 [rows], or NULL.
+ *  vocab      1 .. 2^24.   workspace: gdn_sample_workspace_size(rows, vocab) bytes, 256-byte aligned, contents ignored;
+ *             may be NULL where that is 0.
+ */
+gdn_status gdn_sample_workspace_size(int32_t rows, int32_t vocab, size_t* bytes);
+gdn_status gdn_sample(const void* logits, int64_t stride, int32_t dtype, int32_t rows, int32_t vocab,
+                      const float* temperature, const int32_t* top_k, const float* top_p, const float* min_p,
+                      const float* uniform, int32_t* tokens, float* prob, void* workspace, size_t workspace_bytes,
+                      void* stream);
+
+/* ---------------------------------------------------------------------------------
+ * gdn_tree_follow -- between gdn_tree_verify and gdn_tree_accept: which nodes of each slot's drafted tree the sampled
+ * tokens take. From the slot itself, whose next token is pending[i], the path goes on to the first child (lowest
+ * number) whose drafted token is the one wanted, from where the token sampled at that node is wanted; it ends where no
+ * child has it. With tokens sampled at every node from the model's own distribution this is exact: the tokens
+ * of the path and the one after it are what decoding token by token with the same random numbers would give.
+ *
+ *  drafted, sampled  device int32 [total_nodes]: each node's token, and the one sampled from its logits. Negative ones
+ *             (no token) are never followed.
+ *  pending    device int32 [m]: the token after the slot's last one.
+ *  parents, cu_nodes, m, total_nodes, max_nodes  as given to gdn_tree_verify.
+ *  accepted   device int32 [m]: the path's last node inside its tree (-1: none): gdn_tree_accept's operand.
+ *  next       device int32 [m]: the token after the path: sampled at its last node, or pending[i] if there is none.
+ *  path       device int32 [m][max_nodes]: the path's nodes in order, then -1; or NULL.
+ *  next may be pending itself.
+ */
+gdn_status gdn_tree_follow(const int32_t* drafted, const int32_t* sampled, const int32_t* pending, const int32_t* parents,
+                           const int32_t* cu_nodes, int32_t m, int32_t total_nodes, int32_t max_nodes, int32_t* accepted,
+                           int32_t* next, int32_t* path, void* stream);
 
 /* Thread-local text describing the last non-OK status returned on this thread. */
 const char* gdn_last_error(void);
