@@ -3,6 +3,7 @@
 
 #include "device_common.h"
 #include "launch.h"
+#include "mma.h"
 
 namespace gdn {
 namespace {
@@ -115,52 +116,662 @@ hipError_t decode_t(const LinearArgs& a, int32_t m, hipStream_t s) {
 }
 
 // ----------------------------------------------------------------------------- prefill
+//
+// A sequence goes in chunks of 64 tokens from its own first one. With G_i the sum of g over a chunk's tokens up
+// to i, n its last, and S the state before it:
+//   o_i = scale (e^G_i S q_i + sum_{j <= i} e^(G_i - G_j) (q_i . k_j) v_j)
+//   S  <- e^G_n S + sum_j e^(G_n - G_j) v_j k_j^T
+// all four products on matrix cores. A workgroup takes a v-head of a tile, a run of a sequence's chunks; each of its
+// waves owns D / 4 columns (D / 2 waves of 16 for D = 32) of S^T [d_k][d_v] in accumulators, where they lie as a product's left operand wants them: lane
+// l of a 16x16 tile's result holds rows 4 h + r (h = l / 16, r < 4) of column l % 16, so a step over 32 contracted values takes its
+// values in the order 32 s + 16 u + 4 h + r (u < 2; fp32: 16 s + 4 h + r) from both operands, and S never passes through LDS.
+// q is stored in LDS in that order, k, v as they came (read by rows for q . k, by columns, transposed on the way, for the
+// state), the masked scores in that order again.
+//
+// Precision: with bf16 input every product has one operand that is exact in bf16. The other is fp32 and goes as three bf16
+// thirds, x = a + b + c exactly (8 bits each, cut, not rounded): three products, no rounding but those of fp32 sums. fp32 input
+// goes through fp32 products. Sums of g are kept in base 2 as a multiple of 2^-8, exact up to 2^16, and a rest, so that
+// differences between tokens behind a strongly forgetting one keep their digits.
+//
+// Long sequences are cut into tiles of LinearPlan::tokens so that enough workgroups run: a first pass forms what each tile
+// adds to the state, a scan the state before each tile, and the last pass runs all tiles at once. Tiles begin at a
+// sequence's own first token and their length depends on the layer alone: a sequence has the same bits whatever
+// is packed with it.
 
-// The recurrence token by token: a workgroup a (sequence, v-head), 256 / D threads a state row.
-template <int D, typename T>
-__global__ __launch_bounds__(256) void linear_tokens_kernel(LinearArgs a, const int32_t* cu, int total) {
-  constexpr int TPR = 256 / D, COLS = D / TPR;
-  __shared__ float kq[2][D];
-  const int j = blockIdx.x, i = blockIdx.y, h = j / a.group;
-  const int row = threadIdx.x / TPR, c0 = threadIdx.x % TPR * COLS;
-  const uint64_t sp = a.state_ptrs[i];
-  if (sp == 0) return;
-  const int lo = max(cu[i], 0), hi = min(cu[i + 1], total);
-  if (lo >= hi) return;
-  float* S = reinterpret_cast<float*>(sp) + (static_cast<int64_t>(j) * D + row) * D + c0;
-  float s[COLS];
-#pragma unroll
-  for (int e = 0; e < COLS; ++e) s[e] = S[e];
-  for (int64_t t = lo; t < hi; ++t) {
-    __syncthreads();
-    if (threadIdx.x < D) kq[0][threadIdx.x] = value(static_cast<const T*>(a.k) + t * a.k_stride + h * D + threadIdx.x);
-    else if (threadIdx.x < 2 * D)
-      kq[1][threadIdx.x - D] = value(static_cast<const T*>(a.q) + t * a.q_stride + h * D + threadIdx.x - D);
-    const float v = value(static_cast<const T*>(a.v) + t * a.v_stride + static_cast<int64_t>(j) * D + row);
-    const float f = expf(a.g[t * a.g_stride + j]);
-    __syncthreads();
-    float o = 0.f;
-#pragma unroll
-    for (int e = 0; e < COLS; ++e) {
-      s[e] = fmaf(v, kq[0][c0 + e], f * s[e]);
-      o = fmaf(s[e], kq[1][c0 + e], o);
-    }
-    o = group_sum<TPR>(o);
-    if (threadIdx.x % TPR == 0) put(a.o, a.o_bf16, (t * a.hv + j) * D + row, a.scale * o);
+constexpr int kChunk = 64;
+constexpr float kForget = -128.0f;  // e^-128 is 0 in fp32
+constexpr float kLog2e = 1.44269504088896340736f;
+
+__device__ __forceinline__ void barrier_lds() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+  __builtin_amdgcn_s_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+__device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// Sum over the wave's lanes up to each one.
+__device__ __forceinline__ float wave_scan(float v) {
+  const auto add = [&](auto moved) { v += __int_as_float(moved); };
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x111, 0xF, 0xF, false));  // row_shr 1, 2, 4, 8
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x112, 0xF, 0xF, false));
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x114, 0xF, 0xF, false));
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x118, 0xF, 0xF, false));
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x142, 0xA, 0xF, false));  // lane 15 of a row to the next row
+  add(__builtin_amdgcn_update_dpp(0, __float_as_int(v), 0x143, 0xC, 0xF, false));  // lane 31 to the upper rows
+  return v;
+}
+
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+typedef short i16x8 __attribute__((ext_vector_type(8)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef __attribute__((address_space(3))) i16x4 lds_i16x4;
+
+// Products of an input's values (bf16 or fp32), exact, with fp32 numbers.
+template <typename T>
+struct Prod;
+
+template <>
+struct Prod<uint16_t> {
+  static constexpr int STEP = 32, PER = 8;  // contracted values a step, a lane's of them
+  typedef bf16x8 Exact;
+  struct Full {
+    bf16x8 a, b, c;
+  };
+  // the high halves of two words
+  __device__ __forceinline__ static uint32_t tops(uint32_t lo, uint32_t hi) { return __builtin_amdgcn_perm(hi, lo, 0x07060302u); }
+  __device__ __forceinline__ static void thirds(float x, uint32_t& a, uint32_t& b, uint32_t& c) {
+    a = __float_as_uint(x);
+    const float r = x - __uint_as_float(a & 0xFFFF0000u);
+    b = __float_as_uint(r);
+    c = __float_as_uint(r - __uint_as_float(b & 0xFFFF0000u));
   }
+  __device__ __forceinline__ static Full full(const float (&x)[8]) {
+    u32x4 a, b, c;
 #pragma unroll
-  for (int e = 0; e < COLS; ++e) S[e] = s[e];
+    for (int e = 0; e < 4; ++e) {
+      uint32_t a0, b0, c0, a1, b1, c1;
+      thirds(x[2 * e], a0, b0, c0);
+      thirds(x[2 * e + 1], a1, b1, c1);
+      a[e] = tops(a0, a1);
+      b[e] = tops(b0, b1);
+      c[e] = tops(c0, c1);
+    }
+    return Full{__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, c)};
+  }
+  __device__ __forceinline__ static float value(const Exact& x, int e) { return static_cast<float>(x[e]); }
+  __device__ __forceinline__ static f32x4 exact(const Exact& a, const Exact& b, const f32x4& acc) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
+  }
+  // one of the three products of a full operand, the smallest first
+  static constexpr int PARTS = 3;
+  __device__ __forceinline__ static const bf16x8& part(const Full& f, int p) { return p == 0 ? f.c : p == 1 ? f.b : f.a; }
+  __device__ __forceinline__ static f32x4 left(const Full& a, const Exact& b, const f32x4& acc, int p) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(part(a, p), b, acc, 0, 0, 0);
+  }
+  __device__ __forceinline__ static f32x4 right(const Exact& a, const Full& b, const f32x4& acc, int p) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, part(b, p), acc, 0, 0, 0);
+  }
+};
+
+template <>
+struct Prod<float> {
+  static constexpr int STEP = 16, PER = 4;
+  typedef f32x4 Exact;
+  typedef f32x4 Full;
+  __device__ __forceinline__ static Full full(const float (&x)[4]) { return f32x4{x[0], x[1], x[2], x[3]}; }
+  __device__ __forceinline__ static float value(const Exact& x, int e) { return x[e]; }
+  __device__ __forceinline__ static f32x4 exact(const Exact& a, const Exact& b, f32x4 acc) {
+#pragma unroll
+    for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
+    return acc;
+  }
+  static constexpr int PARTS = 4;
+  __device__ __forceinline__ static f32x4 left(const Full& a, const Exact& b, const f32x4& acc, int p) {
+    return __builtin_amdgcn_mfma_f32_16x16x4f32(a[p], b[p], acc, 0, 0, 0);
+  }
+  __device__ __forceinline__ static f32x4 right(const Exact& a, const Full& b, const f32x4& acc, int p) {
+    return left(a, b, acc, p);
+  }
+};
+
+// Where a tile lies.
+struct Place {
+  int seq;   // -1: there is no such tile
+  int part;  // which of its sequence's
+  int slot;  // its room for a state in the workspace; -1: the only tile of its sequence
+};
+
+struct LinearPlan {
+  const int32_t* cu;
+  int32_t n;
+  int32_t total;
+  int32_t tokens;      // a tile's
+  const Place* tiles;  // by tile and (slots) by room; null: found by the workgroup
+  const Place* slots;
+  float* states;       // [rooms][hv][D][D]
+  float* kept;         // [rooms][hv]: e^(sum of g)
+  int32_t first;       // the launch's first tile
+};
+
+__device__ __forceinline__ void sequence(const LinearPlan& p, int i, int& lo, int& hi) {
+  lo = max(p.cu[i], 0);
+  hi = max(min(p.cu[i + 1], p.total), lo);
+}
+
+// Tile b, or with SLOTS the tile of room b, by a scan over the sequences, 64 at a time.
+template <bool SLOTS>
+__device__ Place find_place(const LinearPlan& p, int b) {
+  const int lane = threadIdx.x & (kWave - 1);
+  int tiles = 0, rooms = 0;
+  for (int i0 = 0; i0 < p.n; i0 += kWave) {
+    int lo = 0, hi = 0;
+    if (i0 + lane < p.n) sequence(p, i0 + lane, lo, hi);
+    const int t = (hi - lo) / p.tokens + ((hi - lo) % p.tokens != 0), r = t > 1 ? t : 0;
+    int ts = t, rs = r;
+#pragma unroll
+    for (int m = 1; m < kWave; m *= 2) {
+      const int a = __shfl_up(ts, m), c = __shfl_up(rs, m);
+      if (lane >= m) {
+        ts += a;
+        rs += c;
+      }
+    }
+    const int from = SLOTS ? rooms + rs - r : tiles + ts - t, here = SLOTS ? r : t;
+    const uint64_t hit = __ballot(b >= from && b < from + here);
+    if (hit) {
+      const int l = __builtin_ctzll(hit);
+      const int part = b - __shfl(from, l), room = rooms + __shfl(rs - r, l);
+      return Place{i0 + l, part, __shfl(r, l) ? room + part : -1};
+    }
+    tiles += __shfl(ts, kWave - 1);
+    rooms += __shfl(rs, kWave - 1);
+  }
+  return Place{-1, 0, -1};
+}
+
+template <bool SLOTS>
+__device__ __forceinline__ Place place_of(const LinearPlan& p, int b) {
+  const Place* table = SLOTS ? p.slots : p.tiles;
+  Place w = table ? table[b] : find_place<SLOTS>(p, b);
+  w.seq = __builtin_amdgcn_readfirstlane(w.seq);
+  w.part = __builtin_amdgcn_readfirstlane(w.part);
+  w.slot = __builtin_amdgcn_readfirstlane(w.slot);
+  return w;
+}
+
+// Both tables, for calls of many sequences: one workgroup, 1024 sequences at a time.
+constexpr int kTableThreads = 1024;
+__global__ __launch_bounds__(kTableThreads) void linear_table_kernel(LinearPlan p, Place* tiles, int n_tiles, Place* slots,
+                                                                     int n_slots) {
+  __shared__ int part[2][kTableThreads / kWave];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
+  int t0 = 0, r0 = 0;
+  for (int i0 = 0; i0 < p.n; i0 += kTableThreads) {
+    const int i = i0 + tid;
+    int lo = 0, hi = 0;
+    if (i < p.n) sequence(p, i, lo, hi);
+    const int t = (hi - lo) / p.tokens + ((hi - lo) % p.tokens != 0), r = t > 1 ? t : 0;
+    int ts = t, rs = r;
+#pragma unroll
+    for (int m = 1; m < kWave; m *= 2) {
+      const int a = __shfl_up(ts, m), c = __shfl_up(rs, m);
+      if (lane >= m) {
+        ts += a;
+        rs += c;
+      }
+    }
+    __syncthreads();
+    if (lane == kWave - 1) {
+      part[0][w] = ts;
+      part[1][w] = rs;
+    }
+    __syncthreads();
+    int at = t0 + ts - t, room = r0 + rs - r;
+    for (int v = 0; v < kTableThreads / kWave; ++v) {
+      if (v < w) {
+        at += part[0][v];
+        room += part[1][v];
+      }
+      t0 += part[0][v];
+      r0 += part[1][v];
+    }
+    for (int k = 0; k < t; ++k) {
+      if (at + k < n_tiles) tiles[at + k] = Place{i, k, r ? room + k : -1};
+      if (r && room + k < n_slots) slots[room + k] = Place{i, k, room + k};
+    }
+  }
+  for (int b = t0 + tid; b < n_tiles; b += kTableThreads) tiles[b] = Place{-1, 0, -1};
+  for (int b = r0 + tid; b < n_slots; b += kTableThreads) slots[b] = Place{-1, 0, -1};
+}
+
+template <int D, typename T>
+struct LinearCfg {
+  static constexpr int WAVES = D == 32 ? 2 : 4, THREADS = WAVES * kWave;
+  static constexpr int COLS = D / WAVES;    // d_v a wave
+  static constexpr int VT = COLS / 16;      // 16x16 tiles: of d_v a wave
+  static constexpr int KT = D / 16;         // of d_k
+  static constexpr int STEP = Prod<T>::STEP;
+  static constexpr int DS = D / STEP;       // steps over d
+  static constexpr int JS = kChunk / STEP;  // and over tokens
+  static constexpr int EPP = 16 / sizeof(T);        // values in 16 bytes
+  static constexpr int PPR = D / EPP;               // 16-byte pieces a row
+  static constexpr int PIECES = kChunk * PPR / THREADS;
+  // Rows of tiles are 16 bytes longer than their values, which spreads 16 rows' pieces of 16 bytes over all banks.
+  static constexpr int PITCH = D + EPP;
+  static constexpr int PROWS = kChunk + EPP;  // of the scores
+  static constexpr int PLANES = sizeof(T) == 2 ? 3 : 1;
+};
+
+// OUT: outputs and the state behind the tile; else what the tile adds to the state.
+template <int D, typename T, bool OUT>
+__global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1)) void linear_chunks_kernel(LinearArgs a, LinearPlan p) {
+  using C = LinearCfg<D, T>;
+  using P = Prod<T>;
+  using Exact = typename P::Exact;
+  using Full = typename P::Full;
+  constexpr int PITCH = C::PITCH, PROWS = C::PROWS;
+  __shared__ __attribute__((aligned(16))) T kl[kChunk * PITCH];
+  __shared__ __attribute__((aligned(16))) T vl[kChunk * PITCH];
+  __shared__ __attribute__((aligned(16))) T ql[OUT ? kChunk * PITCH : 16];
+  __shared__ __attribute__((aligned(16))) T pl[OUT ? C::PLANES * kChunk * PROWS : 16];
+  __shared__ __attribute__((aligned(16))) float gl[4][kChunk];  // G's multiple of 2^-8, its rest, e^G_i, e^(G_n - G_i)
+  __shared__ int broken[2];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int l16 = lane & 15, h4 = 4 * (lane >> 4);
+  const int b = blockIdx.x % a.hv, tile = p.first + blockIdx.x / a.hv;
+  // workgroups go round-robin to the 8 XCDs: neighbouring heads, which share k and q, to one of them
+  const int j = a.hv % 8 == 0 ? (b % 8) * (a.hv / 8) + b / 8 : b;
+  const Place at = place_of<!OUT>(p, tile);
+  if (at.seq < 0) return;
+  const uint64_t sp = a.state_ptrs[at.seq];
+  if (sp == 0) return;
+  int lo, hi;
+  sequence(p, at.seq, lo, hi);
+  lo = __builtin_amdgcn_readfirstlane(lo);
+  hi = __builtin_amdgcn_readfirstlane(hi);
+  const bool last = hi - lo <= (at.part + 1) * static_cast<int64_t>(p.tokens);
+  if (!OUT && last) return;  // (no tile follows)
+  const int start = lo + at.part * p.tokens, end = last ? hi : start + p.tokens;
+  const int h = j / a.group;
+  const int64_t head = static_cast<int64_t>(j) * D * D;
+  float* own = reinterpret_cast<float*>(sp) + head;
+  float* room = at.slot < 0 ? nullptr : p.states + static_cast<int64_t>(at.slot) * a.hv * D * D + head;
+  const int c0 = w * C::COLS;
+
+  f32x4 s[C::KT][C::VT];
+  if constexpr (OUT) {
+    const float* from = room ? room : own;
+#pragma unroll
+    for (int t = 0; t < C::VT; ++t)
+#pragma unroll
+      for (int k = 0; k < C::KT; ++k)
+        s[k][t] = *reinterpret_cast<const f32x4*>(from + (c0 + 16 * t + l16) * D + 16 * k + h4);
+    // score tiles above the diagonal inside a step stay zero
+    if constexpr (sizeof(T) == 2) {
+      for (int x = tid; x < 3 * 2 * 16 * 8; x += C::THREADS) {
+        const int plane = x / 256, r = x % 256 / 8, h = x % 8 / 2, half = x % 2;  // 4 bytes each
+        const int i = r < 16 ? r : 32 + r - 16, pos = (r < 16 ? 0 : 32) + 8 * h + 4 + 2 * half;
+        *reinterpret_cast<uint32_t*>(pl + (plane * kChunk + i) * PROWS + pos) = 0;
+      }
+    }
+  } else {
+#pragma unroll
+    for (int t = 0; t < C::VT; ++t)
+#pragma unroll
+      for (int k = 0; k < C::KT; ++k) s[k][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+  }
+
+  // --- a chunk's rows into registers, then into LDS
+  u32x4 kr[C::PIECES], vr[C::PIECES], qr[OUT ? C::PIECES : 1];
+  float gr = 0.f;
+  const int row0 = tid / C::PPR, piece = tid % C::PPR;
+  constexpr int ROWS_UP = C::THREADS / C::PPR;
+  const T* kb = static_cast<const T*>(a.k) + h * D + piece * C::EPP;
+  const T* qb = static_cast<const T*>(a.q) + h * D + piece * C::EPP;
+  const T* vb = static_cast<const T*>(a.v) + static_cast<int64_t>(j) * D + piece * C::EPP;
+  const auto load = [&](int t, int len) {
+#pragma unroll
+    for (int u = 0; u < C::PIECES; ++u) {
+      const int64_t r = t + min(row0 + u * ROWS_UP, len - 1);
+      kr[u] = *reinterpret_cast<const u32x4*>(kb + r * a.k_stride);
+      vr[u] = *reinterpret_cast<const u32x4*>(vb + r * a.v_stride);
+      if constexpr (OUT) qr[u] = *reinterpret_cast<const u32x4*>(qb + r * a.q_stride);
+    }
+    if (w == 0) gr = lane < len ? a.g[(t + static_cast<int64_t>(lane)) * a.g_stride + j] : 0.f;
+  };
+  // whether a value of 16 bytes is an infinity or a NaN
+  const auto odd = [](const u32x4& x) {
+    uint32_t o = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      if constexpr (sizeof(T) == 2) o |= ((x[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
+      else o |= ((x[e] & 0x7F800000u) + 0x00800000u) & 0x80000000u;
+    }
+    return o != 0;
+  };
+  float total_hi = 0.f, total_lo = 0.f;
+  const auto stage = [&](int len, int turn) {
+    bool any = false;
+#pragma unroll
+    for (int u = 0; u < C::PIECES; ++u) {
+      const int r = row0 + u * ROWS_UP;
+      const bool there = r < len;
+      const u32x4 zero = {0, 0, 0, 0};
+      const u32x4 k = there ? kr[u] : zero, v = there ? vr[u] : zero;
+      any |= odd(k) || odd(v);
+      *reinterpret_cast<u32x4*>(kl + r * PITCH + piece * C::EPP) = k;
+      *reinterpret_cast<u32x4*>(vl + r * PITCH + piece * C::EPP) = v;
+      if constexpr (OUT) {
+        const u32x4 q = there ? qr[u] : zero;
+        if constexpr (sizeof(T) == 2) {  // values 8 p .. + 7 of 32: h = 2 (p % 2) and the next, u = p / 2
+          T* to = ql + r * PITCH + 32 * (piece / 4) + 16 * (piece % 2) + 4 * (piece % 4 / 2);
+          *reinterpret_cast<u32x2*>(to) = u32x2{q[0], q[1]};
+          *reinterpret_cast<u32x2*>(to + 8) = u32x2{q[2], q[3]};
+        } else {
+          *reinterpret_cast<u32x4*>(ql + r * PITCH + piece * C::EPP) = q;
+        }
+      }
+    }
+    if (any) broken[turn] = 1;
+    if (w == 0) {
+      const float x = (gr < kForget ? kForget : gr) * kLog2e;  // (a NaN stays)
+      const float whole = rintf(x * 256.f) * 0x1p-8f;
+      const float gh = wave_scan(whole), gt = wave_scan(x - whole);
+      const float nh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gh), kWave - 1));
+      const float nt = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gt), kWave - 1));
+      gl[0][lane] = gh;
+      gl[1][lane] = gt;
+      gl[2][lane] = exp2_hw(gh + gt);
+      gl[3][lane] = exp2_hw((nh - gh) + (nt - gt));
+    }
+  };
+  // --- operands from LDS
+  const auto k_row = [&](int i, int st) {  // row i of k, step st over d
+    if constexpr (sizeof(T) == 2) {
+      const T* f = kl + i * PITCH + 32 * st + h4;
+      const u32x2 x = *reinterpret_cast<const u32x2*>(f), y = *reinterpret_cast<const u32x2*>(f + 16);
+      return __builtin_bit_cast(Exact, u32x4{x[0], x[1], y[0], y[1]});
+    } else {
+      return *reinterpret_cast<const Exact*>(kl + i * PITCH + 16 * st + h4);
+    }
+  };
+  const auto q_row = [&](int i, int st) {
+    return *reinterpret_cast<const Exact*>(ql + i * PITCH + (sizeof(T) == 2 ? 32 * st + 2 * h4 : 16 * st + h4));
+  };
+  const auto column = [&](const T* tl, int c, int st) {  // columns c + l16 of k or v, step st over tokens
+    if constexpr (sizeof(T) == 2) {
+      const T* f = tl + (32 * st + h4 + (l16 >> 2)) * PITCH + c + 4 * (l16 & 3);
+      const i16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(f));
+      const i16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_i16x4*)(f + 16 * PITCH));
+      const i16x8 z = {x[0], x[1], x[2], x[3], y[0], y[1], y[2], y[3]};
+      return __builtin_bit_cast(Exact, z);
+    } else {
+      Exact z;
+#pragma unroll
+      for (int r = 0; r < 4; ++r) z[r] = tl[(16 * st + h4 + r) * PITCH + c + l16];
+      return z;
+    }
+  };
+
+  f32x4 o[OUT ? 4 : 1][C::VT];  // o^T: rows d_v, columns tokens 16 i + l16
+  int o_at = 0, o_len = 0;
+  const auto store = [&]() {
+    if constexpr (OUT) {
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        if (16 * i + l16 >= o_len) continue;
+        const int64_t to = ((o_at + static_cast<int64_t>(16 * i + l16)) * a.hv + j) * D + c0 + h4;
+#pragma unroll
+        for (int t = 0; t < C::VT; ++t) {
+          const f32x4 v = o[i][t] * a.scale;
+          if (a.o_bf16) {
+            const u32x2 x = {static_cast<uint32_t>(to_bf16(v[0])) | static_cast<uint32_t>(to_bf16(v[1])) << 16,
+                             static_cast<uint32_t>(to_bf16(v[2])) | static_cast<uint32_t>(to_bf16(v[3])) << 16};
+            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.o) + to + 16 * t) = x;
+          } else {
+            *reinterpret_cast<f32x4*>(static_cast<float*>(a.o) + to + 16 * t) = v;
+          }
+        }
+      }
+    }
+  };
+
+  // A chunk with an infinity or a NaN in k or v is taken a token at a time: in a product with
+  // zeros it would reach the tokens before it.
+  int singly = start;  // tokens before this one
+  const auto span = [&](int t) { return t < singly ? 1 : min(kChunk, end - t); };
+  if (tid < 2) broken[tid] = 0;
+  load(start, span(start));
+  barrier_lds();
+  for (int t = start, turn = 0; t < end; turn ^= 1) {
+    const int len = span(t);
+    stage(len, turn);
+    store();
+    barrier_lds();
+    const bool again = __builtin_amdgcn_readfirstlane(broken[turn]) != 0 && len > 1;
+    if (tid == 0) broken[turn ^ 1] = 0;  // (read before the last barrier, set behind the next)
+    if (again) {
+      singly = t + len;
+      o_len = 0;
+      load(t, 1);
+      barrier_lds();
+      continue;
+    }
+    if (t + len < end) load(t + len, span(t + len));
+    const float kept = exp2_hw(gl[0][kChunk - 1] + gl[1][kChunk - 1]);
+    if constexpr (OUT) {
+      // scores of tokens j (rows) for tokens i (columns), 10 tiles on and below the diagonal
+      for (int x = w; x < 10; x += C::WAVES) {
+        const int ti = x >= 6 ? 3 : x >= 3 ? 2 : x >= 1 ? 1 : 0, tj = x - ti * (ti + 1) / 2;
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+        for (int st = 0; st < C::DS; ++st) acc = P::exact(k_row(16 * tj + l16, st), q_row(16 * ti + l16, st), acc);
+        const int i = 16 * ti + l16, j0 = 16 * tj + h4;
+        const float gi = gl[0][i], ri = gl[1][i];
+        const f32x4 gj = *reinterpret_cast<const f32x4*>(&gl[0][j0]), rj = *reinterpret_cast<const f32x4*>(&gl[1][j0]);
+        float v[4];
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = j0 + r <= i ? acc[r] * exp2_hw((gi - gj[r]) + (ri - rj[r])) : 0.f;
+        if constexpr (sizeof(T) == 2) {
+          uint32_t x3[3][4];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) P::thirds(v[r], x3[0][r], x3[1][r], x3[2][r]);
+          T* to = pl + i * PROWS + 32 * (tj / 2) + 2 * h4 + 4 * (tj % 2);
+#pragma unroll
+          for (int z = 0; z < 3; ++z)
+            *reinterpret_cast<u32x2*>(to + z * kChunk * PROWS) = u32x2{P::tops(x3[z][0], x3[z][1]), P::tops(x3[z][2], x3[z][3])};
+        } else {
+          *reinterpret_cast<f32x4*>(pl + i * PROWS + j0) = f32x4{v[0], v[1], v[2], v[3]};
+        }
+      }
+      // e^G_i S q_i
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+#pragma unroll
+        for (int t = 0; t < C::VT; ++t) o[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+      for (int st = 0; st < C::DS; ++st) {
+        Full sf[C::VT];
+#pragma unroll
+        for (int t = 0; t < C::VT; ++t) {
+          float x[P::PER];
+#pragma unroll
+          for (int e = 0; e < P::PER; ++e) x[e] = s[st * (C::STEP / 16) + e / 4][t][e % 4];
+          sf[t] = P::full(x);
+        }
+        Exact q[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) q[i] = q_row(16 * i + l16, st);
+#pragma unroll
+        for (int part = 0; part < P::PARTS; ++part)
+#pragma unroll
+          for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int t = 0; t < C::VT; ++t) o[i][t] = P::left(sf[t], q[i], o[i][t], part);
+      }
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const float f = gl[2][16 * i + l16];
+#pragma unroll
+        for (int t = 0; t < C::VT; ++t) o[i][t] = o[i][t] * f;
+      }
+      barrier_lds();
+    }
+#pragma unroll
+    for (int k = 0; k < C::KT; ++k)
+#pragma unroll
+      for (int t = 0; t < C::VT; ++t) s[k][t] = s[k][t] * kept;
+#pragma unroll
+    for (int st = 0; st < C::JS; ++st) {
+      Exact v[C::VT];
+      Full vf[C::VT];
+#pragma unroll
+      for (int t = 0; t < C::VT; ++t) v[t] = column(vl, c0 + 16 * t, st);
+      if constexpr (OUT) {
+#pragma unroll
+        for (int i = st * (C::STEP / 16); i < 4; ++i) {
+          Full sc;
+          const T* f = pl + (16 * i + l16) * PROWS + (sizeof(T) == 2 ? 32 * st + 2 * h4 : 16 * st + h4);
+          if constexpr (sizeof(T) == 2) {
+            sc.a = *reinterpret_cast<const bf16x8*>(f);
+            sc.b = *reinterpret_cast<const bf16x8*>(f + kChunk * PROWS);
+            sc.c = *reinterpret_cast<const bf16x8*>(f + 2 * kChunk * PROWS);
+          } else {
+            sc = *reinterpret_cast<const f32x4*>(f);
+          }
+#pragma unroll
+          for (int part = 0; part < P::PARTS; ++part)
+#pragma unroll
+            for (int t = 0; t < C::VT; ++t) o[i][t] = P::right(v[t], sc, o[i][t], part);
+        }
+      }
+      float f[P::PER];
+#pragma unroll
+      for (int u = 0; u < P::PER / 4; ++u) {
+        const f32x4 x = *reinterpret_cast<const f32x4*>(&gl[3][C::STEP * st + 16 * u + h4]);
+#pragma unroll
+        for (int r = 0; r < 4; ++r) f[4 * u + r] = x[r];
+      }
+#pragma unroll
+      for (int t = 0; t < C::VT; ++t) {
+        float x[P::PER];
+#pragma unroll
+        for (int e = 0; e < P::PER; ++e) x[e] = P::value(v[t], e) * f[e];
+        vf[t] = P::full(x);
+      }
+#pragma unroll
+      for (int k = 0; k < C::KT; ++k) {
+        const Exact kc = column(kl, 16 * k, st);
+#pragma unroll
+        for (int part = 0; part < P::PARTS; ++part)
+#pragma unroll
+          for (int t = 0; t < C::VT; ++t) s[k][t] = P::right(kc, vf[t], s[k][t], part);
+      }
+    }
+    total_hi += gl[0][kChunk - 1];
+    total_lo += gl[1][kChunk - 1];
+    barrier_lds();
+    o_at = t;
+    o_len = len;
+    t += len;
+  }
+  store();
+  float* to = OUT ? own : room;
+  if (OUT && !last) return;
+#pragma unroll
+  for (int t = 0; t < C::VT; ++t)
+#pragma unroll
+    for (int k = 0; k < C::KT; ++k) *reinterpret_cast<f32x4*>(to + (c0 + 16 * t + l16) * D + 16 * k + h4) = s[k][t];
+  if (!OUT && tid == 0) p.kept[static_cast<int64_t>(at.slot) * a.hv + j] = exp2_hw(total_hi + total_lo);
+}
+
+// The state before each tile of the sequences that have several, from what the tiles add: in place.
+constexpr int kScanThreads = 256;
+template <int D>
+__global__ __launch_bounds__(kScanThreads) void linear_scan_kernel(LinearArgs a, LinearPlan p) {
+  constexpr int BLOCKS = D * D / 4 / kScanThreads;  // workgroups a head, 4 values a thread
+  const int b = blockIdx.x % (a.hv * BLOCKS), j = b / BLOCKS;
+  const Place at = place_of<true>(p, p.first + blockIdx.x / (a.hv * BLOCKS));
+  if (at.seq < 0 || at.part != 0) return;
+  const uint64_t sp = a.state_ptrs[at.seq];
+  if (sp == 0) return;
+  int lo, hi;
+  sequence(p, at.seq, lo, hi);
+  const int n = (hi - lo) / p.tokens + ((hi - lo) % p.tokens != 0);
+  const int64_t e = static_cast<int64_t>(j) * (D * D / 4) + b % BLOCKS * kScanThreads + threadIdx.x;
+  const int64_t up = static_cast<int64_t>(a.hv) * (D * D / 4);
+  f32x4 z = reinterpret_cast<const f32x4*>(sp)[e];
+  f32x4* to = reinterpret_cast<f32x4*>(p.states) + at.slot * up + e;
+  const float* kept = p.kept + static_cast<int64_t>(at.slot) * a.hv + j;
+  for (int i = 0; i < n; ++i) {
+    const bool more = i + 1 < n;  // (the last tile added nothing)
+    const f32x4 added = more ? to[i * up] : f32x4{0.f, 0.f, 0.f, 0.f};
+    const float f = more ? kept[static_cast<int64_t>(i) * a.hv] : 0.f;
+    to[i * up] = z;
+    z = z * f + added;
+  }
+}
+
+struct LinearSizes {
+  int32_t tokens;  // a tile's
+  int64_t tiles, slots;
+  bool cut;  // sequences may have several tiles
+  size_t table, kept, states, bytes;  // offsets, and all of it
+};
+
+// A tile's length depends on the layer alone.
+int32_t tile_tokens(int32_t hv, int32_t d) {
+  const int32_t chunks = hv * d / 512;
+  return kChunk * (chunks < 2 ? 2 : chunks > 8 ? 8 : chunks);
+}
+
+LinearSizes sizes(int32_t hv, int32_t d, int32_t n, int32_t total, int32_t form) {
+  LinearSizes z{};
+  z.tokens = tile_tokens(hv, d);
+  z.cut = form != 1 && total > z.tokens;
+  if (!z.cut) z.tokens = INT32_MAX;
+  const int64_t seqs = n < total ? n : total;
+  z.tiles = seqs + (z.cut ? total / z.tokens : 0);
+  // a sequence of several tiles is longer than one: at most twice the whole tiles of all tokens
+  z.slots = z.cut ? 2 * static_cast<int64_t>(total / z.tokens) : 0;
+  const int64_t by_seq = z.slots / 2 + seqs;
+  if (z.cut && by_seq < z.slots) z.slots = by_seq;
+  const auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
+  z.table = 0;
+  z.kept = n > kWave ? up((z.tiles + z.slots) * sizeof(Place)) : 0;
+  z.states = z.kept + up(z.slots * hv * sizeof(float));
+  z.bytes = z.states + z.slots * hv * static_cast<size_t>(d) * d * sizeof(float);
+  return z;
+}
+
+template <int D, typename T>
+hipError_t prefill_dt(const LinearArgs& a, LinearPlan p, const LinearSizes& z, hipStream_t s) {
+  using C = LinearCfg<D, T>;
+  // fewer than 2^31 threads a launch
+  const int64_t most = ((int64_t)1 << 31) / (static_cast<int64_t>(a.hv) * (D * D / 4 > 256 ? D * D / 4 : 256));
+  hipError_t e = hipSuccess;
+  const auto in_turns = [&](int64_t n, auto launch) {
+    for (int64_t f = 0; f < n && e == hipSuccess; f += most) {
+      p.first = static_cast<int32_t>(f);
+      launch(static_cast<unsigned>((n - f < most ? n - f : most) * a.hv));
+      e = hipGetLastError();
+    }
+  };
+  in_turns(z.slots, [&](unsigned grid) { linear_chunks_kernel<D, T, false><<<grid, C::THREADS, 0, s>>>(a, p); });
+  in_turns(z.slots, [&](unsigned grid) { linear_scan_kernel<D><<<grid * (D * D / 4 / kScanThreads), kScanThreads, 0, s>>>(a, p); });
+  in_turns(z.tiles, [&](unsigned grid) { linear_chunks_kernel<D, T, true><<<grid, C::THREADS, 0, s>>>(a, p); });
+  return e;
 }
 
 template <typename T>
-hipError_t prefill_t(const LinearArgs& a, const int32_t* cu, int32_t n, int32_t total, hipStream_t s) {
-  const dim3 grid(static_cast<unsigned>(a.hv), static_cast<unsigned>(n));
+hipError_t prefill_t(const LinearArgs& a, const LinearPlan& p, const LinearSizes& z, hipStream_t s) {
   switch (a.d) {
-    case 32: linear_tokens_kernel<32, T><<<grid, 256, 0, s>>>(a, cu, total); break;
-    case 64: linear_tokens_kernel<64, T><<<grid, 256, 0, s>>>(a, cu, total); break;
-    default: linear_tokens_kernel<128, T><<<grid, 256, 0, s>>>(a, cu, total); break;
+    case 32: return prefill_dt<32, T>(a, p, z, s);
+    case 64: return prefill_dt<64, T>(a, p, z, s);
+    default: return prefill_dt<128, T>(a, p, z, s);
   }
-  return hipGetLastError();
 }
 
 }  // namespace
@@ -169,10 +780,24 @@ hipError_t launch_linear_decode(const LinearArgs& a, int32_t m, hipStream_t s) {
   return a.bf16 ? decode_t<uint16_t>(a, m, s) : decode_t<float>(a, m, s);
 }
 
-size_t linear_workspace_bytes(int32_t, int32_t, int32_t, int32_t, int32_t) { return 0; }
+size_t linear_workspace_bytes(int32_t hv, int32_t d, int32_t num_seqs, int32_t total_tokens, int32_t form) {
+  return sizes(hv, d, num_seqs, total_tokens, form).bytes;
+}
 
-hipError_t launch_linear_prefill(const LinearArgs& a, const int32_t* cu, int32_t n, int32_t total, void*, hipStream_t s) {
-  return a.bf16 ? prefill_t<uint16_t>(a, cu, n, total, s) : prefill_t<float>(a, cu, n, total, s);
+hipError_t launch_linear_prefill(const LinearArgs& a, const int32_t* cu, int32_t n, int32_t total, void* workspace, hipStream_t s) {
+  const LinearSizes z = sizes(a.hv, a.d, n, total, a.form);
+  char* ws = static_cast<char*>(workspace);
+  LinearPlan p{cu, n, total, z.tokens, nullptr, nullptr, reinterpret_cast<float*>(ws + z.states),
+               reinterpret_cast<float*>(ws + z.kept), 0};
+  if (n > kWave) {
+    Place* tiles = reinterpret_cast<Place*>(ws);
+    Place* slots = tiles + z.tiles;
+    linear_table_kernel<<<1, kTableThreads, 0, s>>>(p, tiles, static_cast<int>(z.tiles), slots, static_cast<int>(z.slots));
+    if (const hipError_t e = hipGetLastError()) return e;
+    p.tiles = tiles;
+    p.slots = slots;
+  }
+  return a.bf16 ? prefill_t<uint16_t>(a, p, z, s) : prefill_t<float>(a, p, z, s);
 }
 
 }  // namespace gdn
