@@ -1,11 +1,21 @@
 // One token a row of logits from a given random number, gfx950 (include/gdn.h, gdn_sample).
 //
 // Weights are whole numbers: w = round(2^S e^((x - m) / T)), the exponential in 64 bits, S = 62 minus
-// the bits of the vocabulary's size (44 for 2^18 tokens). Their sums are then exact in any order, so a row's
-// token depends on nothing but the row, and a border (top_p's, or the random number's) is met within 2^-S of
-// the largest weight a token. Values are ordered by a key that sorts as an unsigned number, so a filter's
-// border is found by counting (top_k) or weighing (top_p) the 2048 values of the key's leading 11 bits, then
-// the next 11 inside that bin, then the last 10; among equal values the lower index comes first.
+// the bits of the vocabulary's size, at most 51 (44 for 2^18 tokens). Their sums are then exact in any order, atomic or
+// not, so a row's token depends on nothing but the row, and a border (top_p's, or the random number's) is met within
+// 2^-S of the largest weight a token. Tokens whose weight is 0 do not count at all: they come last in the order.
+//
+// A row is cut into tiles of 1024 tokens, a wave each. Three or four launches, each over all rows:
+//   extremes  the largest and the least finite value of every tile
+//   weigh     rows without top_k and top_p: the weight of every tile. Others: counts and weights of 1024 bins of the distance
+//             from the row's largest value, in LDS, then added to the row's
+//   gather    (only where a filter is given) from the bins, the few in which the filters' borders must lie; the weight of every
+//             tile's tokens before them, and a list of the tokens inside them
+//   choose    a workgroup a row: the list sorted by (value, index), the borders met exactly, the kept ones' weights added to their
+//             tiles', the tile in which the weight passes u times the sum, and the token in it
+// A kept token is one whose (value, index), as one number that falls with the value and rises with the index, is not
+// above the last kept one's. A list that would be longer than 4096 (thousands of equal values at a border) is not made:
+// choose then looks the borders up in the row itself, 11 bits of the key at a time.
 
 #include "device_common.h"
 #include "launch.h"
@@ -13,23 +23,57 @@
 namespace gdn {
 namespace {
 
-constexpr int kThreads = 1024;
+constexpr int kThreads = 512, kWaves = kThreads / kWave;
+constexpr int kTile = 1024;               // tokens of a wave
+constexpr int kRounds = kTile / (8 * kWave);
+constexpr int kBins = 1024;
+constexpr int kList = 4096;
 constexpr uint32_t kLowest = 0x007FFFFFu;  // key_of(-infinity)
-constexpr int kTile = 4 * kThreads;         // tokens whose weights are summed together
-constexpr int kMaxTiles = (1 << 24) / kTile;
 
-template <typename T>
-__device__ __forceinline__ uint32_t key_of(T raw) {
-  float x;
-  if constexpr (sizeof(T) == 2) x = bf16_to_f32(raw);
-  else x = raw;
+// ------------------------------------------------------------------- values and weights
+
+// a key that sorts as the value does
+__device__ __forceinline__ uint32_t key_of(float x) {
   if (!(x == x)) return kLowest;  // a NaN is a token that cannot come
   x += 0.0f;                      // (-0 is 0)
   const uint32_t u = __float_as_uint(x);
-  return u & 0x80000000u ? ~u : u | 0x80000000u;
+  return u ^ (static_cast<uint32_t>(static_cast<int32_t>(u) >> 31) | 0x80000000u);
 }
 __device__ __forceinline__ float value_of(uint32_t key) {
   return __uint_as_float(key & 0x80000000u ? key & 0x7FFFFFFFu : ~key);
+}
+template <typename T>
+__device__ __forceinline__ float get(const T* p) {
+  if constexpr (sizeof(T) == 2) return bf16_to_f32(*p);
+  else return *p;
+}
+
+typedef float uf32x4 __attribute__((ext_vector_type(4), aligned(4)));
+typedef uint32_t uu32x4 __attribute__((ext_vector_type(4), aligned(2)));
+
+// values [i, i + 8) of a row, minus infinity past its end
+template <typename T>
+__device__ __forceinline__ void load8(const T* x, int i, int n, float (&v)[8]) {
+  if (i + 8 <= n) {
+    if constexpr (sizeof(T) == 2) {
+      const uu32x4 r = *reinterpret_cast<const uu32x4*>(x + i);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[2 * e] = __uint_as_float(r[e] << 16);
+        v[2 * e + 1] = __uint_as_float(r[e] & 0xFFFF0000u);
+      }
+    } else {
+      const uf32x4 a = *reinterpret_cast<const uf32x4*>(x + i), b = *reinterpret_cast<const uf32x4*>(x + i + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        v[e] = a[e];
+        v[4 + e] = b[e];
+      }
+    }
+  } else {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = i + e < n ? get(x + i + e) : -__builtin_inff();
+  }
 }
 
 // 2^t for t <= 0: the series of e^(f ln 2) for the part of t past its nearest whole number, |f| <= 1/2 (the first
@@ -53,32 +97,356 @@ __device__ __forceinline__ double power_of_two(double t) {
   return ldexp(s, static_cast<int>(n));
 }
 
+enum Mode { kNone, kLikeliest, kPlain, kListed, kLooked };
+
+// What a row's tokens are judged by.
 struct Row {
-  float most;       // the largest value
-  double per;       // log2(e) / T
-  double least;     // min_p, at most 1
-  int shift;        // S
+  float most;      // the largest value
+  double per;      // log2(e) / T
+  float far;       // a distance from the largest value beyond which a weight is surely 0
+  float bins;      // bins by distance
+  double least;    // min_p, at most 1
+  int shift;       // S
+  int32_t k;       // 0: no top_k
+  float p;         // 1: no top_p
+  int mode;        // kNone, kLikeliest, kPlain, or kListed for rows with a filter
+
   // e^((x - most) / T), of the largest value 1
-  __device__ __forceinline__ double weight(uint32_t key) const {
-    if (key == kLowest) return 0.0;
-    const float x = value_of(key);
+  __device__ __forceinline__ double weight(float x) const {
     if (x == most) return 1.0;
+    if (!(most - x <= far) || x == -__builtin_inff()) return 0.0;  // (a NaN, and whatever lies beside an infinity)
     return power_of_two((static_cast<double>(x) - static_cast<double>(most)) * per);
   }
-  __device__ __forceinline__ uint64_t whole(double w) const { return static_cast<uint64_t>(rint(ldexp(w, shift))); }
+  // round(2^S w), w <= 1: the low bits of 2^52 + 2^S w
+  __device__ __forceinline__ unsigned long long whole(double w) const {
+    return __double_as_longlong(ldexp(w, shift) + 0x1p52) & 0xFFFFFFFFFFFFFull;
+  }
+  // -1: no token that could come
+  __device__ __forceinline__ int bin(float x) const {
+    if (x == most) return 0;
+    const float d = most - x;
+    return d <= far && x > -__builtin_inff() ? static_cast<int>(fminf(d * bins, kBins - 1.0f)) : -1;
+  }
 };
 
+// the order of tokens: lower numbers first
+__device__ __forceinline__ unsigned long long place_of(float x, int i) {
+  return static_cast<unsigned long long>(~key_of(x)) << 32 | static_cast<uint32_t>(i);
+}
 
-struct Shared {
-  uint32_t count[2048];
-  unsigned long long weight[2048];
-  unsigned long long tile[kMaxTiles];
-  unsigned long long part[kThreads / kWave];
-  uint32_t most;
-  uint32_t prefix;
+// ------------------------------------------------------------------------ the workspace
+
+struct Plan {  // of a row with a filter, from gather to choose
+  int32_t looked;   // the list is not made
+  int32_t count;    // tokens in the list
+  int32_t top;      // the bin of top_k's border (kBins: none), and how many tokens of it stay
+  uint32_t stay;
+  int32_t from, to;  // the bins between which top_p's border lies (none: from > to)
+  unsigned long long whole;   // the weight of the bins before `top`
+  unsigned long long before;  // the weight of the bins before `from`
+};
+
+struct Space {
+  uint2* ends;                 // [rows][tiles] largest and least key
+  unsigned long long* sums;    // [rows][tiles]
+  unsigned long long* weights; // [rows][kBins]
+  uint32_t* counts;            // [rows][kBins]
+  uint32_t* listed;            // [rows]
+  Plan* plans;                 // [rows]
+  uint32_t* list;              // [rows][kList]
+};
+
+struct Call {
+  SampleArgs a;
+  Space w;
+  int tiles;   // of a row
+  int groups;  // workgroups a row in weigh and gather
+  int shift;
+  int first;   // the launch's first row
+};
+
+__device__ __forceinline__ unsigned long long wave_sum(unsigned long long v) {
+#pragma unroll
+  for (int m = 1; m < kWave; m *= 2) v += __shfl_xor(v, m);
+  return v;
+}
+
+// Sum over the threads up to each one; `all` gets the sum of all.
+struct Scan {
+  unsigned long long part[2][kWaves];
+  int turn;
+};
+__device__ __forceinline__ unsigned long long scan(unsigned long long v, Scan& s, int& turn, unsigned long long& all) {
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+#pragma unroll
+  for (int m = 1; m < kWave; m *= 2) {
+    const unsigned long long o = __shfl_up(v, m);
+    if (lane >= m) v += o;
+  }
+  turn ^= 1;  // (the readers of the last turn's parts need not be done)
+  if (lane == kWave - 1) s.part[turn][w] = v;
+  __syncthreads();
+  all = 0;
+  unsigned long long before = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    if (i == w) before = all;
+    all += s.part[turn][i];
+  }
+  return v + before;
+}
+
+// The row's largest and least values, and what its parameters ask for. Every thread gets it.
+__device__ Row row_of(const Call& c, int r, uint32_t (&part)[2][kWaves]) {
+  uint32_t most = 0, least = 0xFFFFFFFFu;
+  const uint2* e = c.w.ends + static_cast<int64_t>(r) * c.tiles;
+  for (int t = threadIdx.x; t < c.tiles; t += kThreads) {
+    const uint2 x = e[t];
+    most = max(most, x.x);
+    least = min(least, x.y);
+  }
+#pragma unroll
+  for (int m = 1; m < kWave; m *= 2) {
+    most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), m)));
+    least = min(least, static_cast<uint32_t>(__shfl_xor(static_cast<int>(least), m)));
+  }
+  if (threadIdx.x % kWave == 0) {
+    part[0][threadIdx.x / kWave] = most;
+    part[1][threadIdx.x / kWave] = least;
+  }
+  __syncthreads();
+#pragma unroll
+  for (int w = 0; w < kWaves; ++w) {
+    most = max(most, part[0][w]);
+    least = min(least, part[1][w]);
+  }
+  Row row;
+  row.most = value_of(most);
+  const float t = c.a.temperature ? c.a.temperature[r] : 1.0f;
+  row.per = 1.44269504088896340736 / static_cast<double>(t);
+  row.shift = c.shift;
+  row.far = row.most < __builtin_inff() ? static_cast<float>((c.shift + 1.5) / row.per) : -1.f;  // (infinite T: all finite distances)
+  const float range = fminf(row.most - value_of(least), row.far);
+  row.bins = range > 0.f ? fminf(static_cast<float>(kBins) / range, 1e30f) : 0.f;
+  const float min_p = c.a.min_p ? c.a.min_p[r] : 0.f;
+  row.least = min_p > 0.f ? (min_p < 1.f ? min_p : 1.0) : 0.0;
+  row.k = c.a.top_k ? c.a.top_k[r] : 0;
+  if (row.k < 0 || row.k >= c.a.vocab) row.k = 0;
+  const float p = c.a.top_p ? c.a.top_p[r] : 1.f;
+  row.p = p < 1.f ? p : 1.f;
+  row.mode = most <= kLowest ? kNone : !(t > 0.f) ? kLikeliest : row.k == 0 && row.p == 1.f ? kPlain : kListed;
+  return row;
+}
+
+// -------------------------------------------------------------------------- extremes
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void sample_extremes_kernel(Call c) {
+  const int blocks = (c.tiles + kWaves - 1) / kWaves;
+  const int r = c.first + blockIdx.x / blocks, b = blockIdx.x % blocks;
+  const int lane = threadIdx.x & (kWave - 1), t = b * kWaves + threadIdx.x / kWave;
+  if (c.w.counts && b == 0) {  // the row's bins and list begin empty
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+      c.w.counts[static_cast<int64_t>(r) * kBins + i] = 0;
+      c.w.weights[static_cast<int64_t>(r) * kBins + i] = 0;
+    }
+    if (threadIdx.x == 0) c.w.listed[r] = 0;
+  }
+  if (t >= c.tiles) return;
+  const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
+  uint32_t most = kLowest, least = 0xFFFFFFFFu;
+  float v[kRounds][8];
+#pragma unroll
+  for (int n = 0; n < kRounds; ++n) load8(x, t * kTile + 8 * (n * kWave + lane), c.a.vocab, v[n]);
+#pragma unroll
+  for (int n = 0; n < kRounds; ++n)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const uint32_t k = key_of(v[n][e]);
+      most = max(most, k);
+      least = min(least, k > kLowest ? k : 0xFFFFFFFFu);
+    }
+#pragma unroll
+  for (int m = 1; m < kWave; m *= 2) {
+    most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), m)));
+    least = min(least, static_cast<uint32_t>(__shfl_xor(static_cast<int>(least), m)));
+  }
+  if (lane == 0) c.w.ends[static_cast<int64_t>(r) * c.tiles + t] = uint2{most, least};
+}
+
+// ------------------------------------------------------------------------------ weigh
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void sample_weigh_kernel(Call c) {
+  __shared__ unsigned long long weights[kBins];
+  __shared__ uint32_t counts[kBins];
+  __shared__ uint32_t part[2][kWaves];
+  const int r = c.first + blockIdx.x / c.groups, g = blockIdx.x % c.groups;
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  const Row row = row_of(c, r, part);
+  if (row.mode < kPlain) return;
+  const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
+  const bool plain = row.mode == kPlain;
+  if (!plain) {
+    for (int i = threadIdx.x; i < kBins; i += kThreads) {
+      weights[i] = 0;
+      counts[i] = 0;
+    }
+    __syncthreads();
+  }
+  for (int t = g * kWaves + w; t < c.tiles; t += c.groups * kWaves) {
+    unsigned long long sum = 0;
+    for (int n = 0; n < kRounds; ++n) {
+      float v[8];
+      load8(x, t * kTile + 8 * (n * kWave + lane), c.a.vocab, v);
+      if (plain) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const double f = row.weight(v[e]);
+          sum += f < row.least ? 0 : row.whole(f);
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+          const int b = row.bin(v[e]);
+          if (b < 0) continue;
+          atomicAdd(&counts[b], 1u);
+          atomicAdd(&weights[b], row.whole(row.weight(v[e])));
+        }
+      }
+    }
+    if (plain) {
+      sum = wave_sum(sum);
+      if (lane == 0) c.w.sums[static_cast<int64_t>(r) * c.tiles + t] = sum;
+    }
+  }
+  if (plain) return;
+  __syncthreads();
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    if (counts[i]) atomicAdd(&c.w.counts[static_cast<int64_t>(r) * kBins + i], counts[i]);
+    if (weights[i]) atomicAdd(&c.w.weights[static_cast<int64_t>(r) * kBins + i], weights[i]);
+  }
+}
+
+// ----------------------------------------------------------------------------- gather
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void sample_gather_kernel(Call c) {
+  static_assert(kBins == 2 * kThreads, "two bins a thread");
+  __shared__ Scan parts;
+  __shared__ uint32_t part[2][kWaves];
+  __shared__ int top_at, from_at, to_at;
+  __shared__ unsigned long long whole_at, before_at;
+  __shared__ uint32_t stay_at;
+  const int r = c.first + blockIdx.x / c.groups, g = blockIdx.x % c.groups;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
+  const Row row = row_of(c, r, part);
+  if (row.mode != kListed) return;
+  int turn = 0;
+  // the bins' counts and weights, and those of all bins before them
+  unsigned long long n2[2], w2[2], nb[2], wb[2], all_n, all_w;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    n2[e] = c.w.counts[static_cast<int64_t>(r) * kBins + 2 * tid + e];
+    w2[e] = c.w.weights[static_cast<int64_t>(r) * kBins + 2 * tid + e];
+  }
+  nb[0] = scan(n2[0] + n2[1], parts, turn, all_n) - n2[0] - n2[1];
+  wb[0] = scan(w2[0] + w2[1], parts, turn, all_w) - w2[0] - w2[1];
+  nb[1] = nb[0] + n2[0];
+  wb[1] = wb[0] + w2[0];
+  if (tid == 0) {
+    top_at = kBins;
+    whole_at = all_w;
+    stay_at = 0;
+    from_at = to_at = 0;
+    before_at = 0;
+  }
+  __syncthreads();
+  const bool by_count = row.k > 0 && static_cast<unsigned long long>(row.k) < all_n;
+  if (by_count) {
+#pragma unroll
+    for (int e = 0; e < 2; ++e)
+      if (nb[e] < static_cast<unsigned>(row.k) && static_cast<unsigned>(row.k) <= nb[e] + n2[e]) {
+        top_at = 2 * tid + e;
+        stay_at = static_cast<uint32_t>(row.k - nb[e]);
+        whole_at = wb[e];
+      }
+  }
+  __syncthreads();
+  const int top = top_at;
+  unsigned long long most_w = whole_at;  // (of the bin of top_k's border a part stays)
+  if (by_count) most_w += c.w.weights[static_cast<int64_t>(r) * kBins + top];
+  const bool by_weight = row.p < 1.f;
+  if (by_weight) {
+    const double low = static_cast<double>(row.p) * static_cast<double>(whole_at);
+    const double high = static_cast<double>(row.p) * static_cast<double>(most_w);
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const int b = 2 * tid + e;
+      if (n2[e] == 0 || b > top) continue;
+      if (static_cast<double>(wb[e]) < low) atomicMax(&from_at, b);
+      if (static_cast<double>(wb[e]) < high) atomicMax(&to_at, b);
+    }
+  }
+  __syncthreads();
+  const int from = by_weight ? from_at : kBins, to = by_weight ? to_at : -1;
+  const int sure = by_weight ? from : top;  // bins before this one stay
+#pragma unroll
+  for (int e = 0; e < 2; ++e)
+    if (by_weight && 2 * tid + e == from) before_at = wb[e];
+  unsigned long long mine = 0, listed;
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    const int b = 2 * tid + e;
+    if ((b >= from && b <= to) || b == top) mine += n2[e];
+  }
+  scan(mine, parts, turn, listed);
+  const bool looked = listed > kList;
+  if (g == 0 && tid == 0)
+    c.w.plans[r] = Plan{looked, static_cast<int32_t>(looked ? 0 : listed), top, stay_at, from, to, whole_at, before_at};
+  if (looked) return;
+  const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
+  for (int t = g * kWaves + w; t < c.tiles; t += c.groups * kWaves) {
+    unsigned long long sum = 0;
+    for (int n = 0; n < kRounds; ++n) {
+      float v[8];
+      const int i0 = t * kTile + 8 * (n * kWave + lane);
+      load8(x, i0, c.a.vocab, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int b = row.bin(v[e]);
+        if (b >= 0 && b < sure) {
+          const double f = row.weight(v[e]);
+          sum += f < row.least ? 0 : row.whole(f);
+        }
+        const bool in = (b >= from && b <= to) || b == top;
+        const uint64_t mask = __ballot(in);
+        if (mask == 0) continue;
+        uint32_t at = 0;
+        if (lane == __builtin_ctzll(mask)) at = atomicAdd(&c.w.listed[r], static_cast<uint32_t>(__popcll(mask)));
+        at = __shfl(at, __builtin_ctzll(mask)) + __popcll(mask & ((1ull << lane) - 1));
+        if (in && at < kList) c.w.list[static_cast<int64_t>(r) * kList + at] = i0 + e;
+      }
+    }
+    sum = wave_sum(sum);
+    if (lane == 0) c.w.sums[static_cast<int64_t>(r) * c.tiles + t] = sum;
+  }
+}
+
+// ----------------------------------------------------------------------------- choose
+
+struct Choose {
+  union {
+    unsigned long long list[kList];
+    struct {  // the lookup
+      uint32_t count[2048];
+      unsigned long long weight[2048];
+    } look;
+  };
+  Scan parts;
+  uint32_t part[2][kWaves];
+  unsigned long long wide;
   uint32_t at;
-  unsigned long long before;
-  uint32_t found;
 };
 
 // Where a filter's order ends: every key above `key`, and of the equal ones the first `equal` by index.
@@ -88,58 +456,84 @@ struct Border {
 };
 
 // The border of the first `want` tokens (BY_COUNT), or of those before which less than `target` of weight lies, among the tokens
-// up to `limit`'s border. `total` gets the weight up to the border.
+// up to `limit`, from the row itself: counts or weights by the key's leading 11 bits, the next 11 inside the one found, the last 10.
 template <typename T, bool BY_COUNT>
-__device__ Border find(const T* x, int vocab, const Row& row, const Border& limit, uint32_t want, double target, Shared& sh) {
+__device__ Border look_up(const T* x, int vocab, const Row& row, const Border& limit, uint32_t want, double target, Choose& sh, int& turn) {
   const int tid = threadIdx.x;
-  uint32_t prefix = 0;         // the leading bits found so far
-  unsigned long long before = 0;  // count or weight of the keys above them
+  uint32_t prefix = 0;
+  unsigned long long before = 0;  // count or weight of the keys above those bits
+  uint32_t found = 0;
   int left = 32;
   for (int level = 0; level < 3; ++level) {
     const int bits = level == 2 ? 10 : 11, bins = 1 << bits, low = left - bits;
-    for (int b = tid; b < bins; b += kThreads) {
-      sh.count[b] = 0;
-      sh.weight[b] = 0;
-    }
     __syncthreads();
-    for (int i = tid; i < vocab; i += kThreads) {
-      const uint32_t key = key_of(x[i]);
-      if (key < limit.key || (level > 0 && (key >> left) != prefix)) continue;
-      const uint32_t b = (key >> low) & (bins - 1);
-      atomicAdd(&sh.count[b], 1u);
-      if (!BY_COUNT && key > limit.key) atomicAdd(&sh.weight[b], static_cast<unsigned long long>(row.whole(row.weight(key))));
+    for (int b = tid; b < 2048; b += kThreads) {
+      sh.look.count[b] = 0;
+      sh.look.weight[b] = 0;
     }
+    if (tid == 0) sh.wide = 0;
     __syncthreads();
-    if (tid == 0) {
-      if (!BY_COUNT && limit.key != 0 && (level == 0 || (limit.key >> left) == prefix)) {
-        const uint32_t b = (limit.key >> low) & (bins - 1);
-        sh.weight[b] += limit.equal * static_cast<unsigned long long>(row.whole(row.weight(limit.key)));
+    for (int i0 = 8 * tid; i0 < vocab; i0 += 8 * kThreads) {
+      float v[8];
+      load8(x, i0, vocab, v);
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        if (row.bin(v[e]) < 0) continue;
+        const uint32_t key = key_of(v[e]);
+        if (key < limit.key || (level > 0 && (key >> left) != prefix)) continue;
+        const uint32_t b = (key >> low) & (bins - 1);
+        atomicAdd(&sh.look.count[b], 1u);
+        if (!BY_COUNT && key > limit.key) atomicAdd(&sh.look.weight[b], row.whole(row.weight(v[e])));
       }
-      int at = -1;
-      unsigned long long sum = before, sum_at = before;
-      for (int b = bins - 1; b >= 0; --b) {
-        if (sh.count[b] == 0) continue;
-        if (at >= 0 && (BY_COUNT ? sum >= want : static_cast<double>(sum) >= target)) break;
-        at = b;
-        sum_at = sum;
-        sum += BY_COUNT ? sh.count[b] : sh.weight[b];
-      }
-      sh.at = at;
-      sh.before = sum_at;
-      sh.found = sh.count[at];
     }
     __syncthreads();
-    prefix = level == 0 ? sh.at : (prefix << bits) | sh.at;
-    before = sh.before;
+    if (!BY_COUNT && tid == 0 && limit.key != 0 && (level == 0 || (limit.key >> left) == prefix))
+      sh.look.weight[(limit.key >> low) & (bins - 1)] += limit.equal * row.whole(row.weight(value_of(limit.key)));
+    __syncthreads();
+    // four bins a thread, from the highest; the last with anything in it before which too little lies
+    unsigned long long n[4], sum = 0, all;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int b = bins - 1 - (4 * tid + e);
+      n[e] = b < 0 ? 0 : BY_COUNT ? sh.look.count[b] : sh.look.weight[b];
+      sum += n[e];
+    }
+    unsigned long long at = before + scan(sum, sh.parts, turn, all) - sum;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      const int b = bins - 1 - (4 * tid + e);
+      // (bins lie below 2^11, so a later one is a larger number: its place from the top, plus one)
+      if (b >= 0 && sh.look.count[b] && (BY_COUNT ? at < want : static_cast<double>(at) < target)) atomicMax(&sh.wide, bins - static_cast<unsigned long long>(b));
+      at += n[e];
+    }
+    __syncthreads();
+    if (sh.wide == 0) {  // (a target of 0: the first of all)
+      __syncthreads();
+#pragma unroll
+      for (int e = 3; e >= 0; --e) {
+        const int b = bins - 1 - (4 * tid + e);
+        if (b >= 0 && sh.look.count[b]) atomicMax(&sh.wide, 4096ull + b);
+      }
+      __syncthreads();
+    }
+    const unsigned long long hit = sh.wide;
+    const int b = static_cast<int>(hit >= 4096 ? hit - 4096 : bins - hit);
+    // what lies before it
+    unsigned long long above = 0;
+    for (int q = b + 1 + tid; q < bins; q += kThreads) above += BY_COUNT ? sh.look.count[q] : sh.look.weight[q];
+    scan(above, sh.parts, turn, all);
+    before += all;
+    found = sh.look.count[b];
+    prefix = level == 0 ? b : (prefix << bits) | b;
     left = low;
-    __syncthreads();
   }
-  Border out{prefix, sh.found};
+  __syncthreads();
+  Border out{prefix, found};
   if (out.key == limit.key) out.equal = min(out.equal, limit.equal);
   if (BY_COUNT) {
     out.equal = min(out.equal, static_cast<uint32_t>(want - before));
   } else {
-    const unsigned long long w = row.whole(row.weight(out.key));
+    const unsigned long long w = row.whole(row.weight(value_of(out.key)));
     uint32_t lo = 1, hi = out.equal;  // the largest j with before + (j - 1) w < target, at least 1
     while (lo < hi) {
       const uint32_t mid = lo + (hi - lo + 1) / 2;
@@ -151,146 +545,292 @@ __device__ Border find(const T* x, int vocab, const Row& row, const Border& limi
   return out;
 }
 
+// The place of the last token up to a border: the equal-th in index order of those with its key.
 template <typename T>
-__global__ __launch_bounds__(kThreads) void sample_kernel(SampleArgs a, int shift) {
-  __shared__ Shared sh;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), r = blockIdx.x, vocab = a.vocab;
-  const T* x = static_cast<const T*>(a.logits) + r * a.stride;
-  if (tid == 0) sh.most = 0;
+__device__ unsigned long long last_place(const T* x, int vocab, const Border& b, Choose& sh, int& turn) {
+  unsigned long long seen = 0, all;
   __syncthreads();
-  uint32_t most = 0;
-  for (int i = tid; i < vocab; i += kThreads) most = max(most, key_of(x[i]));
-  atomicMax(&sh.most, most);
+  if (threadIdx.x == 0) sh.at = 0xFFFFFFFFu;
+  for (int i0 = 0; i0 < vocab; i0 += 8 * kThreads) {
+    const int i = i0 + 8 * threadIdx.x;
+    float v[8];
+    load8(x, i, vocab, v);
+    unsigned long long mine = 0;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) mine += i + e < vocab && key_of(v[e]) == b.key;
+    unsigned long long at = seen + scan(mine, sh.parts, turn, all) - mine;
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (i + e < vocab && key_of(v[e]) == b.key && ++at == b.equal) sh.at = i + e;
+    seen += all;
+    if (seen >= b.equal) break;
+  }
   __syncthreads();
-  most = sh.most;
-  if (most == kLowest) {
-    if (tid == 0) {
-      a.tokens[r] = -1;
-      if (a.prob) a.prob[r] = 0.f;
-    }
+  return static_cast<unsigned long long>(~b.key) << 32 | sh.at;
+}
+
+template <typename T>
+__global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
+  __shared__ Choose sh;
+  extern __shared__ unsigned long long tiles[];
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave, r = c.first + blockIdx.x, vocab = c.a.vocab;
+  const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
+  const Row row = row_of(c, r, sh.part);
+  const auto answer = [&](int token, float prob) {
+    c.a.tokens[r] = token;
+    if (c.a.prob) c.a.prob[r] = prob;
+  };
+  if (row.mode == kNone) {
+    if (tid == 0) answer(-1, 0.f);
     return;
   }
-  const float t = a.temperature ? a.temperature[r] : 1.0f;
-  if (tid == 0) sh.at = vocab;
-  __syncthreads();
-  if (!(t > 0.f)) {
-    for (int i = tid; i < vocab; i += kThreads)
-      if (key_of(x[i]) == most) {
-        atomicMin(&sh.at, static_cast<uint32_t>(i));
+  if (row.mode == kLikeliest) {
+    if (tid == 0) sh.at = 0xFFFFFFFFu;
+    __syncthreads();
+    const uint32_t most = key_of(row.most);
+    for (int t = tid; t < c.tiles; t += kThreads)
+      if (c.w.ends[static_cast<int64_t>(r) * c.tiles + t].x == most) {
+        atomicMin(&sh.at, static_cast<uint32_t>(t));
         break;
       }
     __syncthreads();
-    if (tid == 0) {
-      a.tokens[r] = sh.at;
-      if (a.prob) a.prob[r] = 1.f;
-    }
-    return;
-  }
-  Row row{value_of(most), 1.44269504088896340736 / static_cast<double>(t), 0.0, shift};
-  const float least = a.min_p ? a.min_p[r] : 0.f;
-  row.least = least > 0.f ? (least < 1.f ? least : 1.0) : 0.0;
-  const int32_t k = a.top_k ? a.top_k[r] : 0;
-  const float p = a.top_p ? a.top_p[r] : 1.f;
-  Border border{0, static_cast<uint32_t>(vocab)};
-  if (k > 0 && k < vocab) border = find<T, true>(x, vocab, row, border, k, 0.0, sh);
-  // the index behind which equal keys are out
-  const auto cut_of = [&](const Border& b) {
+    const int i0 = sh.at * kTile;
     __syncthreads();
     if (tid == 0) sh.at = 0xFFFFFFFFu;
-    uint32_t seen = 0;
-    for (int i0 = 0; i0 < vocab && b.key != 0; i0 += kThreads) {
-      const int i = i0 + tid;
-      const bool eq = i < vocab && key_of(x[i]) == b.key;
-      const uint64_t mask = __ballot(eq);
-      __syncthreads();
-      if (lane == 0) sh.part[tid / kWave] = __popcll(mask);
-      __syncthreads();
-      uint32_t mine = seen + __popcll(mask & ((1ull << lane) - 1));
-      for (int w = 0; w < kThreads / kWave; ++w) {
-        if (w < tid / kWave) mine += sh.part[w];
-        seen += sh.part[w];
-      }
-      if (eq && mine + 1 == b.equal) sh.at = i;
-      if (seen >= b.equal) break;
-    }
     __syncthreads();
-    return sh.at;
-  };
-  uint32_t cut = cut_of(border);
-  const auto weight = [&](int i, bool floor) -> uint64_t {
-    const uint32_t key = key_of(x[i]);
-    if (key < border.key || (key == border.key && static_cast<uint32_t>(i) > cut)) return 0;
-    const double w = row.weight(key);
-    return floor && w < row.least ? 0 : row.whole(w);
-  };
-  const auto sum_all = [&](bool floor) {
-    const int tiles = (vocab + kTile - 1) / kTile;
+    for (int i = i0 + tid; i < min(i0 + kTile, vocab); i += kThreads)
+      if (key_of(get(x + i)) == most) atomicMin(&sh.at, static_cast<uint32_t>(i));
     __syncthreads();
-    for (int i = tid; i < tiles; i += kThreads) sh.tile[i] = 0;
-    __syncthreads();
-    for (int n = 0; n < tiles; ++n) {
-      unsigned long long s = 0;
-      for (int i = n * kTile + tid; i < min(vocab, (n + 1) * kTile); i += kThreads) s += weight(i, floor);
-#pragma unroll
-      for (int m = 1; m < kWave; m *= 2) s += __shfl_xor(s, m);
-      if (lane == 0) atomicAdd(&sh.tile[n], s);
-    }
-    __syncthreads();
-    unsigned long long s = 0;
-    for (int n = 0; n < tiles; ++n) s += sh.tile[n];
-    return s;
-  };
-  if (p < 1.f) {
-    const double target = static_cast<double>(p) * static_cast<double>(sum_all(false));
-    __syncthreads();
-    border = find<T, false>(x, vocab, row, border, 0, target, sh);
-    cut = cut_of(border);
+    if (tid == 0) answer(sh.at, 1.f);
+    return;
   }
-  const unsigned long long total = sum_all(true);
-  const float u = fminf(fmaxf(a.uniform[r], 0.f), 0x1.fffffep-1f);
-  const double goal = static_cast<double>(u) * static_cast<double>(total);
-  int n = 0;
-  unsigned long long before = 0;
-  while (static_cast<double>(before + sh.tile[n]) <= goal) before += sh.tile[n++];
-  // the tile's tokens, 1024 at a time
-  for (int i0 = n * kTile;; i0 += kThreads) {
-    const int i = i0 + tid;
-    const unsigned long long w = i < vocab ? weight(i, true) : 0;
-    unsigned long long s = w;
+  int turn = 0;
+  unsigned long long end = ~0ull;  // the last kept token's place
+  const auto kept = [&](float v, int i) -> unsigned long long {
+    if (place_of(v, i) > end) return 0;
+    const double f = row.weight(v);
+    return f < row.least ? 0 : row.whole(f);
+  };
+  if (row.mode == kListed && c.w.plans[r].looked) {
+    Border border{0, 0xFFFFFFFFu};
+    if (row.k > 0) {
+      unsigned long long n = 0, all;
+      for (int i = tid; i < kBins; i += kThreads) n += c.w.counts[static_cast<int64_t>(r) * kBins + i];
+      scan(n, sh.parts, turn, all);
+      if (static_cast<unsigned long long>(row.k) < all) border = look_up<T, true>(x, vocab, row, border, row.k, 0.0, sh, turn);
+    }
+    if (row.p < 1.f) {
+      unsigned long long n = 0, all;
+      const bool cut = border.key != 0;
+      for (int i0 = 8 * tid; i0 < vocab; i0 += 8 * kThreads) {
+        float v[8];
+        load8(x, i0, vocab, v);
 #pragma unroll
-    for (int m = 1; m < kWave; m *= 2) {
-      const unsigned long long o = __shfl_up(s, m);
-      if (lane >= m) s += o;
+        for (int e = 0; e < 8; ++e)
+          if (!cut || key_of(v[e]) > border.key) n += row.whole(row.weight(v[e]));
+      }
+      scan(n, sh.parts, turn, all);
+      if (cut) all += border.equal * row.whole(row.weight(value_of(border.key)));
+      border = look_up<T, false>(x, vocab, row, border, 0, static_cast<double>(row.p) * static_cast<double>(all), sh, turn);
+    }
+    if (border.key != 0) end = last_place(x, vocab, border, sh, turn);
+    for (int t = w; t < c.tiles; t += kWaves) {
+      unsigned long long sum = 0;
+      for (int n = 0; n < kRounds; ++n) {
+        float v[8];
+        const int i0 = t * kTile + 8 * (n * kWave + lane);
+        load8(x, i0, vocab, v);
+#pragma unroll
+        for (int e = 0; e < 8; ++e) sum += kept(v[e], i0 + e);
+      }
+      sum = wave_sum(sum);
+      if (lane == 0) tiles[t] = sum;
     }
     __syncthreads();
-    if (lane == kWave - 1) sh.part[tid / kWave] = s;
-    __syncthreads();
-    unsigned long long all = 0;
-    s += before;
-    for (int v = 0; v < kThreads / kWave; ++v) {
-      if (v < tid / kWave) s += sh.part[v];
-      all += sh.part[v];
+  } else {
+    for (int t = tid; t < c.tiles; t += kThreads) tiles[t] = c.w.sums[static_cast<int64_t>(r) * c.tiles + t];
+    if (row.mode == kListed && c.w.plans[r].count > 0) {
+      const Plan plan = c.w.plans[r];
+      int size = 2;
+      while (size < plan.count) size *= 2;
+      for (int i = tid; i < size; i += kThreads) {
+        unsigned long long v = ~0ull;
+        if (i < plan.count) {
+          const int at = c.w.list[static_cast<int64_t>(r) * kList + i];
+          v = place_of(get(x + at), at);
+        }
+        sh.list[i] = v;
+      }
+      // sorted by exchanges between partners at falling distances, in runs of rising length
+      for (int run = 2; run <= size; run *= 2)
+        for (int d = run / 2; d > 0; d /= 2) {
+          __syncthreads();
+          for (int q = tid; q < size / 2; q += kThreads) {
+            const int i = 2 * q - (q & (d - 1)), j = i + d;
+            const unsigned long long a = sh.list[i], b = sh.list[j];
+            if ((a > b) == ((i & run) == 0)) {
+              sh.list[i] = b;
+              sh.list[j] = a;
+            }
+          }
+        }
+      __syncthreads();
+      // eight tokens a thread, in order
+      float v[8];
+      unsigned long long wt[8], at_top = 0, stays = 0, all;
+      int b[8];
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = 8 * tid + e;
+        b[e] = kBins + 1;
+        wt[e] = 0;
+        if (i < plan.count) {
+          v[e] = value_of(~static_cast<uint32_t>(sh.list[i] >> 32));
+          b[e] = row.bin(v[e]);
+          wt[e] = row.whole(row.weight(v[e]));
+          at_top += b[e] < plan.top;
+        }
+      }
+      scan(at_top, sh.parts, turn, all);
+      const int stay_end = plan.top < kBins ? static_cast<int>(all) + static_cast<int>(plan.stay) : kBins + kList;
+      // (the tokens of top_k's bin come last in the list: those up to stay_end are its)
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (b[e] == plan.top && 8 * tid + e < stay_end) stays += wt[e];
+      scan(stays, sh.parts, turn, all);
+      const double target = static_cast<double>(row.p) * static_cast<double>(plan.whole + all);
+      const bool by_weight = plan.from <= plan.to;
+      unsigned long long mine = 0;
+#pragma unroll
+      for (int e = 0; e < 8; ++e)
+        if (b[e] <= plan.to) mine += wt[e];
+      unsigned long long before = plan.before + scan(mine, sh.parts, turn, all) - mine;
+      int last = -1;
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int i = 8 * tid + e;
+        const bool stay = i < plan.count && i < stay_end &&
+                          (!by_weight || (b[e] <= plan.to && (static_cast<double>(before) < target || (i == 0 && plan.from == 0))));
+        if (b[e] <= plan.to) before += wt[e];
+        if (!stay) continue;
+        last = i;
+        if (!(row.weight(v[e]) < row.least)) atomicAdd(&tiles[static_cast<uint32_t>(sh.list[i]) / kTile], wt[e]);
+      }
+      if (tid == 0) sh.at = 0;
+      __syncthreads();
+      if (last >= 0) atomicMax(&sh.at, static_cast<uint32_t>(last));
+      __syncthreads();
+      end = sh.list[sh.at];
     }
-    if (w != 0 && static_cast<double>(s) > goal && static_cast<double>(s - w) <= goal) {
-      a.tokens[r] = i;
-      if (a.prob) a.prob[r] = static_cast<float>(row.weight(key_of(x[i])) / ldexp(static_cast<double>(total), -shift));
+    __syncthreads();
+  }
+  // the tile in which the weight passes the goal
+  unsigned long long total = 0, all, before = 0;
+  for (int t = tid; t < c.tiles; t += kThreads) total += tiles[t];
+  scan(total, sh.parts, turn, all);
+  total = all;
+  const float u = fminf(fmaxf(c.a.uniform[r], 0.f), 0x1.fffffep-1f);
+  const double goal = static_cast<double>(u) * static_cast<double>(total);
+  for (int t0 = 0;; t0 += kThreads) {
+    const unsigned long long s = t0 + tid < c.tiles ? tiles[t0 + tid] : 0;
+    const unsigned long long upto = before + scan(s, sh.parts, turn, all);
+    if (s != 0 && static_cast<double>(upto) > goal && static_cast<double>(upto - s) <= goal) {
+      sh.at = t0 + tid;
+      sh.wide = upto - s;
     }
     before += all;
-    if (static_cast<double>(before) > goal || i0 + kThreads >= vocab) break;
+    if (static_cast<double>(before) > goal || t0 + kThreads >= c.tiles) break;
   }
+  __syncthreads();
+  // and the token in it
+  static_assert(kTile == 2 * kThreads, "two tokens a thread");
+  const int i = sh.at * kTile + 2 * tid;
+  float v[2];
+  unsigned long long k[2];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    v[e] = i + e < vocab ? get(x + i + e) : -__builtin_inff();
+    k[e] = i + e < vocab ? kept(v[e], i + e) : 0;
+  }
+  unsigned long long upto = sh.wide + scan(k[0] + k[1], sh.parts, turn, all) - k[0] - k[1];
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    upto += k[e];
+    if (k[e] != 0 && static_cast<double>(upto) > goal && static_cast<double>(upto - k[e]) <= goal)
+      answer(i + e, static_cast<float>(row.weight(v[e]) / ldexp(static_cast<double>(total), -row.shift)));
+  }
+}
+
+// ------------------------------------------------------------------------------ launch
+
+struct Sizes {
+  int tiles;
+  size_t ends, sums, weights, counts, listed, plans, list, bytes;
+};
+Sizes sizes(int32_t rows, int32_t vocab) {
+  Sizes z{};
+  z.tiles = (vocab + kTile - 1) / kTile;
+  size_t at = 0;
+  const auto room = [&](size_t& from, size_t bytes) {
+    from = at;
+    at += (bytes + 255) & ~static_cast<size_t>(255);
+  };
+  const size_t r = rows;
+  room(z.ends, r * z.tiles * sizeof(uint2));
+  room(z.sums, r * z.tiles * 8);
+  room(z.weights, r * kBins * 8);
+  room(z.counts, r * kBins * 4);
+  room(z.listed, r * 4);
+  room(z.plans, r * sizeof(Plan));
+  room(z.list, r * kList * 4);
+  z.bytes = at;
+  return z;
+}
+
+template <typename T>
+hipError_t launch_t(Call c, bool filters, hipStream_t s) {
+  const int blocks = (c.tiles + kWaves - 1) / kWaves;
+  const int64_t most = (int64_t{1} << 31) / kThreads / blocks;  // rows of a launch
+  const int rows = c.a.rows;
+  const size_t lds = static_cast<size_t>(c.tiles) * 8;
+  for (int64_t f = 0; f < rows; f += most) {
+    c.first = static_cast<int>(f);
+    const unsigned n = static_cast<unsigned>(rows - f < most ? rows - f : most);
+    sample_extremes_kernel<T><<<n * blocks, kThreads, 0, s>>>(c);
+    sample_weigh_kernel<T><<<n * c.groups, kThreads, 0, s>>>(c);
+    if (filters) sample_gather_kernel<T><<<n * c.groups, kThreads, 0, s>>>(c);
+    sample_choose_kernel<T><<<n, kThreads, lds, s>>>(c);
+    if (const hipError_t e = hipGetLastError()) return e;
+  }
+  return hipSuccess;
 }
 
 }  // namespace
 
-size_t sample_workspace_bytes(int32_t, int32_t) { return 0; }
+size_t sample_workspace_bytes(int32_t rows, int32_t vocab) { return sizes(rows, vocab).bytes; }
 
 hipError_t launch_sample(const SampleArgs& a, hipStream_t s) {
+  const Sizes z = sizes(a.rows, a.vocab);
+  char* ws = static_cast<char*>(a.workspace);
+  const bool filters = a.top_k || a.top_p;
+  Call c{};
+  c.a = a;
+  c.w = Space{reinterpret_cast<uint2*>(ws + z.ends),
+              reinterpret_cast<unsigned long long*>(ws + z.sums),
+              reinterpret_cast<unsigned long long*>(ws + z.weights),
+              filters ? reinterpret_cast<uint32_t*>(ws + z.counts) : nullptr,
+              reinterpret_cast<uint32_t*>(ws + z.listed),
+              reinterpret_cast<Plan*>(ws + z.plans),
+              reinterpret_cast<uint32_t*>(ws + z.list)};
+  c.tiles = z.tiles;
   int bits = 0;
   while ((1 << bits) < a.vocab) ++bits;
-  const int shift = 62 - bits < 52 ? 62 - bits : 52;
-  if (a.bf16) sample_kernel<uint16_t><<<static_cast<unsigned>(a.rows), kThreads, 0, s>>>(a, shift);
-  else sample_kernel<float><<<static_cast<unsigned>(a.rows), kThreads, 0, s>>>(a, shift);
-  return hipGetLastError();
+  c.shift = 62 - bits < 51 ? 62 - bits : 51;
+  // about four workgroups a CU in the passes that add up a row's bins
+  const int blocks = (z.tiles + kWaves - 1) / kWaves;
+  const int want = (1024 + a.rows - 1) / a.rows;
+  c.groups = want < blocks ? want : blocks;
+  return a.bf16 ? launch_t<uint16_t>(c, filters, s) : launch_t<float>(c, filters, s);
 }
 
 }  // namespace gdn

@@ -1,7 +1,7 @@
 """gdn_sample against its definition in 64 bits (tests/sample_ref.py): tokens equal, probabilities within 2^-23.
 
-Weights are multiples of 2^-S of the largest, S >= 38 (44 for 2^18 tokens): a border between two tokens lies off by at most
-vocab 2^-(S+1) of the largest weight, under 2^-25 of the sum at S = 62 - log2(vocab). A test whose random number falls nearer
+Weights are multiples of 2^-S of the largest, S >= 41 (44 for 2^18 tokens): a border between two tokens lies off by at most
+vocab 2^-(S+1) of the largest weight, under 2^-25 of the sum for vocabularies up to 2^18 (S = 62 - log2(vocab)). A test whose random number falls nearer
 than that to a border of its distribution would prove nothing; the fixed seeds have none (asserted)."""
 
 import numpy as np
@@ -171,6 +171,13 @@ def test_offsets_past_32_bits():
     x = base.as_strided((rows, 1000), (stride, 1))
     x.copy_(logits(rows, 1000, "bf16", seed=10))
     check(x, numbers(rows, 13)["u"], k=[5, 50, 500])
+
+
+def test_the_largest_vocabulary():
+    announce("sample: 2^21 tokens")
+    x, n = logits(2, 1 << 21, seed=30, std=1.0), numbers(2, 31)
+    check(x, n["u"], t=n["t"], k=[0, 5000], p=n["p"])
+    check(x, n["u"])
 
 
 def test_the_frequencies_are_the_probabilities():
