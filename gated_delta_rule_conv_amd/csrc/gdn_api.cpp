@@ -734,6 +734,11 @@ gdn_status gdn_linear_prefill(const gdn_dims* dims, const void* q, int64_t q_str
   if (gdn_status st = linear_args(dims, fn, q, q_stride, k, k_stride, v, v_stride, g, g_stride, o, state_ptrs,
                                   total_tokens, &a))
     return st;
+  const int64_t esz = dims->in_dtype == GDN_BF16 ? 2 : 4, far = int64_t{1} << 24;
+  if (total_tokens > 1 && (q_stride * esz >= far || k_stride * esz >= far || v_stride * esz >= far || g_stride * 4 >= far))
+    return fail(GDN_ERR_UNSUPPORTED, "%s: rows 2^24 bytes or more apart not built (q %lld, k %lld, v %lld, g %lld elements)",
+                fn, static_cast<long long>(q_stride), static_cast<long long>(k_stride), static_cast<long long>(v_stride),
+                static_cast<long long>(g_stride));
   const size_t need =
       gdn::linear_workspace_bytes(dims->num_v_heads, dims->head_dim, num_seqs, total_tokens, dims->prefill_form);
   if (need > 0 && (!workspace || workspace_bytes < need))

@@ -1,6 +1,8 @@
 // Linear attention with a decay for each head, gfx950 (include/gdn.h, gdn_linear_prefill and
 // gdn_linear_decode): S_t = e^g_t S_{t-1} + v_t k_t^T, o_t = scale S_t q_t over the slots' fp32 states.
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "launch.h"
 #include "mma.h"
@@ -148,6 +150,13 @@ __device__ __forceinline__ void barrier_lds() {
   __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
 }
 
+// The same number, to be taken as another one each time: what is computed from it is not kept in registers over a
+// loop.
+__device__ __forceinline__ int fresh(int x) {
+  asm volatile("" : "+v"(x));
+  return x;
+}
+
 __device__ __forceinline__ float exp2_hw(float x) { return __builtin_amdgcn_exp2f(x); }
 
 // Sum over the wave's lanes up to each one.
@@ -201,6 +210,19 @@ struct Prod<uint16_t> {
     return Full{__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), __builtin_bit_cast(bf16x8, c)};
   }
   __device__ __forceinline__ static float value(const Exact& x, int e) { return static_cast<float>(x[e]); }
+  __device__ __forceinline__ static void clear(Exact& x, int e) { x[e] = static_cast<__bf16>(0.f); }
+  // whether one of them is an infinity or a NaN
+  __device__ __forceinline__ static bool odd(const Exact& x) {
+    const u32x4 y = __builtin_bit_cast(u32x4, x);
+    uint32_t o = 0;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) o |= (y[e] & 0x7F807F80u) + 0x00800080u;
+    return (o & 0x80008000u) != 0;
+  }
+  __device__ __forceinline__ static Full load(const uint16_t* p, int plane) {
+    return Full{*reinterpret_cast<const bf16x8*>(p), *reinterpret_cast<const bf16x8*>(p + plane),
+                *reinterpret_cast<const bf16x8*>(p + 2 * plane)};
+  }
   __device__ __forceinline__ static f32x4 exact(const Exact& a, const Exact& b, const f32x4& acc) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
   }
@@ -222,6 +244,12 @@ struct Prod<float> {
   typedef f32x4 Full;
   __device__ __forceinline__ static Full full(const float (&x)[4]) { return f32x4{x[0], x[1], x[2], x[3]}; }
   __device__ __forceinline__ static float value(const Exact& x, int e) { return x[e]; }
+  __device__ __forceinline__ static void clear(Exact& x, int e) { x[e] = 0.f; }
+  __device__ __forceinline__ static bool odd(const Exact& x) {
+    return !(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))) < __builtin_inff()) || x[0] != x[0] ||
+           x[1] != x[1] || x[2] != x[2] || x[3] != x[3];
+  }
+  __device__ __forceinline__ static Full load(const float* p, int) { return *reinterpret_cast<const f32x4*>(p); }
   __device__ __forceinline__ static f32x4 exact(const Exact& a, const Exact& b, f32x4 acc) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
@@ -376,10 +404,9 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
   __shared__ __attribute__((aligned(16))) T vl[kChunk * PITCH];
   __shared__ __attribute__((aligned(16))) T ql[OUT ? kChunk * PITCH : 16];
   __shared__ __attribute__((aligned(16))) T pl[OUT ? C::PLANES * kChunk * PROWS : 16];
-  __shared__ __attribute__((aligned(16))) float gl[4][kChunk];  // G's multiple of 2^-8, its rest, e^G_i, e^(G_n - G_i)
-  __shared__ int broken[2];
+  __shared__ __attribute__((aligned(16))) float gl[4][kChunk];  // G's multiple of 2^-8, its rest, scale e^G_i, e^(G_n - G_i)
   const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int l16 = lane & 15, h4 = 4 * (lane >> 4);
+  int l16 = lane & 15, h = lane >> 4, h4 = 4 * h;
   const int b = blockIdx.x % a.hv, tile = p.first + blockIdx.x / a.hv;
   // workgroups go round-robin to the 8 XCDs: neighbouring heads, which share k and q, to one of them
   const int j = a.hv % 8 == 0 ? (b % 8) * (a.hv / 8) + b / 8 : b;
@@ -394,7 +421,7 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
   const bool last = hi - lo <= (at.part + 1) * static_cast<int64_t>(p.tokens);
   if (!OUT && last) return;  // (no tile follows)
   const int start = lo + at.part * p.tokens, end = last ? hi : start + p.tokens;
-  const int h = j / a.group;
+  const int kh = j / a.group;
   const int64_t head = static_cast<int64_t>(j) * D * D;
   float* own = reinterpret_cast<float*>(sp) + head;
   float* room = at.slot < 0 ? nullptr : p.states + static_cast<int64_t>(at.slot) * a.hv * D * D + head;
@@ -426,43 +453,41 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
   // --- a chunk's rows into registers, then into LDS
   u32x4 kr[C::PIECES], vr[C::PIECES], qr[OUT ? C::PIECES : 1];
   float gr = 0.f;
-  const int row0 = tid / C::PPR, piece = tid % C::PPR;
+  int row0 = tid / C::PPR, piece = tid % C::PPR;
   constexpr int ROWS_UP = C::THREADS / C::PPR;
-  const T* kb = static_cast<const T*>(a.k) + h * D + piece * C::EPP;
-  const T* qb = static_cast<const T*>(a.q) + h * D + piece * C::EPP;
-  const T* vb = static_cast<const T*>(a.v) + static_cast<int64_t>(j) * D + piece * C::EPP;
-  const auto load = [&](int t, int len) {
-#pragma unroll
-    for (int u = 0; u < C::PIECES; ++u) {
-      const int64_t r = t + min(row0 + u * ROWS_UP, len - 1);
-      kr[u] = *reinterpret_cast<const u32x4*>(kb + r * a.k_stride);
-      vr[u] = *reinterpret_cast<const u32x4*>(vb + r * a.v_stride);
-      if constexpr (OUT) qr[u] = *reinterpret_cast<const u32x4*>(qb + r * a.q_stride);
-    }
-    if (w == 0) gr = lane < len ? a.g[(t + static_cast<int64_t>(lane)) * a.g_stride + j] : 0.f;
+  typedef __attribute__((address_space(1))) const char gchar;
+  typedef __attribute__((address_space(1))) const u32x4 gu32x4;
+  typedef __attribute__((address_space(1))) const float gfloat;
+  // (rows of a chunk at 32-bit offsets from its first: strides are below 2^24 bytes)
+  gchar* kb = (gchar*)(static_cast<const T*>(a.k) + kh * D);
+  gchar* qb = (gchar*)(static_cast<const T*>(a.q) + kh * D);
+  gchar* vb = (gchar*)(static_cast<const T*>(a.v) + static_cast<int64_t>(j) * D);
+  const int ks = static_cast<int>(a.k_stride * sizeof(T)), qs = static_cast<int>(a.q_stride * sizeof(T)),
+            vs = static_cast<int>(a.v_stride * sizeof(T)), gs = static_cast<int>(a.g_stride * 4);
+  gchar *kt = kb, *vt = vb, *qt = qb;
+  int rows_there = 0;
+  const auto aim = [&](int t, int len) {  // the next loads are of the chunk at t
+    kt = kb + static_cast<int64_t>(t) * ks;
+    vt = vb + static_cast<int64_t>(t) * vs;
+    qt = qb + static_cast<int64_t>(t) * qs;
+    rows_there = len - 1;
+    gr = *(gfloat*)((gchar*)(a.g + t * a.g_stride + j) + __umul24(min(lane, len - 1), gs));
   };
-  // whether a value of 16 bytes is an infinity or a NaN
-  const auto odd = [](const u32x4& x) {
-    uint32_t o = 0;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      if constexpr (sizeof(T) == 2) o |= ((x[e] & 0x7F807F80u) + 0x00800080u) & 0x80008000u;
-      else o |= ((x[e] & 0x7F800000u) + 0x00800000u) & 0x80000000u;
-    }
-    return o != 0;
+  const auto load = [&](int u) {
+    const uint32_t r = min(row0 + u * ROWS_UP, rows_there);
+    kr[u] = *(gu32x4*)(kt + (__umul24(r, ks) + piece * 16));
+    vr[u] = *(gu32x4*)(vt + (__umul24(r, vs) + piece * 16));
+    if constexpr (OUT) qr[u] = *(gu32x4*)(qt + (__umul24(r, qs) + piece * 16));
   };
   float total_hi = 0.f, total_lo = 0.f;
-  const auto stage = [&](int len, int turn) {
-    bool any = false;
+  const auto put_rows = [&](auto whole, int len) {
 #pragma unroll
     for (int u = 0; u < C::PIECES; ++u) {
       const int r = row0 + u * ROWS_UP;
-      const bool there = r < len;
+      const bool there = decltype(whole)::value || r < len;
       const u32x4 zero = {0, 0, 0, 0};
-      const u32x4 k = there ? kr[u] : zero, v = there ? vr[u] : zero;
-      any |= odd(k) || odd(v);
-      *reinterpret_cast<u32x4*>(kl + r * PITCH + piece * C::EPP) = k;
-      *reinterpret_cast<u32x4*>(vl + r * PITCH + piece * C::EPP) = v;
+      *reinterpret_cast<u32x4*>(kl + r * PITCH + piece * C::EPP) = there ? kr[u] : zero;
+      *reinterpret_cast<u32x4*>(vl + r * PITCH + piece * C::EPP) = there ? vr[u] : zero;
       if constexpr (OUT) {
         const u32x4 q = there ? qr[u] : zero;
         if constexpr (sizeof(T) == 2) {  // values 8 p .. + 7 of 32: h = 2 (p % 2) and the next, u = p / 2
@@ -474,16 +499,19 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
         }
       }
     }
-    if (any) broken[turn] = 1;
+  };
+  const auto stage = [&](int len) {
+    if (len == kChunk) put_rows(std::true_type{}, len);
+    else put_rows(std::false_type{}, len);
     if (w == 0) {
-      const float x = (gr < kForget ? kForget : gr) * kLog2e;  // (a NaN stays)
+      const float x = lane < len ? (gr < kForget ? kForget : gr) * kLog2e : 0.f;  // (a NaN stays)
       const float whole = rintf(x * 256.f) * 0x1p-8f;
       const float gh = wave_scan(whole), gt = wave_scan(x - whole);
       const float nh = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gh), kWave - 1));
       const float nt = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(gt), kWave - 1));
       gl[0][lane] = gh;
       gl[1][lane] = gt;
-      gl[2][lane] = exp2_hw(gh + gt);
+      gl[2][lane] = exp2_hw(gh + gt) * a.scale;
       gl[3][lane] = exp2_hw((nh - gh) + (nt - gt));
     }
   };
@@ -516,69 +544,84 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
   };
 
   f32x4 o[OUT ? 4 : 1][C::VT];  // o^T: rows d_v, columns tokens 16 i + l16
-  int o_at = 0, o_len = 0;
-  const auto store = [&]() {
+  const auto store = [&](int at, int len) {
     if constexpr (OUT) {
+      typedef __attribute__((address_space(1))) char gout;
+      typedef __attribute__((address_space(1))) f32x4 go4;
+      typedef __attribute__((address_space(1))) u32x2 go2;
+      gout* ob = (gout*)a.o + ((static_cast<int64_t>(at) * a.hv + j) * D + c0) * (a.o_bf16 ? 2 : 4);
+      const int mine = l16;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        if (16 * i + l16 >= o_len) continue;
-        const int64_t to = ((o_at + static_cast<int64_t>(16 * i + l16)) * a.hv + j) * D + c0 + h4;
+        if (16 * i + mine >= len) continue;
+        const uint32_t to = __umul24(16 * i + mine, a.hv * D) + h4;
 #pragma unroll
         for (int t = 0; t < C::VT; ++t) {
-          const f32x4 v = o[i][t] * a.scale;
+          const f32x4 v = o[i][t];
           if (a.o_bf16) {
             const u32x2 x = {static_cast<uint32_t>(to_bf16(v[0])) | static_cast<uint32_t>(to_bf16(v[1])) << 16,
                              static_cast<uint32_t>(to_bf16(v[2])) | static_cast<uint32_t>(to_bf16(v[3])) << 16};
-            *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(a.o) + to + 16 * t) = x;
+            *(go2*)(ob + (to + 16 * t) * 2) = x;
           } else {
-            *reinterpret_cast<f32x4*>(static_cast<float*>(a.o) + to + 16 * t) = v;
+            *(go4*)(ob + (to + 16 * t) * 4) = v;
           }
         }
       }
     }
   };
 
-  // A chunk with an infinity or a NaN in k or v is taken a token at a time: in a product with
-  // zeros it would reach the tokens before it.
-  int singly = start;  // tokens before this one
-  const auto span = [&](int t) { return t < singly ? 1 : min(kChunk, end - t); };
-  if (tid < 2) broken[tid] = 0;
-  load(start, span(start));
+  const auto span = [&](int t) { return min(kChunk, end - t); };
+  aim(start, span(start));
+#pragma unroll
+  for (int u = 0; u < C::PIECES; ++u) load(u);
   barrier_lds();
-  for (int t = start, turn = 0; t < end; turn ^= 1) {
+  for (int t = start; t < end;) {
     const int len = span(t);
-    stage(len, turn);
-    store();
+    // (addresses are formed anew in every chunk: kept over the loop they would cost the registers of two waves a SIMD)
+    l16 = fresh(l16);
+    h = fresh(h);
+    h4 = 4 * h;
+    row0 = fresh(row0);
+    piece = fresh(piece);
+    stage(len);
     barrier_lds();
-    const bool again = __builtin_amdgcn_readfirstlane(broken[turn]) != 0 && len > 1;
-    if (tid == 0) broken[turn ^ 1] = 0;  // (read before the last barrier, set behind the next)
-    if (again) {
-      singly = t + len;
-      o_len = 0;
-      load(t, 1);
-      barrier_lds();
-      continue;
-    }
-    if (t + len < end) load(t + len, span(t + len));
+    const bool more = t + len < end;
+    aim(more ? t + len : t, more ? span(t + len) : len);  // (loads without a branch: past the end, the same rows again)
     const float kept = exp2_hw(gl[0][kChunk - 1] + gl[1][kChunk - 1]);
     if constexpr (OUT) {
-      // scores of tokens j (rows) for tokens i (columns), 10 tiles on and below the diagonal
-      for (int x = w; x < 10; x += C::WAVES) {
-        const int ti = x >= 6 ? 3 : x >= 3 ? 2 : x >= 1 ? 1 : 0, tj = x - ti * (ti + 1) / 2;
-        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+      // scores of tokens j (rows) for tokens i (columns), 10 tiles on and below the diagonal, side by side
+      constexpr int SIDE = (10 + C::WAVES - 1) / C::WAVES;
+      f32x4 acc[SIDE];
+      int ti[SIDE], tj[SIDE];
 #pragma unroll
-        for (int st = 0; st < C::DS; ++st) acc = P::exact(k_row(16 * tj + l16, st), q_row(16 * ti + l16, st), acc);
-        const int i = 16 * ti + l16, j0 = 16 * tj + h4;
+      for (int y = 0; y < SIDE; ++y) {
+        const int x = min(w + y * C::WAVES, 9);
+        ti[y] = x >= 6 ? 3 : x >= 3 ? 2 : x >= 1 ? 1 : 0;
+        tj[y] = x - ti[y] * (ti[y] + 1) / 2;
+        acc[y] = f32x4{0.f, 0.f, 0.f, 0.f};
+      }
+#pragma unroll
+      for (int st = 0; st < C::DS; ++st)
+#pragma unroll
+        for (int y = 0; y < SIDE; ++y) acc[y] = P::exact(k_row(16 * tj[y] + l16, st), q_row(16 * ti[y] + l16, st), acc[y]);
+#pragma unroll
+      for (int y = 0; y < SIDE; ++y) {
+        const int i = 16 * ti[y] + l16, j0 = 16 * tj[y] + h4;
         const float gi = gl[0][i], ri = gl[1][i];
         const f32x4 gj = *reinterpret_cast<const f32x4*>(&gl[0][j0]), rj = *reinterpret_cast<const f32x4*>(&gl[1][j0]);
         float v[4];
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = j0 + r <= i ? acc[r] * exp2_hw((gi - gj[r]) + (ri - rj[r])) : 0.f;
+        for (int r = 0; r < 4; ++r) {
+          float x = acc[y][r] * (exp2_hw((gi - gj[r]) + (ri - rj[r])) * a.scale);
+          asm volatile("" : "+v"(x));  // (formed in every lane: a branch around it costs more)
+          v[r] = j0 + r <= i ? x : 0.f;
+        }
+        if (w + y * C::WAVES > 9) continue;
         if constexpr (sizeof(T) == 2) {
           uint32_t x3[3][4];
 #pragma unroll
           for (int r = 0; r < 4; ++r) P::thirds(v[r], x3[0][r], x3[1][r], x3[2][r]);
-          T* to = pl + i * PROWS + 32 * (tj / 2) + 2 * h4 + 4 * (tj % 2);
+          T* to = pl + i * PROWS + 32 * (tj[y] / 2) + 2 * h4 + 4 * (tj[y] % 2);
 #pragma unroll
           for (int z = 0; z < 3; ++z)
             *reinterpret_cast<u32x2*>(to + z * kChunk * PROWS) = u32x2{P::tops(x3[z][0], x3[z][1]), P::tops(x3[z][2], x3[z][3])};
@@ -586,13 +629,21 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
           *reinterpret_cast<f32x4*>(pl + i * PROWS + j0) = f32x4{v[0], v[1], v[2], v[3]};
         }
       }
-      // e^G_i S q_i
+      // e^G_i S q_i, the next chunk's loads between its steps
 #pragma unroll
       for (int i = 0; i < 4; ++i)
 #pragma unroll
         for (int t = 0; t < C::VT; ++t) o[i][t] = f32x4{0.f, 0.f, 0.f, 0.f};
+      Exact q[2][4];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) q[0][i] = q_row(16 * i + l16, 0);
 #pragma unroll
       for (int st = 0; st < C::DS; ++st) {
+        if (st + 1 < C::DS)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) q[(st + 1) % 2][i] = q_row(16 * i + l16, st + 1);
+#pragma unroll
+        for (int u = st; u < C::PIECES; u += C::DS) load(u);
         Full sf[C::VT];
 #pragma unroll
         for (int t = 0; t < C::VT; ++t) {
@@ -601,15 +652,13 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
           for (int e = 0; e < P::PER; ++e) x[e] = s[st * (C::STEP / 16) + e / 4][t][e % 4];
           sf[t] = P::full(x);
         }
-        Exact q[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) q[i] = q_row(16 * i + l16, st);
 #pragma unroll
         for (int part = 0; part < P::PARTS; ++part)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int t = 0; t < C::VT; ++t) o[i][t] = P::left(sf[t], q[i], o[i][t], part);
+            for (int t = 0; t < C::VT; ++t) o[i][t] = P::left(sf[t], q[st % 2][i], o[i][t], part);
+        __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -618,35 +667,67 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
         for (int t = 0; t < C::VT; ++t) o[i][t] = o[i][t] * f;
       }
       barrier_lds();
+      // the scores times v
+      int first[C::VT];  // the first token whose v is an infinity or a NaN in the lane's column
+#pragma unroll
+      for (int t = 0; t < C::VT; ++t) first[t] = kChunk;
+      bool any = false;
+#pragma unroll
+      for (int st = 0; st < C::JS; ++st) {
+        Exact v[C::VT];
+        bool odd = false;
+#pragma unroll
+        for (int t = 0; t < C::VT; ++t) {
+          v[t] = column(vl, c0 + 16 * t, st);
+          odd |= P::odd(v[t]);
+        }
+        if (__ballot(odd)) {  // left out of the products: a score of 0 would not keep it from the tokens before it
+          any = true;
+#pragma unroll
+          for (int t = 0; t < C::VT; ++t)
+#pragma unroll
+            for (int e = 0; e < P::PER; ++e)
+              if (!(fabsf(P::value(v[t], e)) < __builtin_inff())) {
+                first[t] = min(first[t], C::STEP * st + 16 * (e / 4) + h4 + e % 4);
+                P::clear(v[t], e);
+              }
+        }
+#pragma unroll
+        for (int i = st * (C::STEP / 16); i < 4; ++i) {
+          const Full sc = P::load(pl + (16 * i + l16) * PROWS + (sizeof(T) == 2 ? 32 * st + 2 * h4 : 16 * st + h4), kChunk * PROWS);
+#pragma unroll
+          for (int part = 0; part < P::PARTS; ++part)
+#pragma unroll
+            for (int t = 0; t < C::VT; ++t) o[i][t] = P::right(v[t], sc, o[i][t], part);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if (any) {
+#pragma unroll
+        for (int t = 0; t < C::VT; ++t) {
+          int f = min(first[t], __shfl_xor(first[t], 16));
+          f = min(f, __shfl_xor(f, 32));
+#pragma unroll
+          for (int r = 0; r < 4; ++r) {
+            const int from = __shfl(f, h4 + r);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              if (16 * i + l16 >= from) o[i][t][r] = __builtin_nanf("");
+          }
+        }
+      }
+      store(t, len);
+    } else {
+#pragma unroll
+      for (int u = 0; u < C::PIECES; ++u) load(u);
     }
+    // the state
 #pragma unroll
     for (int k = 0; k < C::KT; ++k)
 #pragma unroll
       for (int t = 0; t < C::VT; ++t) s[k][t] = s[k][t] * kept;
 #pragma unroll
     for (int st = 0; st < C::JS; ++st) {
-      Exact v[C::VT];
-      Full vf[C::VT];
-#pragma unroll
-      for (int t = 0; t < C::VT; ++t) v[t] = column(vl, c0 + 16 * t, st);
-      if constexpr (OUT) {
-#pragma unroll
-        for (int i = st * (C::STEP / 16); i < 4; ++i) {
-          Full sc;
-          const T* f = pl + (16 * i + l16) * PROWS + (sizeof(T) == 2 ? 32 * st + 2 * h4 : 16 * st + h4);
-          if constexpr (sizeof(T) == 2) {
-            sc.a = *reinterpret_cast<const bf16x8*>(f);
-            sc.b = *reinterpret_cast<const bf16x8*>(f + kChunk * PROWS);
-            sc.c = *reinterpret_cast<const bf16x8*>(f + 2 * kChunk * PROWS);
-          } else {
-            sc = *reinterpret_cast<const f32x4*>(f);
-          }
-#pragma unroll
-          for (int part = 0; part < P::PARTS; ++part)
-#pragma unroll
-            for (int t = 0; t < C::VT; ++t) o[i][t] = P::right(v[t], sc, o[i][t], part);
-        }
-      }
       float f[P::PER];
 #pragma unroll
       for (int u = 0; u < P::PER / 4; ++u) {
@@ -654,30 +735,37 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
 #pragma unroll
         for (int r = 0; r < 4; ++r) f[4 * u + r] = x[r];
       }
+      Full vf[C::VT];
 #pragma unroll
       for (int t = 0; t < C::VT; ++t) {
+        const Exact v = column(vl, c0 + 16 * t, st);
         float x[P::PER];
 #pragma unroll
-        for (int e = 0; e < P::PER; ++e) x[e] = P::value(v[t], e) * f[e];
+        for (int e = 0; e < P::PER; ++e) x[e] = P::value(v, e) * f[e];
         vf[t] = P::full(x);
       }
+      Exact kc[2][2];
 #pragma unroll
-      for (int k = 0; k < C::KT; ++k) {
-        const Exact kc = column(kl, 16 * k, st);
+      for (int k = 0; k < 2; ++k) kc[0][k] = column(kl, 16 * k, st);
+#pragma unroll
+      for (int k = 0; k < C::KT; k += 2) {
+        if (k + 2 < C::KT)
+#pragma unroll
+          for (int x = 0; x < 2; ++x) kc[(k / 2 + 1) % 2][x] = column(kl, 16 * (k + 2 + x), st);
 #pragma unroll
         for (int part = 0; part < P::PARTS; ++part)
 #pragma unroll
-          for (int t = 0; t < C::VT; ++t) s[k][t] = P::right(kc, vf[t], s[k][t], part);
+          for (int x = 0; x < 2; ++x)
+#pragma unroll
+            for (int t = 0; t < C::VT; ++t) s[k + x][t] = P::right(kc[k / 2 % 2][x], vf[t], s[k + x][t], part);
+        __builtin_amdgcn_sched_barrier(0);
       }
     }
     total_hi += gl[0][kChunk - 1];
     total_lo += gl[1][kChunk - 1];
     barrier_lds();
-    o_at = t;
-    o_len = len;
     t += len;
   }
-  store();
   float* to = OUT ? own : room;
   if (OUT && !last) return;
 #pragma unroll

@@ -502,6 +502,7 @@ gdn_status gdn_group_norm(const gdn_norm_dims* dims, const void* x, int64_t x_st
  *  state_ptrs device u64, fp32 [Hv][d_v][d_k] states, 16-byte aligned, updated in place. An entry of 0 marks an
  *             inactive slot (nothing read or written for it, its o rows untouched). Distinct slots.
  *  Alignment: q, k, v 16-byte aligned, their strides multiples of 16 bytes.
+ *  Errors: GDN_ERR_UNSUPPORTED where rows of a prefill's q, k, v or g lie 2^24 bytes or more apart.
  *
  * gdn_linear_prefill: packed ragged sequences, cu_seqlens device int32 [num_seqs+1] as for gdn_prefill_chunked;
  * zero-length sequences keep their state; rows outside [0, total_tokens) are not touched. A token's o depends on no

@@ -47,7 +47,8 @@ DECODE = dict(dims=linear(), q=FAKE, q_stride=8192, k=FAKE, k_stride=8192, v=FAK
 
 @pytest.mark.parametrize("kw,want", BOTH + [
     (dict(num_seqs=-1), SHAPE), (dict(total_tokens=-1), SHAPE), (dict(num_seqs=0), SHAPE), (dict(cu_seqlens=None), NULL),
-    (dict(workspace=FAKE + 128), ALIGN),
+    (dict(workspace=FAKE + 128), ALIGN), (dict(q_stride=1 << 23), UNSUP), (dict(k_stride=1 << 23), UNSUP),
+    (dict(v_stride=1 << 23), UNSUP), (dict(g_stride=1 << 22), UNSUP),
 ])
 def test_linear_prefill_refusals(kw, want):
     refused(gdn.gdn_linear_prefill, PREFILL, kw, want)
