@@ -219,9 +219,9 @@ struct Prod<uint16_t> {
     for (int e = 0; e < 4; ++e) o |= (y[e] & 0x7F807F80u) + 0x00800080u;
     return (o & 0x80008000u) != 0;
   }
-  __device__ __forceinline__ static Full load(const uint16_t* p, int plane) {
+  __device__ __forceinline__ static Full load(const uint16_t* p, int plane, int skip) {
     return Full{*reinterpret_cast<const bf16x8*>(p), *reinterpret_cast<const bf16x8*>(p + plane),
-                *reinterpret_cast<const bf16x8*>(p + 2 * plane)};
+                *reinterpret_cast<const bf16x8*>(p + (skip ? 1 : 2) * plane)};
   }
   __device__ __forceinline__ static f32x4 exact(const Exact& a, const Exact& b, const f32x4& acc) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
@@ -249,7 +249,7 @@ struct Prod<float> {
     return !(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))) < __builtin_inff()) || x[0] != x[0] ||
            x[1] != x[1] || x[2] != x[2] || x[3] != x[3];
   }
-  __device__ __forceinline__ static Full load(const float* p, int) { return *reinterpret_cast<const f32x4*>(p); }
+  __device__ __forceinline__ static Full load(const float* p, int, int) { return *reinterpret_cast<const f32x4*>(p); }
   __device__ __forceinline__ static f32x4 exact(const Exact& a, const Exact& b, f32x4 acc) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
@@ -374,9 +374,10 @@ __global__ __launch_bounds__(kTableThreads) void linear_table_kernel(LinearPlan 
   for (int b = r0 + tid; b < n_slots; b += kTableThreads) slots[b] = Place{-1, 0, -1};
 }
 
-template <int D, typename T>
+// OUT: the pass with outputs.
+template <int D, typename T, bool OUT>
 struct LinearCfg {
-  static constexpr int WAVES = D == 32 ? 2 : 4, THREADS = WAVES * kWave;
+  static constexpr int WAVES = D == 32 ? 2 : OUT ? 4 : D / 16, THREADS = WAVES * kWave;
   static constexpr int COLS = D / WAVES;    // d_v a wave
   static constexpr int VT = COLS / 16;      // 16x16 tiles: of d_v a wave
   static constexpr int KT = D / 16;         // of d_k
@@ -389,21 +390,24 @@ struct LinearCfg {
   // Rows of tiles are 16 bytes longer than their values, which spreads 16 rows' pieces of 16 bytes over all banks.
   static constexpr int PITCH = D + EPP;
   static constexpr int PROWS = kChunk + EPP;  // of the scores
-  static constexpr int PLANES = sizeof(T) == 2 ? 3 : 1;
 };
 
 // OUT: outputs and the state behind the tile; else what the tile adds to the state.
-template <int D, typename T, bool OUT>
-__global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1)) void linear_chunks_kernel(LinearArgs a, LinearPlan p) {
-  using C = LinearCfg<D, T>;
+template <int D, typename T, typename O, bool OUT>
+__global__ __launch_bounds__((LinearCfg<D, T, OUT>::THREADS), (sizeof(T) == 2 ? OUT ? 2 : 4 : 1)) void linear_chunks_kernel(LinearArgs a,
+                                                                                                                LinearPlan p) {
+  using C = LinearCfg<D, T, OUT>;
   using P = Prod<T>;
   using Exact = typename P::Exact;
   using Full = typename P::Full;
   constexpr int PITCH = C::PITCH, PROWS = C::PROWS;
+  // Outputs in bf16 (half a step: 2^-8) leave out the third parts, 2^-16 of a value, of what they alone are formed from.
+  constexpr int SKIP = sizeof(T) == 2 && sizeof(O) == 2 ? 1 : 0;
+  constexpr int PLANES = sizeof(T) == 2 ? 3 - SKIP : 1;
   __shared__ __attribute__((aligned(16))) T kl[kChunk * PITCH];
   __shared__ __attribute__((aligned(16))) T vl[kChunk * PITCH];
   __shared__ __attribute__((aligned(16))) T ql[OUT ? kChunk * PITCH : 16];
-  __shared__ __attribute__((aligned(16))) T pl[OUT ? C::PLANES * kChunk * PROWS : 16];
+  __shared__ __attribute__((aligned(16))) T pl[OUT ? PLANES * kChunk * PROWS : 16];
   __shared__ __attribute__((aligned(16))) float gl[4][kChunk];  // G's multiple of 2^-8, its rest, scale e^G_i, e^(G_n - G_i)
   const int tid = threadIdx.x, lane = tid & (kWave - 1), w = __builtin_amdgcn_readfirstlane(tid / kWave);
   int l16 = lane & 15, h = lane >> 4, h4 = 4 * h;
@@ -437,7 +441,7 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
         s[k][t] = *reinterpret_cast<const f32x4*>(from + (c0 + 16 * t + l16) * D + 16 * k + h4);
     // score tiles above the diagonal inside a step stay zero
     if constexpr (sizeof(T) == 2) {
-      for (int x = tid; x < 3 * 2 * 16 * 8; x += C::THREADS) {
+      for (int x = tid; x < PLANES * 2 * 16 * 8; x += C::THREADS) {
         const int plane = x / 256, r = x % 256 / 8, h = x % 8 / 2, half = x % 2;  // 4 bytes each
         const int i = r < 16 ? r : 32 + r - 16, pos = (r < 16 ? 0 : 32) + 8 * h + 4 + 2 * half;
         *reinterpret_cast<uint32_t*>(pl + (plane * kChunk + i) * PROWS + pos) = 0;
@@ -549,7 +553,7 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
       typedef __attribute__((address_space(1))) char gout;
       typedef __attribute__((address_space(1))) f32x4 go4;
       typedef __attribute__((address_space(1))) u32x2 go2;
-      gout* ob = (gout*)a.o + ((static_cast<int64_t>(at) * a.hv + j) * D + c0) * (a.o_bf16 ? 2 : 4);
+      gout* ob = (gout*)a.o + ((static_cast<int64_t>(at) * a.hv + j) * D + c0) * sizeof(O);
       const int mine = l16;
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
@@ -558,7 +562,7 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
 #pragma unroll
         for (int t = 0; t < C::VT; ++t) {
           const f32x4 v = o[i][t];
-          if (a.o_bf16) {
+          if constexpr (sizeof(O) == 2) {
             const u32x2 x = {static_cast<uint32_t>(to_bf16(v[0])) | static_cast<uint32_t>(to_bf16(v[1])) << 16,
                              static_cast<uint32_t>(to_bf16(v[2])) | static_cast<uint32_t>(to_bf16(v[3])) << 16};
             *(go2*)(ob + (to + 16 * t) * 2) = x;
@@ -623,7 +627,7 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
           for (int r = 0; r < 4; ++r) P::thirds(v[r], x3[0][r], x3[1][r], x3[2][r]);
           T* to = pl + i * PROWS + 32 * (tj[y] / 2) + 2 * h4 + 4 * (tj[y] % 2);
 #pragma unroll
-          for (int z = 0; z < 3; ++z)
+          for (int z = 0; z < PLANES; ++z)
             *reinterpret_cast<u32x2*>(to + z * kChunk * PROWS) = u32x2{P::tops(x3[z][0], x3[z][1]), P::tops(x3[z][2], x3[z][3])};
         } else {
           *reinterpret_cast<f32x4*>(pl + i * PROWS + j0) = f32x4{v[0], v[1], v[2], v[3]};
@@ -653,7 +657,7 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
           sf[t] = P::full(x);
         }
 #pragma unroll
-        for (int part = 0; part < P::PARTS; ++part)
+        for (int part = SKIP; part < P::PARTS; ++part)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -694,9 +698,9 @@ __global__ __launch_bounds__((LinearCfg<D, T>::THREADS), (sizeof(T) == 2 ? 2 : 1
         }
 #pragma unroll
         for (int i = st * (C::STEP / 16); i < 4; ++i) {
-          const Full sc = P::load(pl + (16 * i + l16) * PROWS + (sizeof(T) == 2 ? 32 * st + 2 * h4 : 16 * st + h4), kChunk * PROWS);
+          const Full sc = P::load(pl + (16 * i + l16) * PROWS + (sizeof(T) == 2 ? 32 * st + 2 * h4 : 16 * st + h4), kChunk * PROWS, SKIP);
 #pragma unroll
-          for (int part = 0; part < P::PARTS; ++part)
+          for (int part = SKIP; part < P::PARTS; ++part)
 #pragma unroll
             for (int t = 0; t < C::VT; ++t) o[i][t] = P::right(v[t], sc, o[i][t], part);
         }
@@ -836,9 +840,8 @@ LinearSizes sizes(int32_t hv, int32_t d, int32_t n, int32_t total, int32_t form)
 
 template <int D, typename T>
 hipError_t prefill_dt(const LinearArgs& a, LinearPlan p, const LinearSizes& z, hipStream_t s) {
-  using C = LinearCfg<D, T>;
   // fewer than 2^31 threads a launch
-  const int64_t most = ((int64_t)1 << 31) / (static_cast<int64_t>(a.hv) * (D * D / 4 > 256 ? D * D / 4 : 256));
+  const int64_t most = ((int64_t)1 << 31) / (static_cast<int64_t>(a.hv) * (D * D / 4 > 512 ? D * D / 4 : 512));
   hipError_t e = hipSuccess;
   const auto in_turns = [&](int64_t n, auto launch) {
     for (int64_t f = 0; f < n && e == hipSuccess; f += most) {
@@ -847,9 +850,15 @@ hipError_t prefill_dt(const LinearArgs& a, LinearPlan p, const LinearSizes& z, h
       e = hipGetLastError();
     }
   };
-  in_turns(z.slots, [&](unsigned grid) { linear_chunks_kernel<D, T, false><<<grid, C::THREADS, 0, s>>>(a, p); });
+  in_turns(z.slots, [&](unsigned grid) {
+    linear_chunks_kernel<D, T, float, false><<<grid, LinearCfg<D, T, false>::THREADS, 0, s>>>(a, p);
+  });
   in_turns(z.slots, [&](unsigned grid) { linear_scan_kernel<D><<<grid * (D * D / 4 / kScanThreads), kScanThreads, 0, s>>>(a, p); });
-  in_turns(z.tiles, [&](unsigned grid) { linear_chunks_kernel<D, T, true><<<grid, C::THREADS, 0, s>>>(a, p); });
+  in_turns(z.tiles, [&](unsigned grid) {
+    constexpr int threads = LinearCfg<D, T, true>::THREADS;
+    if (a.o_bf16) linear_chunks_kernel<D, T, uint16_t, true><<<grid, threads, 0, s>>>(a, p);
+    else linear_chunks_kernel<D, T, float, true><<<grid, threads, 0, s>>>(a, p);
+  });
   return e;
 }
 
