@@ -827,7 +827,7 @@ gdn_status gdn_block_norm(const gdn_block_norm_dims* dims, const void* x, int64_
 
 static gdn_status check_sample(const char* fn, int32_t rows, int32_t vocab) {
   if (rows < 0) return fail(GDN_ERR_SHAPE, "%s: negative rows", fn);
-  if (vocab < 1 || vocab > (1 << 21)) return fail(GDN_ERR_SHAPE, "%s: vocab %d outside 1 .. 2^21", fn, vocab);
+  if (vocab < 1 || vocab > (1 << 20)) return fail(GDN_ERR_SHAPE, "%s: vocab %d outside 1 .. 2^20", fn, vocab);
   return GDN_OK;
 }
 

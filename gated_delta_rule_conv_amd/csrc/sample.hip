@@ -5,11 +5,14 @@
 // not, so a row's token depends on nothing but the row, and a border (top_p's, or the random number's) is met within
 // 2^-S of the largest weight a token. Tokens whose weight is 0 do not count at all: they come last in the order.
 //
-// A row is cut into tiles of 1024 tokens, a wave each. Three or four launches, each over all rows:
+// A row is cut into tiles of 512 tokens, a wave each. Without filters two launches over all rows:
+//   tiles     the largest value of every tile, and the tile's weight against it: logits are read once
+//   choose    (below)
+// and with them three or four:
 //   extremes  the largest and the least finite value of every tile
 //   weigh     rows without top_k and top_p: the weight of every tile. Others: counts and weights of 1024 bins of the distance
 //             from the row's largest value, in LDS, then added to the row's
-//   gather    (only where a filter is given) from the bins, the few in which the filters' borders must lie; the weight of every
+//   gather    (only where top_k or top_p is given) from the bins, the few in which their borders must lie; the weight of every
 //             tile's tokens before them, and a list of the tokens inside them
 //   choose    a workgroup a row: the list sorted by (value, index), the borders met exactly, the kept ones' weights added to their
 //             tiles', the tile in which the weight passes u times the sum, and the token in it
@@ -24,8 +27,7 @@ namespace gdn {
 namespace {
 
 constexpr int kThreads = 512, kWaves = kThreads / kWave;
-constexpr int kTile = 1024;               // tokens of a wave
-constexpr int kRounds = kTile / (8 * kWave);
+constexpr int kTile = 8 * kWave;  // tokens of a wave
 constexpr int kBins = 1024;
 constexpr int kList = 4096;
 constexpr uint32_t kLowest = 0x007FFFFFu;  // key_of(-infinity)
@@ -76,56 +78,67 @@ __device__ __forceinline__ void load8(const T* x, int i, int n, float (&v)[8]) {
   }
 }
 
-// 2^t for t <= 0: the series of e^(f ln 2) for the part of t past its nearest whole number, |f| <= 1/2 (the first
-// term left out is under 2^-52), times a power of two.
-__device__ __forceinline__ double power_of_two(double t) {
-  t = t < -1100.0 ? -1100.0 : t;
-  const double n = rint(t), f = (t - n) * 0.693147180559945309417;
-  double s = 1.0 / 479001600.0;
-  s = fma(s, f, 1.0 / 39916800.0);
-  s = fma(s, f, 1.0 / 3628800.0);
-  s = fma(s, f, 1.0 / 362880.0);
-  s = fma(s, f, 1.0 / 40320.0);
-  s = fma(s, f, 1.0 / 5040.0);
-  s = fma(s, f, 1.0 / 720.0);
-  s = fma(s, f, 1.0 / 120.0);
-  s = fma(s, f, 1.0 / 24.0);
-  s = fma(s, f, 1.0 / 6.0);
-  s = fma(s, f, 0.5);
-  s = fma(s, f, 1.0);
-  s = fma(s, f, 1.0);
-  return ldexp(s, static_cast<int>(n));
+// 2^(j / 32) times 2^S, j < 32: the 32 lie in 32 pairs of LDS banks, so that reads of any of them do not meet.
+constexpr int kSteps = 32;
+__device__ __forceinline__ void fill_steps(double* steps, int shift) {
+  if (threadIdx.x < kSteps) {  // the series of e^(j ln 2 / 32); the first term left out is under 2^-56
+    const double f = threadIdx.x * (0.693147180559945309417 / kSteps);
+    double s = 1.0;
+#pragma unroll
+    for (int n = 18; n > 0; --n) s = fma(s, f / n, 1.0);
+    steps[threadIdx.x] = ldexp(s, shift);
+  }
 }
 
-enum Mode { kNone, kLikeliest, kPlain, kListed, kLooked };
+enum Mode { kNone, kLikeliest, kPlain, kListed };
 
 // What a row's tokens are judged by.
 struct Row {
-  float most;      // the largest value
-  double per;      // log2(e) / T
-  float far;       // a distance from the largest value beyond which a weight is surely 0
-  float bins;      // bins by distance
-  double least;    // min_p, at most 1
-  int shift;       // S
-  int32_t k;       // 0: no top_k
-  float p;         // 1: no top_p
-  int mode;        // kNone, kLikeliest, kPlain, or kListed for rows with a filter
+  float most;          // the largest value
+  double per;          // 32 log2(e) / T
+  double off;          // - most per
+  float far;           // a distance from the largest value beyond which a weight is surely 0
+  float bins;          // bins by distance
+  double least;        // 2^S min_p, min_p at most 1
+  const double* steps;
+  int shift;           // S
+  int32_t k;           // 0: no top_k
+  float p;             // 1: no top_p
+  int mode;            // kNone, kLikeliest, kPlain, or kListed for rows with top_k or top_p
 
-  // e^((x - most) / T), of the largest value 1
-  __device__ __forceinline__ double weight(float x) const {
-    if (x == most) return 1.0;
-    if (!(most - x <= far) || x == -__builtin_inff()) return 0.0;  // (a NaN, and whatever lies beside an infinity)
-    return power_of_two((static_cast<double>(x) - static_cast<double>(most)) * per);
+  __device__ __forceinline__ void against(float largest) {
+    most = largest;
+    off = -static_cast<double>(largest) * per;
+    // (infinite T: all finite distances; beside an infinity nothing else weighs anything)
+    far = largest < __builtin_inff() ? static_cast<float>((shift + 1.5) * kSteps / per) : -1.f;
   }
-  // round(2^S w), w <= 1: the low bits of 2^52 + 2^S w
-  __device__ __forceinline__ unsigned long long whole(double w) const {
-    return __double_as_longlong(ldexp(w, shift) + 0x1p52) & 0xFFFFFFFFFFFFFull;
+  // 2^S e^((x - most) / T): t = 32 log2 of the exponential, its nearest whole number n and the rest f, |f| <= 1/2;
+  // 2^(t / 32) = 2^(n / 32) e^(f ln 2 / 32), the series good to 2^-48.
+  __device__ __forceinline__ double weight(float x) const {
+    const double t = fma(static_cast<double>(x), per, off);
+    const double whole = t + 0x1.8p52;
+    const int n = static_cast<int>(__double_as_longlong(whole));
+    const double f = (t - (whole - 0x1.8p52)) * (0.693147180559945309417 / kSteps);
+    double s = fma(f, 1.0 / 120.0, 1.0 / 24.0);
+    s = fma(s, f, 1.0 / 6.0);
+    s = fma(s, f, 0.5);
+    s = fma(s, f, 1.0);
+    s = fma(s, f, 1.0);
+    const long long step = __double_as_longlong(steps[n & (kSteps - 1)]) + (static_cast<long long>(n >> 5) << 52);
+    const double w = __longlong_as_double(step) * s;
+    // (a NaN is not near, nor is minus infinity at an infinite T; whatever was formed from them is dropped)
+    const bool near = most - x <= far && x > -__builtin_inff();
+    return x == most ? __longlong_as_double(static_cast<long long>(shift + 1023) << 52) : near ? w : 0.0;
+  }
+  // rounded: the low bits of 2^52 + w
+  __device__ __forceinline__ static unsigned long long whole(double w) {
+    return __double_as_longlong(w + 0x1p52) & 0xFFFFFFFFFFFFFull;
   }
   // -1: no token that could come
   __device__ __forceinline__ int bin(float x) const {
-    if (x == most) return 0;
     const float d = most - x;
-    return d <= far && x > -__builtin_inff() ? static_cast<int>(fminf(d * bins, kBins - 1.0f)) : -1;
+    const int b = static_cast<int>(fminf(d * bins, kBins - 1.0f));
+    return x == most ? 0 : d <= far && x > -__builtin_inff() ? b : -1;
   }
 };
 
@@ -165,24 +178,49 @@ struct Call {
   int first;   // the launch's first row
 };
 
-__device__ __forceinline__ unsigned long long wave_sum(unsigned long long v) {
-#pragma unroll
-  for (int m = 1; m < kWave; m *= 2) v += __shfl_xor(v, m);
-  return v;
+// Lane operations along rows of 16 lanes, then over the rows (DPP): lane 63 has seen all.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ uint32_t moved(uint32_t v, uint32_t none) {
+  return static_cast<uint32_t>(__builtin_amdgcn_update_dpp(static_cast<int>(none), static_cast<int>(v), CTRL, ROWS, 0xF, false));
+}
+template <typename F>
+__device__ __forceinline__ uint32_t wave_all(uint32_t v, uint32_t none, F join) {
+  v = join(v, moved<0x111, 0xF>(v, none));
+  v = join(v, moved<0x112, 0xF>(v, none));
+  v = join(v, moved<0x114, 0xF>(v, none));
+  v = join(v, moved<0x118, 0xF>(v, none));
+  v = join(v, moved<0x142, 0xA>(v, none));
+  v = join(v, moved<0x143, 0xC>(v, none));
+  return static_cast<uint32_t>(__builtin_amdgcn_readlane(static_cast<int>(v), kWave - 1));
+}
+__device__ __forceinline__ uint32_t wave_max(uint32_t v) {
+  return wave_all(v, 0u, [](uint32_t a, uint32_t b) { return max(a, b); });
+}
+__device__ __forceinline__ uint32_t wave_min(uint32_t v) {
+  return wave_all(v, 0xFFFFFFFFu, [](uint32_t a, uint32_t b) { return min(a, b); });
+}
+template <int CTRL, int ROWS>
+__device__ __forceinline__ unsigned long long add_moved(unsigned long long v) {
+  const uint32_t lo = moved<CTRL, ROWS>(static_cast<uint32_t>(v), 0), hi = moved<CTRL, ROWS>(static_cast<uint32_t>(v >> 32), 0);
+  return v + (static_cast<unsigned long long>(hi) << 32 | lo);
+}
+// the sum over the lanes up to each one
+__device__ __forceinline__ unsigned long long wave_scan(unsigned long long v) {
+  v = add_moved<0x111, 0xF>(v);
+  v = add_moved<0x112, 0xF>(v);
+  v = add_moved<0x114, 0xF>(v);
+  v = add_moved<0x118, 0xF>(v);
+  v = add_moved<0x142, 0xA>(v);
+  return add_moved<0x143, 0xC>(v);
 }
 
 // Sum over the threads up to each one; `all` gets the sum of all.
 struct Scan {
   unsigned long long part[2][kWaves];
-  int turn;
 };
 __device__ __forceinline__ unsigned long long scan(unsigned long long v, Scan& s, int& turn, unsigned long long& all) {
   const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-#pragma unroll
-  for (int m = 1; m < kWave; m *= 2) {
-    const unsigned long long o = __shfl_up(v, m);
-    if (lane >= m) v += o;
-  }
+  v = wave_scan(v);
   turn ^= 1;  // (the readers of the last turn's parts need not be done)
   if (lane == kWave - 1) s.part[turn][w] = v;
   __syncthreads();
@@ -196,20 +234,35 @@ __device__ __forceinline__ unsigned long long scan(unsigned long long v, Scan& s
   return v + before;
 }
 
+// What a row's parameters ask for.
+__device__ __forceinline__ Row parameters(const Call& c, int r, const double* steps) {
+  Row row{};
+  const float t = c.a.temperature ? c.a.temperature[r] : 1.0f;
+  const float min_p = c.a.min_p ? c.a.min_p[r] : 0.f;
+  row.k = c.a.top_k ? c.a.top_k[r] : 0;
+  const float p = c.a.top_p ? c.a.top_p[r] : 1.f;
+  row.per = 1.44269504088896340736 * kSteps / static_cast<double>(t);
+  row.shift = c.shift;
+  row.steps = steps;
+  row.least = ldexp(min_p > 0.f ? (min_p < 1.f ? min_p : 1.0) : 0.0, c.shift);
+  if (row.k < 0 || row.k >= c.a.vocab) row.k = 0;
+  row.p = p < 1.f ? p : 1.f;
+  row.mode = !(t > 0.f) ? kLikeliest : row.k == 0 && row.p == 1.f ? kPlain : kListed;
+  return row;
+}
+
 // The row's largest and least values, and what its parameters ask for. Every thread gets it.
-__device__ Row row_of(const Call& c, int r, uint32_t (&part)[2][kWaves]) {
+__device__ __forceinline__ Row row_of(const Call& c, int r, const double* steps, uint32_t (&part)[2][kWaves]) {
   uint32_t most = 0, least = 0xFFFFFFFFu;
   const uint2* e = c.w.ends + static_cast<int64_t>(r) * c.tiles;
+  Row row = parameters(c, r, steps);
   for (int t = threadIdx.x; t < c.tiles; t += kThreads) {
     const uint2 x = e[t];
     most = max(most, x.x);
     least = min(least, x.y);
   }
-#pragma unroll
-  for (int m = 1; m < kWave; m *= 2) {
-    most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), m)));
-    least = min(least, static_cast<uint32_t>(__shfl_xor(static_cast<int>(least), m)));
-  }
+  most = wave_max(most);
+  least = wave_min(least);
   if (threadIdx.x % kWave == 0) {
     part[0][threadIdx.x / kWave] = most;
     part[1][threadIdx.x / kWave] = least;
@@ -220,58 +273,86 @@ __device__ Row row_of(const Call& c, int r, uint32_t (&part)[2][kWaves]) {
     most = max(most, part[0][w]);
     least = min(least, part[1][w]);
   }
-  Row row;
-  row.most = value_of(most);
-  const float t = c.a.temperature ? c.a.temperature[r] : 1.0f;
-  row.per = 1.44269504088896340736 / static_cast<double>(t);
-  row.shift = c.shift;
-  row.far = row.most < __builtin_inff() ? static_cast<float>((c.shift + 1.5) / row.per) : -1.f;  // (infinite T: all finite distances)
+  row.against(value_of(most));
   const float range = fminf(row.most - value_of(least), row.far);
   row.bins = range > 0.f ? fminf(static_cast<float>(kBins) / range, 1e30f) : 0.f;
-  const float min_p = c.a.min_p ? c.a.min_p[r] : 0.f;
-  row.least = min_p > 0.f ? (min_p < 1.f ? min_p : 1.0) : 0.0;
-  row.k = c.a.top_k ? c.a.top_k[r] : 0;
-  if (row.k < 0 || row.k >= c.a.vocab) row.k = 0;
-  const float p = c.a.top_p ? c.a.top_p[r] : 1.f;
-  row.p = p < 1.f ? p : 1.f;
-  row.mode = most <= kLowest ? kNone : !(t > 0.f) ? kLikeliest : row.k == 0 && row.p == 1.f ? kPlain : kListed;
+  if (most <= kLowest) row.mode = kNone;
   return row;
 }
 
 // -------------------------------------------------------------------------- extremes
 
+__device__ __forceinline__ uint2 ends_of(const float (&v)[8]) {
+  uint32_t most = kLowest, least = 0xFFFFFFFFu;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) {
+    const uint32_t k = key_of(v[e]);
+    most = max(most, k);
+    least = min(least, k > kLowest ? k : 0xFFFFFFFFu);
+  }
+  return uint2{wave_max(most), wave_min(least)};
+}
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void sample_extremes_kernel(Call c) {
-  const int blocks = (c.tiles + kWaves - 1) / kWaves;
-  const int r = c.first + blockIdx.x / blocks, b = blockIdx.x % blocks;
-  const int lane = threadIdx.x & (kWave - 1), t = b * kWaves + threadIdx.x / kWave;
-  if (c.w.counts && b == 0) {  // the row's bins and list begin empty
+  const int r = c.first + blockIdx.x / c.groups, g = blockIdx.x % c.groups;
+  const int lane = threadIdx.x & (kWave - 1);
+  if (c.w.counts && g == 0) {  // the row's bins and list begin empty
     for (int i = threadIdx.x; i < kBins; i += kThreads) {
       c.w.counts[static_cast<int64_t>(r) * kBins + i] = 0;
       c.w.weights[static_cast<int64_t>(r) * kBins + i] = 0;
     }
     if (threadIdx.x == 0) c.w.listed[r] = 0;
   }
-  if (t >= c.tiles) return;
   const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
-  uint32_t most = kLowest, least = 0xFFFFFFFFu;
-  float v[kRounds][8];
-#pragma unroll
-  for (int n = 0; n < kRounds; ++n) load8(x, t * kTile + 8 * (n * kWave + lane), c.a.vocab, v[n]);
-#pragma unroll
-  for (int n = 0; n < kRounds; ++n)
-#pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const uint32_t k = key_of(v[n][e]);
-      most = max(most, k);
-      least = min(least, k > kLowest ? k : 0xFFFFFFFFu);
-    }
-#pragma unroll
-  for (int m = 1; m < kWave; m *= 2) {
-    most = max(most, static_cast<uint32_t>(__shfl_xor(static_cast<int>(most), m)));
-    least = min(least, static_cast<uint32_t>(__shfl_xor(static_cast<int>(least), m)));
+  uint2* to = c.w.ends + static_cast<int64_t>(r) * c.tiles;
+  const int step = c.groups * kWaves;
+  for (int t = g * kWaves + threadIdx.x / kWave; t < c.tiles; t += 2 * step) {
+    float v[2][8];
+    load8(x, t * kTile + 8 * lane, c.a.vocab, v[0]);
+    load8(x, min(t + step, c.tiles - 1) * kTile + 8 * lane, c.a.vocab, v[1]);
+    const uint2 a = ends_of(v[0]), b = ends_of(v[1]);
+    if (lane == 0) to[t] = a;
+    if (lane == 0 && t + step < c.tiles) to[t + step] = b;
   }
-  if (lane == 0) c.w.ends[static_cast<int64_t>(r) * c.tiles + t] = uint2{most, least};
+}
+
+// ------------------------------------------------------------------------------ tiles
+
+// The tile's largest value and its weight against that.
+template <typename T>
+__global__ __launch_bounds__(kThreads) void sample_tiles_kernel(Call c) {
+  __shared__ double steps[kSteps];
+  const int r = c.first + blockIdx.x / c.groups, g = blockIdx.x % c.groups;
+  const int lane = threadIdx.x & (kWave - 1);
+  fill_steps(steps, c.shift);
+  __syncthreads();
+  Row row = parameters(c, r, steps);
+  const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
+  const int step = c.groups * kWaves;
+  float v[8], next[8];
+  int t = g * kWaves + threadIdx.x / kWave;
+  if (t < c.tiles) load8(x, t * kTile + 8 * lane, c.a.vocab, next);
+  for (; t < c.tiles; t += step) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[e] = next[e];
+    load8(x, min(t + step, c.tiles - 1) * kTile + 8 * lane, c.a.vocab, next);
+    uint32_t most = kLowest;
+#pragma unroll
+    for (int e = 0; e < 8; ++e) most = max(most, key_of(v[e]));
+    most = wave_max(most);
+    unsigned long long sum = 0;
+    if (row.mode == kPlain && most > kLowest) {
+      row.against(value_of(most));
+#pragma unroll
+      for (int e = 0; e < 8; ++e) sum += row.whole(row.weight(v[e]));
+      sum = wave_scan(sum);
+    }
+    if (lane == kWave - 1) {
+      c.w.ends[static_cast<int64_t>(r) * c.tiles + t] = uint2{most, 0xFFFFFFFFu};
+      c.w.sums[static_cast<int64_t>(r) * c.tiles + t] = sum;
+    }
+  }
 }
 
 // ------------------------------------------------------------------------------ weigh
@@ -281,43 +362,44 @@ __global__ __launch_bounds__(kThreads) void sample_weigh_kernel(Call c) {
   __shared__ unsigned long long weights[kBins];
   __shared__ uint32_t counts[kBins];
   __shared__ uint32_t part[2][kWaves];
+  __shared__ double steps[kSteps];
   const int r = c.first + blockIdx.x / c.groups, g = blockIdx.x % c.groups;
-  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
-  const Row row = row_of(c, r, part);
-  if (row.mode < kPlain) return;
+  const int lane = threadIdx.x & (kWave - 1), step = c.groups * kWaves;
   const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
-  const bool plain = row.mode == kPlain;
-  if (!plain) {
-    for (int i = threadIdx.x; i < kBins; i += kThreads) {
-      weights[i] = 0;
-      counts[i] = 0;
-    }
-    __syncthreads();
+  int t = g * kWaves + threadIdx.x / kWave;
+  float v[8], next[8];
+  if (t < c.tiles) load8(x, t * kTile + 8 * lane, c.a.vocab, next);
+  fill_steps(steps, c.shift);
+  for (int i = threadIdx.x; i < kBins; i += kThreads) {
+    weights[i] = 0;
+    counts[i] = 0;
   }
-  for (int t = g * kWaves + w; t < c.tiles; t += c.groups * kWaves) {
-    unsigned long long sum = 0;
-    for (int n = 0; n < kRounds; ++n) {
-      float v[8];
-      load8(x, t * kTile + 8 * (n * kWave + lane), c.a.vocab, v);
-      if (plain) {
+  const Row row = row_of(c, r, steps, part);  // (with a barrier)
+  if (row.mode < kPlain) return;
+  const bool plain = row.mode == kPlain, heavy = row.p < 1.f;
+  for (; t < c.tiles; t += step) {
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const double f = row.weight(v[e]);
-          sum += f < row.least ? 0 : row.whole(f);
-        }
-      } else {
+    for (int e = 0; e < 8; ++e) v[e] = next[e];
+    load8(x, min(t + step, c.tiles - 1) * kTile + 8 * lane, c.a.vocab, next);
+    if (plain) {
+      unsigned long long sum = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-          const int b = row.bin(v[e]);
-          if (b < 0) continue;
-          atomicAdd(&counts[b], 1u);
-          atomicAdd(&weights[b], row.whole(row.weight(v[e])));
+      for (int e = 0; e < 8; ++e) {
+        const double w = row.weight(v[e]);
+        sum += w < row.least ? 0 : row.whole(w);
+      }
+      sum = wave_scan(sum);
+      if (lane == kWave - 1) c.w.sums[static_cast<int64_t>(r) * c.tiles + t] = sum;
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) {
+        const int b = row.bin(v[e]);
+        if (b >= 0) atomicAdd(&counts[b], 1u);
+        if (heavy) {  // (top_k alone needs no weights of bins)
+          const unsigned long long w = row.whole(row.weight(v[e]));
+          if (b >= 0) atomicAdd(&weights[b], w);
         }
       }
-    }
-    if (plain) {
-      sum = wave_sum(sum);
-      if (lane == 0) c.w.sums[static_cast<int64_t>(r) * c.tiles + t] = sum;
     }
   }
   if (plain) return;
@@ -335,34 +417,44 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(Call c) {
   static_assert(kBins == 2 * kThreads, "two bins a thread");
   __shared__ Scan parts;
   __shared__ uint32_t part[2][kWaves];
+  __shared__ double steps[kSteps];
   __shared__ int top_at, from_at, to_at;
-  __shared__ unsigned long long whole_at, before_at;
+  __shared__ unsigned long long whole_at, most_at, before_at;
   __shared__ uint32_t stay_at;
   const int r = c.first + blockIdx.x / c.groups, g = blockIdx.x % c.groups;
-  const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave;
-  const Row row = row_of(c, r, part);
-  if (row.mode != kListed) return;
-  int turn = 0;
+  const int tid = threadIdx.x, lane = tid & (kWave - 1), step = c.groups * kWaves;
+  const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
+  int t = g * kWaves + tid / kWave;
+  float v[8], next[8];
+  if (t < c.tiles) load8(x, t * kTile + 8 * lane, c.a.vocab, next);
   // the bins' counts and weights, and those of all bins before them
   unsigned long long n2[2], w2[2], nb[2], wb[2], all_n, all_w;
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    n2[e] = c.w.counts[static_cast<int64_t>(r) * kBins + 2 * tid + e];
-    w2[e] = c.w.weights[static_cast<int64_t>(r) * kBins + 2 * tid + e];
+  {
+    const uint2 n = *reinterpret_cast<const uint2*>(c.w.counts + static_cast<int64_t>(r) * kBins + 2 * tid);
+    const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(c.w.weights + static_cast<int64_t>(r) * kBins + 2 * tid);
+    n2[0] = n.x;
+    n2[1] = n.y;
+    w2[0] = w.x;
+    w2[1] = w.y;
   }
+  fill_steps(steps, c.shift);
+  const Row row = row_of(c, r, steps, part);
+  if (row.mode != kListed) return;
+  int turn = 0;
   nb[0] = scan(n2[0] + n2[1], parts, turn, all_n) - n2[0] - n2[1];
   wb[0] = scan(w2[0] + w2[1], parts, turn, all_w) - w2[0] - w2[1];
   nb[1] = nb[0] + n2[0];
   wb[1] = wb[0] + w2[0];
+  const bool by_count = row.k > 0 && static_cast<unsigned long long>(row.k) < all_n, by_weight = row.p < 1.f;
   if (tid == 0) {
-    top_at = kBins;
-    whole_at = all_w;
-    stay_at = 0;
     from_at = to_at = 0;
     before_at = 0;
+    if (!by_count) {
+      top_at = kBins;
+      stay_at = 0;
+      whole_at = most_at = all_w;
+    }
   }
-  __syncthreads();
-  const bool by_count = row.k > 0 && static_cast<unsigned long long>(row.k) < all_n;
   if (by_count) {
 #pragma unroll
     for (int e = 0; e < 2; ++e)
@@ -370,66 +462,77 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(Call c) {
         top_at = 2 * tid + e;
         stay_at = static_cast<uint32_t>(row.k - nb[e]);
         whole_at = wb[e];
+        most_at = wb[e] + w2[e];  // (of the bin of top_k's border a part stays)
       }
   }
   __syncthreads();
   const int top = top_at;
-  unsigned long long most_w = whole_at;  // (of the bin of top_k's border a part stays)
-  if (by_count) most_w += c.w.weights[static_cast<int64_t>(r) * kBins + top];
-  const bool by_weight = row.p < 1.f;
   if (by_weight) {
     const double low = static_cast<double>(row.p) * static_cast<double>(whole_at);
-    const double high = static_cast<double>(row.p) * static_cast<double>(most_w);
+    const double high = static_cast<double>(row.p) * static_cast<double>(most_at);
+    // the last bin before which too little lies, for either
+    int a = -1, b = -1;
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int b = 2 * tid + e;
-      if (n2[e] == 0 || b > top) continue;
-      if (static_cast<double>(wb[e]) < low) atomicMax(&from_at, b);
-      if (static_cast<double>(wb[e]) < high) atomicMax(&to_at, b);
+      if (n2[e] == 0 || 2 * tid + e > top) continue;
+      if (static_cast<double>(wb[e]) < low) a = 2 * tid + e;
+      if (static_cast<double>(wb[e]) < high) b = 2 * tid + e;
     }
+    const int wa = static_cast<int>(wave_max(static_cast<uint32_t>(a + 1))), wb1 = static_cast<int>(wave_max(static_cast<uint32_t>(b + 1)));
+    if (lane == 0 && wa) atomicMax(&from_at, wa - 1);
+    if (lane == 0 && wb1) atomicMax(&to_at, wb1 - 1);
+    __syncthreads();
   }
-  __syncthreads();
   const int from = by_weight ? from_at : kBins, to = by_weight ? to_at : -1;
   const int sure = by_weight ? from : top;  // bins before this one stay
-#pragma unroll
-  for (int e = 0; e < 2; ++e)
-    if (by_weight && 2 * tid + e == from) before_at = wb[e];
-  unsigned long long mine = 0, listed;
+  unsigned long long mine = 0, inside;
 #pragma unroll
   for (int e = 0; e < 2; ++e) {
     const int b = 2 * tid + e;
+    if (by_weight && b == from) before_at = wb[e];
     if ((b >= from && b <= to) || b == top) mine += n2[e];
   }
-  scan(mine, parts, turn, listed);
-  const bool looked = listed > kList;
+  scan(mine, parts, turn, inside);
+  const bool looked = inside > kList;
   if (g == 0 && tid == 0)
-    c.w.plans[r] = Plan{looked, static_cast<int32_t>(looked ? 0 : listed), top, stay_at, from, to, whole_at, before_at};
+    c.w.plans[r] = Plan{looked, static_cast<int32_t>(looked ? 0 : inside), top, stay_at, from, to, whole_at, before_at};
   if (looked) return;
-  const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
-  for (int t = g * kWaves + w; t < c.tiles; t += c.groups * kWaves) {
-    unsigned long long sum = 0;
-    for (int n = 0; n < kRounds; ++n) {
-      float v[8];
-      const int i0 = t * kTile + 8 * (n * kWave + lane);
-      load8(x, i0, c.a.vocab, v);
+  for (; t < c.tiles; t += step) {
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        const int b = row.bin(v[e]);
-        if (b >= 0 && b < sure) {
-          const double f = row.weight(v[e]);
-          sum += f < row.least ? 0 : row.whole(f);
-        }
-        const bool in = (b >= from && b <= to) || b == top;
-        const uint64_t mask = __ballot(in);
-        if (mask == 0) continue;
-        uint32_t at = 0;
-        if (lane == __builtin_ctzll(mask)) at = atomicAdd(&c.w.listed[r], static_cast<uint32_t>(__popcll(mask)));
-        at = __shfl(at, __builtin_ctzll(mask)) + __popcll(mask & ((1ull << lane) - 1));
-        if (in && at < kList) c.w.list[static_cast<int64_t>(r) * kList + at] = i0 + e;
+    for (int e = 0; e < 8; ++e) v[e] = next[e];
+    load8(x, min(t + step, c.tiles - 1) * kTile + 8 * lane, c.a.vocab, next);
+    const int i0 = t * kTile + 8 * lane;
+    uint32_t stays = 0, listed = 0;  // bits of the lane's tokens
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+      const int b = row.bin(v[e]);
+      stays |= (b >= 0 && b < sure) << e;
+      listed |= ((b >= from && b <= to) || b == top) << e;
+    }
+    // one of a lane's tokens at a time, as many times as the lane with most of them has (few stay, mostly)
+    unsigned long long sum = 0;
+    while (__ballot(stays != 0)) {
+      const int e = __builtin_ctz(stays | 0x100u);
+      float y = v[0];
+#pragma unroll
+      for (int q = 1; q < 8; ++q) y = e == q ? v[q] : y;
+      const double w = row.weight(y);
+      sum += stays == 0 || w < row.least ? 0 : row.whole(w);
+      stays &= stays - 1;
+    }
+    if (__ballot(listed != 0)) {
+      const unsigned long long upto = wave_scan(__builtin_popcount(listed));
+      uint32_t at = 0;
+      if (lane == kWave - 1) at = atomicAdd(&c.w.listed[r], static_cast<uint32_t>(upto));
+      at = __builtin_amdgcn_readlane(at, kWave - 1) + static_cast<uint32_t>(upto) - __builtin_popcount(listed);
+      while (listed) {
+        if (at < kList) c.w.list[static_cast<int64_t>(r) * kList + at] = i0 + __builtin_ctz(listed);
+        ++at;
+        listed &= listed - 1;
       }
     }
-    sum = wave_sum(sum);
-    if (lane == 0) c.w.sums[static_cast<int64_t>(r) * c.tiles + t] = sum;
+    sum = wave_scan(sum);
+    if (lane == kWave - 1) c.w.sums[static_cast<int64_t>(r) * c.tiles + t] = sum;
   }
 }
 
@@ -445,6 +548,7 @@ struct Choose {
   };
   Scan parts;
   uint32_t part[2][kWaves];
+  double steps[kSteps];
   unsigned long long wide;
   uint32_t at;
 };
@@ -569,13 +673,15 @@ __device__ unsigned long long last_place(const T* x, int vocab, const Border& b,
   return static_cast<unsigned long long>(~b.key) << 32 | sh.at;
 }
 
-template <typename T>
+// TILES: the weights are the tiles' own, each against its largest value.
+template <typename T, bool TILES>
 __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
   __shared__ Choose sh;
   extern __shared__ unsigned long long tiles[];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave, r = c.first + blockIdx.x, vocab = c.a.vocab;
   const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
-  const Row row = row_of(c, r, sh.part);
+  fill_steps(sh.steps, c.shift);
+  Row row = row_of(c, r, sh.steps, sh.part);
   const auto answer = [&](int token, float prob) {
     c.a.tokens[r] = token;
     if (c.a.prob) c.a.prob[r] = prob;
@@ -607,11 +713,10 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
   int turn = 0;
   unsigned long long end = ~0ull;  // the last kept token's place
   const auto kept = [&](float v, int i) -> unsigned long long {
-    if (place_of(v, i) > end) return 0;
     const double f = row.weight(v);
-    return f < row.least ? 0 : row.whole(f);
+    return place_of(v, i) > end || f < row.least ? 0 : row.whole(f);
   };
-  if (row.mode == kListed && c.w.plans[r].looked) {
+  if (!TILES && row.mode == kListed && c.w.plans[r].looked) {
     Border border{0, 0xFFFFFFFFu};
     if (row.k > 0) {
       unsigned long long n = 0, all;
@@ -636,44 +741,56 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
     if (border.key != 0) end = last_place(x, vocab, border, sh, turn);
     for (int t = w; t < c.tiles; t += kWaves) {
       unsigned long long sum = 0;
-      for (int n = 0; n < kRounds; ++n) {
-        float v[8];
-        const int i0 = t * kTile + 8 * (n * kWave + lane);
-        load8(x, i0, vocab, v);
+      float v[8];
+      const int i0 = t * kTile + 8 * lane;
+      load8(x, i0, vocab, v);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) sum += kept(v[e], i0 + e);
-      }
-      sum = wave_sum(sum);
-      if (lane == 0) tiles[t] = sum;
+      for (int e = 0; e < 8; ++e) sum += kept(v[e], i0 + e);
+      sum = wave_scan(sum);
+      if (lane == kWave - 1) tiles[t] = sum;
     }
     __syncthreads();
   } else {
-    for (int t = tid; t < c.tiles; t += kThreads) tiles[t] = c.w.sums[static_cast<int64_t>(r) * c.tiles + t];
-    if (row.mode == kListed && c.w.plans[r].count > 0) {
-      const Plan plan = c.w.plans[r];
-      int size = 2;
-      while (size < plan.count) size *= 2;
-      for (int i = tid; i < size; i += kThreads) {
-        unsigned long long v = ~0ull;
-        if (i < plan.count) {
-          const int at = c.w.list[static_cast<int64_t>(r) * kList + i];
-          v = place_of(get(x + at), at);
-        }
-        sh.list[i] = v;
+    for (int t = tid; t < c.tiles; t += kThreads) {
+      unsigned long long sum = c.w.sums[static_cast<int64_t>(r) * c.tiles + t];
+      if (TILES && sum) {  // against the row's largest value
+        const double f = row.weight(value_of(c.w.ends[static_cast<int64_t>(r) * c.tiles + t].x));
+        sum = static_cast<unsigned long long>(rint(static_cast<double>(sum) * ldexp(f, -c.shift)));
       }
-      // sorted by exchanges between partners at falling distances, in runs of rising length
-      for (int run = 2; run <= size; run *= 2)
-        for (int d = run / 2; d > 0; d /= 2) {
-          __syncthreads();
-          for (int q = tid; q < size / 2; q += kThreads) {
-            const int i = 2 * q - (q & (d - 1)), j = i + d;
-            const unsigned long long a = sh.list[i], b = sh.list[j];
-            if ((a > b) == ((i & run) == 0)) {
-              sh.list[i] = b;
-              sh.list[j] = a;
+      tiles[t] = sum;
+    }
+    if (!TILES && row.mode == kListed && c.w.plans[r].count > 0) {
+      const Plan plan = c.w.plans[r];
+      const auto nth = [&](int i) {
+        const int at = c.w.list[static_cast<int64_t>(r) * kList + i];
+        return place_of(get(x + at), at);
+      };
+      if (plan.count <= kThreads) {  // each one's number is how many lie before it
+        const unsigned long long mine = tid < plan.count ? nth(tid) : ~0ull;
+        unsigned long long* from = sh.list + kThreads;
+        from[tid] = mine;
+        __syncthreads();
+        int before = 0;
+        for (int i = 0; i < plan.count; ++i) before += from[i] < mine;
+        if (tid < plan.count) sh.list[before] = mine;
+      } else {
+        int size = 2 * kThreads;
+        while (size < plan.count) size *= 2;
+        for (int i = tid; i < size; i += kThreads) sh.list[i] = i < plan.count ? nth(i) : ~0ull;
+        // exchanges between partners at falling distances, in runs of rising length
+        for (int run = 2; run <= size; run *= 2)
+          for (int d = run / 2; d > 0; d /= 2) {
+            __syncthreads();
+            for (int q = tid; q < size / 2; q += kThreads) {
+              const int i = 2 * q - (q & (d - 1)), j = i + d;
+              const unsigned long long a = sh.list[i], b = sh.list[j];
+              if ((a > b) == ((i & run) == 0)) {
+                sh.list[i] = b;
+                sh.list[j] = a;
+              }
             }
           }
-        }
+      }
       __syncthreads();
       // eight tokens a thread, in order
       float v[8];
@@ -730,7 +847,7 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
   scan(total, sh.parts, turn, all);
   total = all;
   const float u = fminf(fmaxf(c.a.uniform[r], 0.f), 0x1.fffffep-1f);
-  const double goal = static_cast<double>(u) * static_cast<double>(total);
+  double goal = static_cast<double>(u) * static_cast<double>(total);
   for (int t0 = 0;; t0 += kThreads) {
     const unsigned long long s = t0 + tid < c.tiles ? tiles[t0 + tid] : 0;
     const unsigned long long upto = before + scan(s, sh.parts, turn, all);
@@ -743,22 +860,21 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
   }
   __syncthreads();
   // and the token in it
-  static_assert(kTile == 2 * kThreads, "two tokens a thread");
-  const int i = sh.at * kTile + 2 * tid;
-  float v[2];
-  unsigned long long k[2];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    v[e] = i + e < vocab ? get(x + i + e) : -__builtin_inff();
-    k[e] = i + e < vocab ? kept(v[e], i + e) : 0;
+  static_assert(kTile == kThreads, "a token a thread");
+  const int tile = sh.at, i = tile * kTile + tid;
+  const float v = i < vocab ? get(x + i) : -__builtin_inff();
+  before = sh.wide;
+  double chance = 0.0;
+  if (i < vocab && c.a.prob) chance = row.weight(v) / static_cast<double>(total);
+  if constexpr (TILES) {  // in the tile's own weights
+    const double own = static_cast<double>(c.w.sums[static_cast<int64_t>(r) * c.tiles + tile]);
+    goal = fmin((goal - static_cast<double>(before)) * (own / static_cast<double>(tiles[tile])), own - 1.0);
+    before = 0;
+    row.against(value_of(c.w.ends[static_cast<int64_t>(r) * c.tiles + tile].x));
   }
-  unsigned long long upto = sh.wide + scan(k[0] + k[1], sh.parts, turn, all) - k[0] - k[1];
-#pragma unroll
-  for (int e = 0; e < 2; ++e) {
-    upto += k[e];
-    if (k[e] != 0 && static_cast<double>(upto) > goal && static_cast<double>(upto - k[e]) <= goal)
-      answer(i + e, static_cast<float>(row.weight(v[e]) / ldexp(static_cast<double>(total), -row.shift)));
-  }
+  const unsigned long long k = i < vocab ? kept(v, i) : 0;
+  const unsigned long long upto = before + scan(k, sh.parts, turn, all);
+  if (k != 0 && static_cast<double>(upto) > goal && static_cast<double>(upto - k) <= goal) answer(i, static_cast<float>(chance));
 }
 
 // ------------------------------------------------------------------------------ launch
@@ -788,18 +904,23 @@ Sizes sizes(int32_t rows, int32_t vocab) {
 }
 
 template <typename T>
-hipError_t launch_t(Call c, bool filters, hipStream_t s) {
-  const int blocks = (c.tiles + kWaves - 1) / kWaves;
-  const int64_t most = (int64_t{1} << 31) / kThreads / blocks;  // rows of a launch
+hipError_t launch_t(Call c, hipStream_t s) {
+  const int64_t most = (int64_t{1} << 31) / kThreads / c.groups;  // rows of a launch
   const int rows = c.a.rows;
   const size_t lds = static_cast<size_t>(c.tiles) * 8;
+  const bool borders = c.a.top_k || c.a.top_p, own = !borders && !c.a.min_p;
   for (int64_t f = 0; f < rows; f += most) {
     c.first = static_cast<int>(f);
     const unsigned n = static_cast<unsigned>(rows - f < most ? rows - f : most);
-    sample_extremes_kernel<T><<<n * blocks, kThreads, 0, s>>>(c);
-    sample_weigh_kernel<T><<<n * c.groups, kThreads, 0, s>>>(c);
-    if (filters) sample_gather_kernel<T><<<n * c.groups, kThreads, 0, s>>>(c);
-    sample_choose_kernel<T><<<n, kThreads, lds, s>>>(c);
+    if (own) {
+      sample_tiles_kernel<T><<<n * c.groups, kThreads, 0, s>>>(c);
+      sample_choose_kernel<T, true><<<n, kThreads, lds, s>>>(c);
+    } else {
+      sample_extremes_kernel<T><<<n * c.groups, kThreads, 0, s>>>(c);
+      sample_weigh_kernel<T><<<n * c.groups, kThreads, 0, s>>>(c);
+      if (borders) sample_gather_kernel<T><<<n * c.groups, kThreads, 0, s>>>(c);
+      sample_choose_kernel<T, false><<<n, kThreads, lds, s>>>(c);
+    }
     if (const hipError_t e = hipGetLastError()) return e;
   }
   return hipSuccess;
@@ -826,11 +947,11 @@ hipError_t launch_sample(const SampleArgs& a, hipStream_t s) {
   int bits = 0;
   while ((1 << bits) < a.vocab) ++bits;
   c.shift = 62 - bits < 51 ? 62 - bits : 51;
-  // about four workgroups a CU in the passes that add up a row's bins
+  // about four workgroups a CU in the passes over all tokens
   const int blocks = (z.tiles + kWaves - 1) / kWaves;
   const int want = (1024 + a.rows - 1) / a.rows;
   c.groups = want < blocks ? want : blocks;
-  return a.bf16 ? launch_t<uint16_t>(c, filters, s) : launch_t<float>(c, filters, s);
+  return a.bf16 ? launch_t<uint16_t>(c, s) : launch_t<float>(c, s);
 }
 
 }  // namespace gdn

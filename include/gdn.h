@@ -570,8 +570,8 @@ gdn_status gdn_block_norm(const gdn_block_norm_dims* dims, const void* x, int64_
  *   prob     w_token / that sum
  * T <= 0 (or NaN): the lowest index that has m, prob 1. A NaN logit counts as minus infinity; a row with nothing above
  * minus infinity gives token -1, prob 0. Beside an x of plus infinity only others like it weigh anything.
- * Weights are whole multiples of 2^-S with S = min(51, 62 - ceil(log2 vocab)): smaller ones are 0, sums are exact, and a row's
- * token depends on nothing else in the call.
+ * Weights are whole multiples of 2^-S (with temperature alone: of 2^-S of the largest among 512 neighbours) with
+ * S = min(51, 62 - ceil(log2 vocab)): smaller ones are 0, and a row's token depends on nothing else in the call.
  *
  *  logits     [rows][vocab] in dtype (a gdn_dtype), row stride in elements, any alignment of the type.
  *  temperature, top_p, min_p  device fp32 [rows], top_k device int32 [rows]; NULL, or an entry that filters nothing
@@ -579,7 +579,7 @@ gdn_status gdn_block_norm(const gdn_block_norm_dims* dims, const void* x, int64_
  *             p <= 0 keeps the first of the order alone.
  *  uniform    device fp32 [rows] in [0, 1); others count as the nearest number there, NaN as 0.
  *  tokens     device int32 [rows].   prob: device fp32 [rows], or NULL.
- *  vocab      1 .. 2^21.   workspace: gdn_sample_workspace_size(rows, vocab) bytes, 256-byte aligned, contents ignored;
+ *  vocab      1 .. 2^20.   workspace: gdn_sample_workspace_size(rows, vocab) bytes, 256-byte aligned, contents ignored;
  *             may be NULL where that is 0.
  */
 gdn_status gdn_sample_workspace_size(int32_t rows, int32_t vocab, size_t* bytes);

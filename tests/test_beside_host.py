@@ -138,7 +138,7 @@ SAMPLE = dict(logits=FAKE, stride=1000, dtype=0, rows=4, vocab=1000, temperature
 
 
 @pytest.mark.parametrize("kw,want", [
-    (dict(rows=-1), SHAPE), (dict(vocab=0), SHAPE), (dict(vocab=(1 << 21) + 1, stride=1 << 25), SHAPE), (dict(dtype=2), DTYPE),
+    (dict(rows=-1), SHAPE), (dict(vocab=0), SHAPE), (dict(vocab=(1 << 20) + 1, stride=1 << 25), SHAPE), (dict(dtype=2), DTYPE),
     (dict(logits=None), NULL), (dict(uniform=None), NULL), (dict(tokens=None), NULL), (dict(stride=999), SHAPE), (dict(stride=-1000), SHAPE),
     (dict(logits=FAKE + 2), ALIGN), (dict(dtype=1, logits=FAKE + 1), ALIGN), (dict(workspace=FAKE + 16), ALIGN),
 ])

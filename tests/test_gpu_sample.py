@@ -1,8 +1,7 @@
 """gdn_sample against its definition in 64 bits (tests/sample_ref.py): tokens equal, probabilities within 2^-23.
 
-Weights are multiples of 2^-S of the largest, S >= 41 (44 for 2^18 tokens): a border between two tokens lies off by at most
-vocab 2^-(S+1) of the largest weight, under 2^-25 of the sum for vocabularies up to 2^18 (S = 62 - log2(vocab)). A test whose random number falls nearer
-than that to a border of its distribution would prove nothing; the fixed seeds have none (asserted)."""
+A random number that falls nearer to a border of its distribution than the weights' whole multiples allow (sample_ref.border)
+would prove nothing; the fixed seeds have none (asserted)."""
 
 import numpy as np
 import pytest
@@ -37,7 +36,7 @@ def check(x, u, t=None, k=None, p=None, least=None):
         v = float(np.float32(u[r]))
         want, prob = sample(h[r], v, **kw)
         if v > 0 and v < 1:
-            assert border(h[r], v, **kw) > 2.0 ** -25 or h.shape[1] == 1, f"row {r}: choose another seed"
+            assert border(h[r], v, **kw) > 1, f"row {r}: choose another seed"
         assert got[r] == want, f"row {r}: {got[r]}, not {want} ({kw}, u {u[r]})"
         assert abs(chance[r] - prob) <= 2.0 ** -23 * prob, f"row {r}"
     return got
@@ -174,8 +173,8 @@ def test_offsets_past_32_bits():
 
 
 def test_the_largest_vocabulary():
-    announce("sample: 2^21 tokens")
-    x, n = logits(2, 1 << 21, seed=30, std=1.0), numbers(2, 31)
+    announce("sample: 2^20 tokens")
+    x, n = logits(2, 1 << 20, seed=30, std=1.0), numbers(2, 31)
     check(x, n["u"], t=n["t"], k=[0, 5000], p=n["p"])
     check(x, n["u"])
 
