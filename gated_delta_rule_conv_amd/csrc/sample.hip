@@ -1,6 +1,6 @@
 // One token a row of logits from a given random number, gfx950 (include/gdn.h, gdn_sample).
 //
-// Weights are whole numbers: w = round(2^S e^((x - m) / T)), the exponential in 64 bits, S = 62 minus
+// Weights are whole numbers: w = round(2^S e^((x - m) / T)), the exponential in 64 bits to 2^-39, S = 62 minus
 // the bits of the vocabulary's size, at most 51 (44 for 2^18 tokens). Their sums are then exact in any order, atomic or
 // not, so a row's token depends on nothing but the row, and a border (top_p's, or the random number's) is met within
 // 2^-S of the largest weight a token. Tokens whose weight is 0 do not count at all: they come last in the order.
@@ -94,9 +94,11 @@ enum Mode { kNone, kLikeliest, kPlain, kListed };
 
 // What a row's tokens are judged by.
 struct Row {
-  float most;          // the largest value
+  float most;          // the largest value; 0 where that is an infinity, whose tokens then have 0 and all others minus infinity
+  bool infinite;
+  double base;         // most
   double per;          // 32 log2(e) / T
-  double off;          // - most per
+  double low;          // 32 log2 of what is surely rounded to 0
   float far;           // a distance from the largest value beyond which a weight is surely 0
   float bins;          // bins by distance
   double least;        // 2^S min_p, min_p at most 1
@@ -107,28 +109,34 @@ struct Row {
   int mode;            // kNone, kLikeliest, kPlain, or kListed for rows with top_k or top_p
 
   __device__ __forceinline__ void against(float largest) {
-    most = largest;
-    off = -static_cast<double>(largest) * per;
-    // (infinite T: all finite distances; beside an infinity nothing else weighs anything)
-    far = largest < __builtin_inff() ? static_cast<float>((shift + 1.5) * kSteps / per) : -1.f;
+    infinite = largest == __builtin_inff();
+    most = infinite ? 0.f : largest;
+    base = most;
+    far = static_cast<float>((shift + 1.5) * kSteps / per);  // (infinite T: all finite distances)
+  }
+  __device__ __forceinline__ float seen(float x) const { return !infinite ? x : x == __builtin_inff() ? 0.f : -__builtin_inff(); }
+  template <int N>
+  __device__ __forceinline__ void see(float (&v)[N]) const {
+    if (infinite) {  // (the row agrees)
+#pragma unroll
+      for (int e = 0; e < N; ++e) v[e] = seen(v[e]);
+    }
   }
   // 2^S e^((x - most) / T): t = 32 log2 of the exponential, its nearest whole number n and the rest f, |f| <= 1/2;
-  // 2^(t / 32) = 2^(n / 32) e^(f ln 2 / 32), the series good to 2^-48.
+  // 2^(t / 32) = 2^(n / 32) e^(f ln 2 / 32), the series good to 2^-39. (A NaN, also from minus infinity at an infinite T,
+  // is dropped by the largest of it and `low`.)
   __device__ __forceinline__ double weight(float x) const {
-    const double t = fma(static_cast<double>(x), per, off);
+    constexpr double c = 0.693147180559945309417 / kSteps;
+    const double t = __builtin_fmax((static_cast<double>(x) - base) * per, low);
     const double whole = t + 0x1.8p52;
     const int n = static_cast<int>(__double_as_longlong(whole));
-    const double f = (t - (whole - 0x1.8p52)) * (0.693147180559945309417 / kSteps);
-    double s = fma(f, 1.0 / 120.0, 1.0 / 24.0);
-    s = fma(s, f, 1.0 / 6.0);
-    s = fma(s, f, 0.5);
+    const double f = t - (whole - 0x1.8p52);
+    double s = fma(f, c * c * c * c / 24.0, c * c * c / 6.0);
+    s = fma(s, f, c * c / 2.0);
+    s = fma(s, f, c);
     s = fma(s, f, 1.0);
-    s = fma(s, f, 1.0);
-    const long long step = __double_as_longlong(steps[n & (kSteps - 1)]) + (static_cast<long long>(n >> 5) << 52);
-    const double w = __longlong_as_double(step) * s;
-    // (a NaN is not near, nor is minus infinity at an infinite T; whatever was formed from them is dropped)
-    const bool near = most - x <= far && x > -__builtin_inff();
-    return x == most ? __longlong_as_double(static_cast<long long>(shift + 1023) << 52) : near ? w : 0.0;
+    const double step = steps[n & (kSteps - 1)];
+    return s * __hiloint2double(__double2hiint(step) + ((n & ~(kSteps - 1)) << 15), __double2loint(step));
   }
   // rounded: the low bits of 2^52 + w
   __device__ __forceinline__ static unsigned long long whole(double w) {
@@ -138,9 +146,16 @@ struct Row {
   __device__ __forceinline__ int bin(float x) const {
     const float d = most - x;
     const int b = static_cast<int>(fminf(d * bins, kBins - 1.0f));
-    return x == most ? 0 : d <= far && x > -__builtin_inff() ? b : -1;
+    return d <= far && x > -__builtin_inff() ? b : -1;
   }
 };
+// the sum of eight tokens' weights, rounded (the bits of 2^52 + w, less those of the eight 2^52)
+__device__ __forceinline__ unsigned long long sum_of(const Row& row, const float (&v)[8]) {
+  unsigned long long sum = 0 - 8 * 0x4330000000000000ull;
+#pragma unroll
+  for (int e = 0; e < 8; ++e) sum += __double_as_longlong(row.weight(v[e]) + 0x1p52);
+  return sum;
+}
 
 // the order of tokens: lower numbers first
 __device__ __forceinline__ unsigned long long place_of(float x, int i) {
@@ -243,6 +258,7 @@ __device__ __forceinline__ Row parameters(const Call& c, int r, const double* st
   const float p = c.a.top_p ? c.a.top_p[r] : 1.f;
   row.per = 1.44269504088896340736 * kSteps / static_cast<double>(t);
   row.shift = c.shift;
+  row.low = -kSteps * (c.shift + 2.0);
   row.steps = steps;
   row.least = ldexp(min_p > 0.f ? (min_p < 1.f ? min_p : 1.0) : 0.0, c.shift);
   if (row.k < 0 || row.k >= c.a.vocab) row.k = 0;
@@ -274,7 +290,7 @@ __device__ __forceinline__ Row row_of(const Call& c, int r, const double* steps,
     least = min(least, part[1][w]);
   }
   row.against(value_of(most));
-  const float range = fminf(row.most - value_of(least), row.far);
+  const float range = row.infinite ? 0.f : fminf(row.most - value_of(least), row.far);
   row.bins = range > 0.f ? fminf(static_cast<float>(kBins) / range, 1e30f) : 0.f;
   if (most <= kLowest) row.mode = kNone;
   return row;
@@ -337,16 +353,15 @@ __global__ __launch_bounds__(kThreads) void sample_tiles_kernel(Call c) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = next[e];
     load8(x, min(t + step, c.tiles - 1) * kTile + 8 * lane, c.a.vocab, next);
-    uint32_t most = kLowest;
+    float top = -__builtin_inff();
 #pragma unroll
-    for (int e = 0; e < 8; ++e) most = max(most, key_of(v[e]));
-    most = wave_max(most);
+    for (int e = 0; e < 8; ++e) top = fmaxf(top, v[e]);  // (of a NaN and a number: the number)
+    const uint32_t most = wave_max(key_of(top));
     unsigned long long sum = 0;
     if (row.mode == kPlain && most > kLowest) {
       row.against(value_of(most));
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum += row.whole(row.weight(v[e]));
-      sum = wave_scan(sum);
+      row.see(v);
+      sum = wave_scan(sum_of(row, v));
     }
     if (lane == kWave - 1) {
       c.w.ends[static_cast<int64_t>(r) * c.tiles + t] = uint2{most, 0xFFFFFFFFu};
@@ -381,6 +396,7 @@ __global__ __launch_bounds__(kThreads) void sample_weigh_kernel(Call c) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = next[e];
     load8(x, min(t + step, c.tiles - 1) * kTile + 8 * lane, c.a.vocab, next);
+    row.see(v);
     if (plain) {
       unsigned long long sum = 0;
 #pragma unroll
@@ -501,6 +517,7 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(Call c) {
 #pragma unroll
     for (int e = 0; e < 8; ++e) v[e] = next[e];
     load8(x, min(t + step, c.tiles - 1) * kTile + 8 * lane, c.a.vocab, next);
+    row.see(v);
     const int i0 = t * kTile + 8 * lane;
     uint32_t stays = 0, listed = 0;  // bits of the lane's tokens
 #pragma unroll
@@ -580,6 +597,7 @@ __device__ Border look_up(const T* x, int vocab, const Row& row, const Border& l
     for (int i0 = 8 * tid; i0 < vocab; i0 += 8 * kThreads) {
       float v[8];
       load8(x, i0, vocab, v);
+      row.see(v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
         if (row.bin(v[e]) < 0) continue;
@@ -651,7 +669,7 @@ __device__ Border look_up(const T* x, int vocab, const Row& row, const Border& l
 
 // The place of the last token up to a border: the equal-th in index order of those with its key.
 template <typename T>
-__device__ unsigned long long last_place(const T* x, int vocab, const Border& b, Choose& sh, int& turn) {
+__device__ unsigned long long last_place(const T* x, int vocab, const Row& row, const Border& b, Choose& sh, int& turn) {
   unsigned long long seen = 0, all;
   __syncthreads();
   if (threadIdx.x == 0) sh.at = 0xFFFFFFFFu;
@@ -659,6 +677,7 @@ __device__ unsigned long long last_place(const T* x, int vocab, const Border& b,
     const int i = i0 + 8 * threadIdx.x;
     float v[8];
     load8(x, i, vocab, v);
+    row.see(v);
     unsigned long long mine = 0;
 #pragma unroll
     for (int e = 0; e < 8; ++e) mine += i + e < vocab && key_of(v[e]) == b.key;
@@ -693,7 +712,7 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
   if (row.mode == kLikeliest) {
     if (tid == 0) sh.at = 0xFFFFFFFFu;
     __syncthreads();
-    const uint32_t most = key_of(row.most);
+    const uint32_t most = key_of(row.infinite ? __builtin_inff() : row.most);
     for (int t = tid; t < c.tiles; t += kThreads)
       if (c.w.ends[static_cast<int64_t>(r) * c.tiles + t].x == most) {
         atomicMin(&sh.at, static_cast<uint32_t>(t));
@@ -730,6 +749,7 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
       for (int i0 = 8 * tid; i0 < vocab; i0 += 8 * kThreads) {
         float v[8];
         load8(x, i0, vocab, v);
+        row.see(v);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
           if (!cut || key_of(v[e]) > border.key) n += row.whole(row.weight(v[e]));
@@ -738,12 +758,13 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
       if (cut) all += border.equal * row.whole(row.weight(value_of(border.key)));
       border = look_up<T, false>(x, vocab, row, border, 0, static_cast<double>(row.p) * static_cast<double>(all), sh, turn);
     }
-    if (border.key != 0) end = last_place(x, vocab, border, sh, turn);
+    if (border.key != 0) end = last_place(x, vocab, row, border, sh, turn);
     for (int t = w; t < c.tiles; t += kWaves) {
       unsigned long long sum = 0;
       float v[8];
       const int i0 = t * kTile + 8 * lane;
       load8(x, i0, vocab, v);
+      row.see(v);
 #pragma unroll
       for (int e = 0; e < 8; ++e) sum += kept(v[e], i0 + e);
       sum = wave_scan(sum);
@@ -754,7 +775,7 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
     for (int t = tid; t < c.tiles; t += kThreads) {
       unsigned long long sum = c.w.sums[static_cast<int64_t>(r) * c.tiles + t];
       if (TILES && sum) {  // against the row's largest value
-        const double f = row.weight(value_of(c.w.ends[static_cast<int64_t>(r) * c.tiles + t].x));
+        const double f = row.weight(row.seen(value_of(c.w.ends[static_cast<int64_t>(r) * c.tiles + t].x)));
         sum = static_cast<unsigned long long>(rint(static_cast<double>(sum) * ldexp(f, -c.shift)));
       }
       tiles[t] = sum;
@@ -763,7 +784,7 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
       const Plan plan = c.w.plans[r];
       const auto nth = [&](int i) {
         const int at = c.w.list[static_cast<int64_t>(r) * kList + i];
-        return place_of(get(x + at), at);
+        return place_of(row.seen(get(x + at)), at);
       };
       if (plan.count <= kThreads) {  // each one's number is how many lie before it
         const unsigned long long mine = tid < plan.count ? nth(tid) : ~0ull;
@@ -862,17 +883,17 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
   // and the token in it
   static_assert(kTile == kThreads, "a token a thread");
   const int tile = sh.at, i = tile * kTile + tid;
-  const float v = i < vocab ? get(x + i) : -__builtin_inff();
+  const float own_v = i < vocab ? get(x + i) : -__builtin_inff();
   before = sh.wide;
   double chance = 0.0;
-  if (i < vocab && c.a.prob) chance = row.weight(v) / static_cast<double>(total);
+  if (i < vocab && c.a.prob) chance = row.weight(row.seen(own_v)) / static_cast<double>(total);
   if constexpr (TILES) {  // in the tile's own weights
     const double own = static_cast<double>(c.w.sums[static_cast<int64_t>(r) * c.tiles + tile]);
     goal = fmin((goal - static_cast<double>(before)) * (own / static_cast<double>(tiles[tile])), own - 1.0);
     before = 0;
     row.against(value_of(c.w.ends[static_cast<int64_t>(r) * c.tiles + tile].x));
   }
-  const unsigned long long k = i < vocab ? kept(v, i) : 0;
+  const unsigned long long k = i < vocab ? kept(row.seen(own_v), i) : 0;
   const unsigned long long upto = before + scan(k, sh.parts, turn, all);
   if (k != 0 && static_cast<double>(upto) > goal && static_cast<double>(upto - k) <= goal) answer(i, static_cast<float>(chance));
 }

@@ -48,11 +48,11 @@ def sample(x, u, **kw):
 def border(x, u, **kw):
     """How near u is to a border of the distribution over how near two right answers can be: a weight is a multiple
     of 2^-S of the largest (S = min(51, 62 - log2 vocab)), so a border lies off by at most vocab 2^-(S+1) of that, twice
-    that where tiles are rounded too, and 2^-46 of the sum for the exponentials. Below 1 either neighbour is right.
+    that where tiles are rounded too, and 2^-38 of the sum for the exponentials (good to 2^-39). Below 1 either neighbour is right.
     Equal weights are whole multiples: nothing is lost."""
     ids, w = distribution(x, **kw)
     if ids.size == 0 or (w == w[0]).all():
         return np.inf
     shift = min(51, 62 - max(0, int(np.ceil(np.log2(x.size)))))
-    off = 2 * x.size * 2.0 ** -(shift + 1) * w.max() / w.sum() + 2.0 ** -46
+    off = 2 * x.size * 2.0 ** -(shift + 1) * w.max() / w.sum() + 2.0 ** -38
     return float(np.abs(np.cumsum(w) / w.sum() - u).min()) / off
