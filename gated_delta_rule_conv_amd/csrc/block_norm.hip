@@ -3,7 +3,8 @@
 //
 // Bound by HBM: x, r and the gate are read once, h and y written once. A row lives in the registers of W waves
 // (lane c of the row's 64 W: values [8 (c + 64 W t), + 8), t < V), so both norms are sums over registers
-// and h goes from its sum to its norm unrounded.
+// and h goes from its sum to its norm unrounded. x, r and the gate are loaded as they come before anything is computed, which is
+// why their types are compiled in; the parameters come from L2 while the sums run.
 
 #include "conv_taps.h"
 #include "device_common.h"
@@ -15,24 +16,79 @@
 namespace gdn {
 namespace {
 
-// values [k, k + 8) of a row of n
-__device__ __forceinline__ void load8(const void* p, int bf16, int64_t off, int k, int n, float (&v)[8]) {
-  const f32x4 lo = load_any(p, bf16, off, k, n), hi = load_any(p, bf16, off, k + 4, n);
+typedef uint32_t uu32x4 __attribute__((ext_vector_type(4), aligned(2)));
+struct None {};
+
+// 8 values as they lie in memory.
+template <typename T>
+struct Raw8;
+template <>
+struct Raw8<uint16_t> {
+  uu32x4 r;
+  __device__ __forceinline__ void load(const uint16_t* p) { r = *reinterpret_cast<const uu32x4*>(p); }
+  __device__ __forceinline__ void set(int e, uint16_t v) {
+    const uint32_t old = r[e / 2];
+    r[e / 2] = e % 2 ? (old & 0xFFFFu) | static_cast<uint32_t>(v) << 16 : (old & 0xFFFF0000u) | v;
+  }
+  __device__ __forceinline__ void clear() { r = uu32x4{0, 0, 0, 0}; }
+  __device__ __forceinline__ float operator[](int e) const {
+    return __uint_as_float(e % 2 ? r[e / 2] & 0xFFFF0000u : r[e / 2] << 16);
+  }
+};
+template <>
+struct Raw8<float> {
+  uf32x4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = *reinterpret_cast<const uf32x4*>(p);
+    b = *reinterpret_cast<const uf32x4*>(p + 4);
+  }
+  __device__ __forceinline__ void set(int e, float v) {
+    if (e < 4) a[e] = v;
+    else b[e - 4] = v;
+  }
+  __device__ __forceinline__ void clear() { a = b = uf32x4{0.f, 0.f, 0.f, 0.f}; }
+  __device__ __forceinline__ float operator[](int e) const { return e < 4 ? a[e] : b[e - 4]; }
+};
+template <>
+struct Raw8<None> {
+  __device__ __forceinline__ float operator[](int) const { return 1.f; }
+};
+
+// values [k, k + 8) of a row of n. EIGHTS: 8 divides n, so that a lane has all of them or (k >= n) none: it reads the row's
+// first ones then, and what it forms of them is dropped.
+template <bool EIGHTS, typename T>
+__device__ __forceinline__ void load8(Raw8<T>& to, const void* row, int k, int n) {
+  if constexpr (sizeof(Raw8<T>) >= 16) {
+    const T* p = static_cast<const T*>(row);
+    if constexpr (EIGHTS) {
+      to.load(p + (k < n ? k : 0));
+    } else if (k + 8 <= n) {
+      to.load(p + k);
+    } else {
+      to.clear();
 #pragma unroll
-  for (int e = 0; e < 4; ++e) {
-    v[e] = lo[e];
-    v[4 + e] = hi[e];
+      for (int e = 0; e < 8; ++e)
+        if (k + e < n) to.set(e, p[k + e]);
+    }
   }
 }
 
-__device__ __forceinline__ void store8(void* p, int bf16, int64_t off, int k, int n, const float (&v)[8]) {
-  const f32x4 lo = {v[0], v[1], v[2], v[3]}, hi = {v[4], v[5], v[6], v[7]};
-  if (bf16) {
-    store4u(static_cast<uint16_t*>(p) + off, k, n, lo);
-    store4u(static_cast<uint16_t*>(p) + off, k + 4, n, hi);
-  } else {
-    store4u(static_cast<float*>(p) + off, k, n, lo);
-    store4u(static_cast<float*>(p) + off, k + 4, n, hi);
+template <bool EIGHTS, typename T>
+__device__ __forceinline__ void store8(T* p, int k, int n, const float (&v)[8]) {
+  if (EIGHTS ? k < n : k + 8 <= n) {
+    if constexpr (sizeof(T) == 2) {
+      uu32x4 r;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) r[e] = static_cast<uint32_t>(to_bf16(v[2 * e])) | static_cast<uint32_t>(to_bf16(v[2 * e + 1])) << 16;
+      *reinterpret_cast<uu32x4*>(p + k) = r;
+    } else {
+      *reinterpret_cast<uf32x4*>(p + k) = uf32x4{v[0], v[1], v[2], v[3]};
+      *reinterpret_cast<uf32x4*>(p + k + 4) = uf32x4{v[4], v[5], v[6], v[7]};
+    }
+  } else if constexpr (!EIGHTS) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e)
+      if (k + e < n) put(p + k + e, v[e]);
   }
 }
 
@@ -48,10 +104,11 @@ struct Gather {
   template <typename F>
   __device__ __forceinline__ float operator()(float v, F join) {
     if constexpr (W == 1) return v;
-    const int wave = threadIdx.x / kWave;
     turn ^= 1;  // (the readers of the last turn's values need not be done)
-    if (threadIdx.x % kWave == 0) part[turn][wave] = v;
-    __syncthreads();
+    if (threadIdx.x % kWave == 0) part[turn][threadIdx.x / kWave] = v;
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");  // (loads stay in flight)
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
     float r = part[turn][0];
 #pragma unroll
     for (int w = 1; w < W; ++w) r = join(r, part[turn][w]);
@@ -59,7 +116,7 @@ struct Gather {
   }
 };
 
-// v -> (v - mean) rs over a row: the root mean square's inverse, or, centered, the standard deviation's.
+// v -> (v - mean) rs over a row: the root mean square's inverse, or, centered, the standard deviation's. v is 0 past the row's end.
 template <int W, int V>
 __device__ __forceinline__ void normalise(float (&v)[V][8], const BlockNormArgs& a, int c, Gather<W>& gather) {
   const auto add = [](float x, float y) { return x + y; };
@@ -108,86 +165,116 @@ __device__ __forceinline__ void normalise(float (&v)[V][8], const BlockNormArgs&
     for (int e = 0; e < 8; ++e) v[t][e] = (v[t][e] - mean) * rs;
 }
 
-template <int W, int V>
+template <typename TX, typename TR, typename TZ, int W, int V, bool EIGHTS>
 __global__ __launch_bounds__((W < 4 ? 4 : W) * kWave) void block_norm_kernel(BlockNormArgs a) {
   __shared__ float part[2][16];
+  static_assert(W == 1 || W >= 4, "whole workgroups, or waves on their own");
   Gather<W> gather{part};
   constexpr int ROWS = W < 4 ? 4 / W : 1;
   const int64_t row = static_cast<int64_t>(blockIdx.x) * ROWS + (ROWS > 1 ? threadIdx.x / (W * kWave) : 0);
   if (row >= a.rows) return;  // (W = 1: no barrier follows)
   const int c = threadIdx.x % (W * kWave), n = a.width;
   const auto at = [&](int t) { return 8 * (c + W * kWave * t); };
+  const auto row_of = [&](const auto* p, int64_t stride) { return p + row * stride; };
+  Raw8<TX> x[V];
+  Raw8<TZ> z[V];
+  Raw8<TR> r[V];
+#pragma unroll
+  for (int t = 0; t < V; ++t) load8<EIGHTS>(x[t], row_of(static_cast<const TX*>(a.x), a.x_stride), at(t), n);
+  if constexpr (sizeof(TZ) > 1) {
+#pragma unroll
+    for (int t = 0; t < V; ++t) load8<EIGHTS>(z[t], row_of(static_cast<const TZ*>(a.gate), a.gate_stride), at(t), n);
+  }
+  if (a.residual) {
+#pragma unroll
+    for (int t = 0; t < V; ++t) load8<EIGHTS>(r[t], row_of(static_cast<const TR*>(a.residual), a.residual_stride), at(t), n);
+  } else {
+#pragma unroll
+    for (int t = 0; t < V; ++t) r[t].clear();
+  }
   float v[V][8];
 #pragma unroll
-  for (int t = 0; t < V; ++t) load8(a.x, a.x_bf16, row * a.x_stride, at(t), n, v[t]);
-  const auto apply = [&](const void* w, const void* b) {
-    if (w) {
+  for (int t = 0; t < V; ++t)
+#pragma unroll
+    for (int e = 0; e < 8; ++e) v[t][e] = !EIGHTS || at(t) < n ? x[t][e] : 0.f;
+  // v = v w + b, where they are given
+  const auto affine = [&](const void* w, const void* b) {
+    const auto with = [&](auto zero, const void* p, auto join) {
+      using T = decltype(zero);
 #pragma unroll
       for (int t = 0; t < V; ++t) {
-        float p[8];
-        load8(w, a.param_bf16, 0, at(t), n, p);
+        Raw8<T> q;
+        load8<EIGHTS>(q, p, at(t), n);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) v[t][e] *= p[e];
+        for (int e = 0; e < 8; ++e) v[t][e] = join(v[t][e], q[e]);
       }
-    }
-    if (b) {
-#pragma unroll
-      for (int t = 0; t < V; ++t) {
-        float p[8];
-        load8(b, a.param_bf16, 0, at(t), n, p);
-#pragma unroll
-        for (int e = 0; e < 8; ++e) v[t][e] += p[e];
-      }
-    }
+    };
+    const auto times = [](float p, float q) { return p * q; };
+    const auto plus = [](float p, float q) { return p + q; };
+    if (w) a.param_bf16 ? with(uint16_t{}, w, times) : with(float{}, w, times);
+    if (b) a.param_bf16 ? with(uint16_t{}, b, plus) : with(float{}, b, plus);
   };
   if (a.post) {
     normalise<W, V>(v, a, c, gather);
-    apply(a.post_weight, a.post_bias);
+    affine(a.post_weight, a.post_bias);
   }
-  if (a.gate) {
+  if constexpr (sizeof(TZ) > 1) {
+    const auto gate = [&](auto act) {
 #pragma unroll
-    for (int t = 0; t < V; ++t) {
-      float z[8];
-      load8(a.gate, a.gate_bf16, row * a.gate_stride, at(t), n, z);
+      for (int t = 0; t < V; ++t)
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        v[t][e] *= a.activation == GDN_ACT_NONE ? z[e] : a.activation == GDN_ACT_SILU ? silu(z[e]) : sigmoid(z[e]);
-    }
+        for (int e = 0; e < 8; ++e) v[t][e] *= act(z[t][e]);
+    };
+    if (a.activation == GDN_ACT_NONE) gate([](float p) { return p; });
+    else if (a.activation == GDN_ACT_SILU) gate([](float p) { return silu(p); });
+    else gate([](float p) { return sigmoid(p); });
   }
 #pragma unroll
   for (int t = 0; t < V; ++t) {
-    float r[8] = {};
-    if (a.residual) load8(a.residual, a.residual_bf16, row * a.residual_stride, at(t), n, r);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) v[t][e] = at(t) + e < n ? fmaf(a.scale, v[t][e], r[e]) : 0.f;
-    if (a.h) store8(a.h, a.residual_bf16, row * a.h_stride, at(t), n, v[t]);
+    for (int e = 0; e < 8; ++e) v[t][e] = at(t) + (EIGHTS ? 0 : e) < n ? fmaf(a.scale, v[t][e], r[t][e]) : 0.f;
+    if (a.h) store8<EIGHTS>(static_cast<TR*>(a.h) + row * a.h_stride, at(t), n, v[t]);
   }
   if (!a.y) return;
   normalise<W, V>(v, a, c, gather);
-  apply(a.pre_weight, a.pre_bias);
+  affine(a.pre_weight, a.pre_bias);
 #pragma unroll
-  for (int t = 0; t < V; ++t) store8(a.y, a.y_bf16, row * a.y_stride, at(t), n, v[t]);
+  for (int t = 0; t < V; ++t) {
+    if (a.y_bf16) store8<EIGHTS>(static_cast<uint16_t*>(a.y) + row * a.y_stride, at(t), n, v[t]);
+    else store8<EIGHTS>(static_cast<float*>(a.y) + row * a.y_stride, at(t), n, v[t]);
+  }
 }
 
-template <int W, int V>
+template <typename TX, typename TR, typename TZ, int W, int V, bool EIGHTS>
 hipError_t launch_v(const BlockNormArgs& a, hipStream_t s) {
   constexpr int rows = W < 4 ? 4 / W : 1;
-  block_norm_kernel<W, V><<<static_cast<unsigned>((a.rows + rows - 1) / rows), (W < 4 ? 4 : W) * kWave, 0, s>>>(a);
+  block_norm_kernel<TX, TR, TZ, W, V, EIGHTS>
+      <<<static_cast<unsigned>((a.rows + rows - 1) / rows), (W < 4 ? 4 : W) * kWave, 0, s>>>(a);
   return hipGetLastError();
 }
 
-}  // namespace
-
-namespace {
-hipError_t launch_rows(const BlockNormArgs& a, hipStream_t s) {
-  if (a.width <= 512) return launch_v<1, 1>(a, s);
-  if (a.width <= 1024) return launch_v<1, 2>(a, s);
-  if (a.width <= 2048) return launch_v<4, 1>(a, s);
-  if (a.width <= 4096) return launch_v<4, 2>(a, s);
-  if (a.width <= 8192) return launch_v<4, 4>(a, s);
-  if (a.width <= 16384) return launch_v<16, 2>(a, s);
-  return launch_v<16, 4>(a, s);
+template <typename TX, typename TR, typename TZ>
+hipError_t launch_t(const BlockNormArgs& a, hipStream_t s) {
+  if (a.width % 8 != 0) {  // rows whose last lane has fewer than 8 values
+    if (a.width <= 512) return launch_v<TX, TR, TZ, 1, 1, false>(a, s);
+    if (a.width <= 4096) return launch_v<TX, TR, TZ, 8, 1, false>(a, s);
+    if (a.width <= 8192) return launch_v<TX, TR, TZ, 16, 1, false>(a, s);
+    return launch_v<TX, TR, TZ, 16, 4, false>(a, s);
+  }
+  if (a.width <= 512) return launch_v<TX, TR, TZ, 1, 1, true>(a, s);
+  if (a.width <= 2048) return launch_v<TX, TR, TZ, 4, 1, true>(a, s);
+  if (a.width <= 4096) return launch_v<TX, TR, TZ, 8, 1, true>(a, s);
+  if (a.width <= 8192) return launch_v<TX, TR, TZ, 16, 1, true>(a, s);
+  if (a.width <= 16384) return launch_v<TX, TR, TZ, 16, 2, true>(a, s);
+  return launch_v<TX, TR, TZ, 16, 4, true>(a, s);
 }
+
+template <typename TX, typename TR>
+hipError_t launch_z(const BlockNormArgs& a, hipStream_t s) {
+  if (!a.gate) return launch_t<TX, TR, None>(a, s);
+  return a.gate_bf16 ? launch_t<TX, TR, uint16_t>(a, s) : launch_t<TX, TR, float>(a, s);
+}
+
 }  // namespace
 
 // A launch holds fewer than 2^32 threads: calls of more than 2^21 rows (1024 threads each at most) go in pieces.
@@ -204,7 +291,8 @@ hipError_t launch_block_norm(const BlockNormArgs& args, hipStream_t s) {
     a.gate = at(args.gate, a.gate_bf16, a.gate_stride);
     a.h = const_cast<char*>(at(args.h, a.residual_bf16, a.h_stride));
     a.y = const_cast<char*>(at(args.y, a.y_bf16, a.y_stride));
-    const hipError_t e = launch_rows(a, s);
+    const hipError_t e = a.x_bf16 ? (a.residual_bf16 ? launch_z<uint16_t, uint16_t>(a, s) : launch_z<uint16_t, float>(a, s))
+                                  : (a.residual_bf16 ? launch_z<float, uint16_t>(a, s) : launch_z<float, float>(a, s));
     if (e != hipSuccess || args.rows - r <= most) return e;
     r += most;
   }
