@@ -258,7 +258,7 @@ __device__ __forceinline__ Row parameters(const Call& c, int r, const double* st
   const float p = c.a.top_p ? c.a.top_p[r] : 1.f;
   row.per = 1.44269504088896340736 * kSteps / static_cast<double>(t);
   row.shift = c.shift;
-  row.low = -kSteps * (c.shift + 2.0);
+  row.low = -kSteps * (c.shift + 12.0);  // (a tile of 512 such tokens is rounded to 0 too)
   row.steps = steps;
   row.least = ldexp(min_p > 0.f ? (min_p < 1.f ? min_p : 1.0) : 0.0, c.shift);
   if (row.k < 0 || row.k >= c.a.vocab) row.k = 0;

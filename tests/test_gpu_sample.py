@@ -148,6 +148,25 @@ def test_flat_and_steep_rows():
         check(x.cuda(), n["u"], **kw)
 
 
+def test_parts_of_a_row_that_weigh_nothing():
+    """Long runs of tokens whose weight rounds to 0, before, between and after the others: not even u = 0 gives one of them."""
+    import torch
+
+    announce("sample: runs without weight")
+    inf, vocab = float("inf"), 9000
+    x = torch.full((8, vocab), -1000.0)
+    x[0:4, [3000, 3001, 7000]] = 0.0
+    x[4:6, 5000:] = inf
+    x[6, 8999] = 0.0
+    x[7, 0] = 0.0
+    u = np.array([0.0, 1e-20, 0.5, 1 - 2.0 ** -24, 0.0, 1 - 2.0 ** -24, 0.0, 1 - 2.0 ** -24], np.float32)
+    for kw in (dict(), dict(least=[1e-30] * 8), dict(p=[0.9] * 8), dict(k=[8999] * 8)):
+        got, chance = run(x.cuda(), u, **kw)
+        stay = 3600 if "p" in kw else 4000  # of the infinities
+        assert got.tolist() == [3000, 3000, 3001, 7000, 5000, 4999 + stay, 8999, 0]
+        assert np.allclose(chance, [1 / 3] * 4 + [1 / stay] * 2 + [1.0] * 2, rtol=2.0 ** -22, atol=0)
+
+
 def test_rows_strides_and_neighbours():
     """Rows of a wider tensor at odd addresses; a row's token does not depend on the others."""
     announce("sample: strides, rows alone")
