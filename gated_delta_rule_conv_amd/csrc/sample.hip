@@ -85,7 +85,7 @@ __device__ __forceinline__ void fill_steps(double* steps, int shift) {
     const double f = threadIdx.x * (0.693147180559945309417 / kSteps);
     double s = 1.0;
 #pragma unroll
-    for (int n = 18; n > 0; --n) s = fma(s, f / n, 1.0);
+    for (int n = 18; n > 0; --n) s = fma(s, f * (1.0 / n), 1.0);
     steps[threadIdx.x] = ldexp(s, shift);
   }
 }
@@ -817,46 +817,49 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
           }
       }
       __syncthreads();
-      // eight tokens a thread, in order
-      float v[8];
-      unsigned long long wt[8], at_top = 0, stays = 0, all;
+      // up to eight tokens a thread, in order
+      const int each = (plan.count + kThreads - 1) / kThreads;
+      double wt[8];
+      unsigned long long at_top = 0, stays = 0, all;
       int b[8];
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int i = 8 * tid + e;
+        if (e >= each) break;
+        const int i = each * tid + e;
         b[e] = kBins + 1;
-        wt[e] = 0;
+        wt[e] = 0.0;
         if (i < plan.count) {
-          v[e] = value_of(~static_cast<uint32_t>(sh.list[i] >> 32));
-          b[e] = row.bin(v[e]);
-          wt[e] = row.whole(row.weight(v[e]));
+          const float v = value_of(~static_cast<uint32_t>(sh.list[i] >> 32));
+          b[e] = row.bin(v);
+          wt[e] = row.weight(v);
           at_top += b[e] < plan.top;
         }
       }
       scan(at_top, sh.parts, turn, all);
       const int stay_end = plan.top < kBins ? static_cast<int>(all) + static_cast<int>(plan.stay) : kBins + kList;
       // (the tokens of top_k's bin come last in the list: those up to stay_end are its)
+      unsigned long long mine = 0;
 #pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (b[e] == plan.top && 8 * tid + e < stay_end) stays += wt[e];
+      for (int e = 0; e < 8; ++e) {
+        if (e >= each) break;
+        if (b[e] == plan.top && each * tid + e < stay_end) stays += row.whole(wt[e]);
+        if (b[e] <= plan.to) mine += row.whole(wt[e]);
+      }
       scan(stays, sh.parts, turn, all);
       const double target = static_cast<double>(row.p) * static_cast<double>(plan.whole + all);
       const bool by_weight = plan.from <= plan.to;
-      unsigned long long mine = 0;
-#pragma unroll
-      for (int e = 0; e < 8; ++e)
-        if (b[e] <= plan.to) mine += wt[e];
       unsigned long long before = plan.before + scan(mine, sh.parts, turn, all) - mine;
       int last = -1;
 #pragma unroll
       for (int e = 0; e < 8; ++e) {
-        const int i = 8 * tid + e;
+        if (e >= each) break;
+        const int i = each * tid + e;
         const bool stay = i < plan.count && i < stay_end &&
                           (!by_weight || (b[e] <= plan.to && (static_cast<double>(before) < target || (i == 0 && plan.from == 0))));
-        if (b[e] <= plan.to) before += wt[e];
+        if (b[e] <= plan.to) before += row.whole(wt[e]);
         if (!stay) continue;
         last = i;
-        if (!(row.weight(v[e]) < row.least)) atomicAdd(&tiles[static_cast<uint32_t>(sh.list[i]) / kTile], wt[e]);
+        if (!(wt[e] < row.least)) atomicAdd(&tiles[static_cast<uint32_t>(sh.list[i]) / kTile], row.whole(wt[e]));
       }
       if (tid == 0) sh.at = 0;
       __syncthreads();
