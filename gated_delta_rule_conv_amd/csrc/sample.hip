@@ -99,7 +99,7 @@ struct Row {
   double base;         // most
   double per;          // 32 log2(e) / T
   double low;          // 32 log2 of what is surely rounded to 0
-  float far;           // a distance from the largest value beyond which a weight is surely 0
+  float far;           // a distance from the largest value beyond which a weight is surely 0 (infinite T: all are nearer)
   float bins;          // bins by distance
   double least;        // 2^S min_p, min_p at most 1
   const double* steps;
@@ -112,7 +112,6 @@ struct Row {
     infinite = largest == __builtin_inff();
     most = infinite ? 0.f : largest;
     base = most;
-    far = static_cast<float>((shift + 1.5) * kSteps / per);  // (infinite T: all finite distances)
   }
   __device__ __forceinline__ float seen(float x) const { return !infinite ? x : x == __builtin_inff() ? 0.f : -__builtin_inff(); }
   template <int N>
@@ -249,29 +248,85 @@ __device__ __forceinline__ unsigned long long scan(unsigned long long v, Scan& s
   return v + before;
 }
 
-// What a row's parameters ask for.
-__device__ __forceinline__ Row parameters(const Call& c, int r, const double* steps) {
-  Row row{};
+// Two such sums at once, of counts and of weights. (No sum of either kind may follow before the next barrier.)
+__device__ __forceinline__ uint32_t wave_scan(uint32_t v) {
+  v += moved<0x111, 0xF>(v, 0);
+  v += moved<0x112, 0xF>(v, 0);
+  v += moved<0x114, 0xF>(v, 0);
+  v += moved<0x118, 0xF>(v, 0);
+  v += moved<0x142, 0xA>(v, 0);
+  return v + moved<0x143, 0xC>(v, 0);
+}
+__device__ __forceinline__ void scan(uint32_t n, unsigned long long v, Scan& s, uint32_t& upto_n, unsigned long long& upto_v,
+                                     uint32_t& all_n, unsigned long long& all_v) {
+  const int lane = threadIdx.x & (kWave - 1), w = threadIdx.x / kWave;
+  upto_n = wave_scan(n);
+  upto_v = wave_scan(v);
+  if (lane == kWave - 1) {
+    s.part[0][w] = upto_n;
+    s.part[1][w] = upto_v;
+  }
+  __syncthreads();
+  all_n = 0;
+  all_v = 0;
+  uint32_t before_n = 0;
+  unsigned long long before_v = 0;
+#pragma unroll
+  for (int i = 0; i < kWaves; ++i) {
+    if (i == w) {
+      before_n = all_n;
+      before_v = all_v;
+    }
+    all_n += static_cast<uint32_t>(s.part[0][i]);
+    all_v += s.part[1][i];
+  }
+  upto_n += before_n;
+  upto_v += before_v;
+}
+
+// What a row's parameters ask for: formed by one lane, for all after the next barrier.
+struct Asked {
+  double per, least;
+  float far, p;
+  int32_t k;
+  int mode;
+};
+__device__ __forceinline__ void ask(const Call& c, int r, Asked& to) {
+  if (threadIdx.x != kThreads - 1) return;  // (its wave has no part in fill_steps)
   const float t = c.a.temperature ? c.a.temperature[r] : 1.0f;
   const float min_p = c.a.min_p ? c.a.min_p[r] : 0.f;
-  row.k = c.a.top_k ? c.a.top_k[r] : 0;
+  const int32_t k = c.a.top_k ? c.a.top_k[r] : 0;
   const float p = c.a.top_p ? c.a.top_p[r] : 1.f;
-  row.per = 1.44269504088896340736 * kSteps / static_cast<double>(t);
+  to.per = 1.44269504088896340736 * kSteps / static_cast<double>(t);
+  to.far = t * (0.693147180559945309417f * (c.shift + 1.5f));
+  to.least = ldexp(min_p > 0.f ? (min_p < 1.f ? min_p : 1.0) : 0.0, c.shift);
+  to.k = k < 0 || k >= c.a.vocab ? 0 : k;
+  to.p = p < 1.f ? p : 1.f;
+  to.mode = !(t > 0.f) ? kLikeliest : to.k == 0 && to.p == 1.f ? kPlain : kListed;
+}
+__device__ __forceinline__ Row asked(const Call& c, const Asked& from, const double* steps) {
+  Row row{};
+  row.per = from.per;
+  row.far = from.far;
+  row.least = from.least;
+  row.k = from.k;
+  row.p = from.p;
+  row.mode = from.mode;
   row.shift = c.shift;
   row.low = -kSteps * (c.shift + 12.0);  // (a tile of 512 such tokens is rounded to 0 too)
   row.steps = steps;
-  row.least = ldexp(min_p > 0.f ? (min_p < 1.f ? min_p : 1.0) : 0.0, c.shift);
-  if (row.k < 0 || row.k >= c.a.vocab) row.k = 0;
-  row.p = p < 1.f ? p : 1.f;
-  row.mode = !(t > 0.f) ? kLikeliest : row.k == 0 && row.p == 1.f ? kPlain : kListed;
   return row;
 }
 
 // The row's largest and least values, and what its parameters ask for. Every thread gets it.
-__device__ __forceinline__ Row row_of(const Call& c, int r, const double* steps, uint32_t (&part)[2][kWaves]) {
+struct Ends {
+  uint32_t part[2][kWaves];
+  Asked asked;
+};
+__device__ __forceinline__ Row row_of(const Call& c, int r, const double* steps, Ends& sh) {
   uint32_t most = 0, least = 0xFFFFFFFFu;
   const uint2* e = c.w.ends + static_cast<int64_t>(r) * c.tiles;
-  Row row = parameters(c, r, steps);
+  ask(c, r, sh.asked);
   for (int t = threadIdx.x; t < c.tiles; t += kThreads) {
     const uint2 x = e[t];
     most = max(most, x.x);
@@ -280,18 +335,19 @@ __device__ __forceinline__ Row row_of(const Call& c, int r, const double* steps,
   most = wave_max(most);
   least = wave_min(least);
   if (threadIdx.x % kWave == 0) {
-    part[0][threadIdx.x / kWave] = most;
-    part[1][threadIdx.x / kWave] = least;
+    sh.part[0][threadIdx.x / kWave] = most;
+    sh.part[1][threadIdx.x / kWave] = least;
   }
   __syncthreads();
 #pragma unroll
   for (int w = 0; w < kWaves; ++w) {
-    most = max(most, part[0][w]);
-    least = min(least, part[1][w]);
+    most = max(most, sh.part[0][w]);
+    least = min(least, sh.part[1][w]);
   }
+  Row row = asked(c, sh.asked, steps);
   row.against(value_of(most));
   const float range = row.infinite ? 0.f : fminf(row.most - value_of(least), row.far);
-  row.bins = range > 0.f ? fminf(static_cast<float>(kBins) / range, 1e30f) : 0.f;
+  row.bins = range > 0.f ? fminf(kBins * __builtin_amdgcn_rcpf(range), 1e30f) : 0.f;
   if (most <= kLowest) row.mode = kNone;
   return row;
 }
@@ -341,9 +397,11 @@ __global__ __launch_bounds__(kThreads) void sample_tiles_kernel(Call c) {
   __shared__ double steps[kSteps];
   const int r = c.first + blockIdx.x / c.groups, g = blockIdx.x % c.groups;
   const int lane = threadIdx.x & (kWave - 1);
+  __shared__ Asked sh;
   fill_steps(steps, c.shift);
+  ask(c, r, sh);
   __syncthreads();
-  Row row = parameters(c, r, steps);
+  Row row = asked(c, sh, steps);
   const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
   const int step = c.groups * kWaves;
   float v[8], next[8];
@@ -376,7 +434,7 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void sample_weigh_kernel(Call c) {
   __shared__ unsigned long long weights[kBins];
   __shared__ uint32_t counts[kBins];
-  __shared__ uint32_t part[2][kWaves];
+  __shared__ Ends ends;
   __shared__ double steps[kSteps];
   const int r = c.first + blockIdx.x / c.groups, g = blockIdx.x % c.groups;
   const int lane = threadIdx.x & (kWave - 1), step = c.groups * kWaves;
@@ -389,7 +447,7 @@ __global__ __launch_bounds__(kThreads) void sample_weigh_kernel(Call c) {
     weights[i] = 0;
     counts[i] = 0;
   }
-  const Row row = row_of(c, r, steps, part);  // (with a barrier)
+  const Row row = row_of(c, r, steps, ends);  // (with a barrier)
   if (row.mode < kPlain) return;
   const bool plain = row.mode == kPlain, heavy = row.p < 1.f;
   for (; t < c.tiles; t += step) {
@@ -432,7 +490,7 @@ template <typename T>
 __global__ __launch_bounds__(kThreads) void sample_gather_kernel(Call c) {
   static_assert(kBins == 2 * kThreads, "two bins a thread");
   __shared__ Scan parts;
-  __shared__ uint32_t part[2][kWaves];
+  __shared__ Ends ends;
   __shared__ double steps[kSteps];
   __shared__ uint32_t found[kList], n_found, found_at;  // the workgroup's part of the list
   __shared__ int top_at, from_at, to_at;
@@ -445,7 +503,8 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(Call c) {
   float v[8], next[8];
   if (t < c.tiles) load8(x, t * kTile + 8 * lane, c.a.vocab, next);
   // the bins' counts and weights, and those of all bins before them
-  unsigned long long n2[2], w2[2], nb[2], wb[2], all_n, all_w;
+  uint32_t n2[2], nb[2], all_n;
+  unsigned long long w2[2], wb[2], all_w;
   {
     const uint2 n = *reinterpret_cast<const uint2*>(c.w.counts + static_cast<int64_t>(r) * kBins + 2 * tid);
     const ulonglong2 w = *reinterpret_cast<const ulonglong2*>(c.w.weights + static_cast<int64_t>(r) * kBins + 2 * tid);
@@ -455,14 +514,15 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(Call c) {
     w2[1] = w.y;
   }
   fill_steps(steps, c.shift);
-  const Row row = row_of(c, r, steps, part);
+  const Row row = row_of(c, r, steps, ends);
   if (row.mode != kListed) return;
   int turn = 0;
-  nb[0] = scan(n2[0] + n2[1], parts, turn, all_n) - n2[0] - n2[1];
-  wb[0] = scan(w2[0] + w2[1], parts, turn, all_w) - w2[0] - w2[1];
+  scan(n2[0] + n2[1], w2[0] + w2[1], parts, nb[0], wb[0], all_n, all_w);
+  nb[0] -= n2[0] + n2[1];
+  wb[0] -= w2[0] + w2[1];
   nb[1] = nb[0] + n2[0];
   wb[1] = wb[0] + w2[0];
-  const bool by_count = row.k > 0 && static_cast<unsigned long long>(row.k) < all_n, by_weight = row.p < 1.f;
+  const bool by_count = row.k > 0 && static_cast<uint32_t>(row.k) < all_n, by_weight = row.p < 1.f;
   if (tid == 0) {
     from_at = to_at = 0;
     before_at = 0;
@@ -568,7 +628,7 @@ struct Choose {
     } look;
   };
   Scan parts;
-  uint32_t part[2][kWaves];
+  Ends ends;
   double steps[kSteps];
   unsigned long long wide;
   uint32_t at;
@@ -704,7 +764,7 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
   const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave, r = c.first + blockIdx.x, vocab = c.a.vocab;
   const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
   fill_steps(sh.steps, c.shift);
-  Row row = row_of(c, r, sh.steps, sh.part);
+  Row row = row_of(c, r, sh.steps, sh.ends);
   const auto answer = [&](int token, float prob) {
     c.a.tokens[r] = token;
     if (c.a.prob) c.a.prob[r] = prob;
@@ -796,7 +856,9 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
         from[tid] = mine;
         __syncthreads();
         int before = 0;
-        for (int i = 0; i < plan.count; ++i) before += from[i] < mine;
+        for (int i = 0; i < plan.count; i += 8)  // (behind the last: none is lower)
+#pragma unroll
+          for (int e = 0; e < 8; ++e) before += from[i + e] < mine;
         if (tid < plan.count) sh.list[before] = mine;
       } else {
         int size = 2 * kThreads;
