@@ -20,6 +20,8 @@
 // above the last kept one's. A list that would be longer than 4096 (thousands of equal values at a border) is not made:
 // choose then looks the borders up in the row itself, 11 bits of the key at a time.
 
+#include <type_traits>
+
 #include "device_common.h"
 #include "launch.h"
 
@@ -486,6 +488,26 @@ __global__ __launch_bounds__(kThreads) void sample_weigh_kernel(Call c) {
 
 // ----------------------------------------------------------------------------- gather
 
+// f(value, whether the lane has one) for the tokens of a lane's bits, one at a time, as many times as the lane with most of them
+// has.
+template <typename F>
+__device__ __forceinline__ void each_of(uint32_t some, const float (&v)[8], F f) {
+  float own[8];
+#pragma unroll
+  for (int q = 0; q < 8; ++q) {
+    own[q] = v[q];
+    asm("" : "+v"(own[q]));  // (in registers: else the choice below becomes an address)
+  }
+  while (__ballot(some != 0)) {
+    const int e = __builtin_ctz(some | 0x100u);
+    float y = own[0];
+#pragma unroll
+    for (int q = 1; q < 8; ++q) y = e == q ? own[q] : y;
+    f(y, some != 0);
+    some &= some - 1;
+  }
+}
+
 template <typename T>
 __global__ __launch_bounds__(kThreads) void sample_gather_kernel(Call c) {
   static_assert(kBins == 2 * kThreads, "two bins a thread");
@@ -588,17 +610,11 @@ __global__ __launch_bounds__(kThreads) void sample_gather_kernel(Call c) {
       stays |= (b >= 0 && b < sure) << e;
       listed |= ((b >= from && b <= to) || b == top) << e;
     }
-    // one of a lane's tokens at a time, as many times as the lane with most of them has (few stay, mostly)
-    unsigned long long sum = 0;
-    while (__ballot(stays != 0)) {
-      const int e = __builtin_ctz(stays | 0x100u);
-      float y = v[0];
-#pragma unroll
-      for (int q = 1; q < 8; ++q) y = e == q ? v[q] : y;
+    unsigned long long sum = 0;  // (few stay, mostly)
+    each_of(stays, v, [&](float y, bool there) {
       const double w = row.weight(y);
-      sum += stays == 0 || w < row.least ? 0 : row.whole(w);
-      stays &= stays - 1;
-    }
+      sum += !there || w < row.least ? 0 : row.whole(w);
+    });
     if (listed) {
       uint32_t at = atomicAdd(&n_found, static_cast<uint32_t>(__builtin_popcount(listed)));
       while (listed) {
@@ -763,6 +779,12 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
   extern __shared__ unsigned long long tiles[];
   const int tid = threadIdx.x, lane = tid & (kWave - 1), w = tid / kWave, r = c.first + blockIdx.x, vocab = c.a.vocab;
   const T* x = static_cast<const T*>(c.a.logits) + r * c.a.stride;
+  Plan plan{};  // (what is read of a row without one goes nowhere)
+  int32_t listed = 0;
+  if (!TILES && c.w.counts) {
+    plan = c.w.plans[r];
+    listed = c.w.list[static_cast<int64_t>(r) * kList + tid];
+  }
   fill_steps(sh.steps, c.shift);
   Row row = row_of(c, r, sh.steps, sh.ends);
   const auto answer = [&](int token, float prob) {
@@ -799,7 +821,7 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
     const double f = row.weight(v);
     return place_of(v, i) > end || f < row.least ? 0 : row.whole(f);
   };
-  if (!TILES && row.mode == kListed && c.w.plans[r].looked) {
+  if (!TILES && row.mode == kListed && plan.looked) {
     Border border{0, 0xFFFFFFFFu};
     if (row.k > 0) {
       unsigned long long n = 0, all;
@@ -844,26 +866,41 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
       }
       tiles[t] = sum;
     }
-    if (!TILES && row.mode == kListed && c.w.plans[r].count > 0) {
-      const Plan plan = c.w.plans[r];
-      const auto nth = [&](int i) {
-        const int at = c.w.list[static_cast<int64_t>(r) * kList + i];
-        return place_of(row.seen(get(x + at)), at);
-      };
-      if (plan.count <= kThreads) {  // each one's number is how many lie before it
-        const unsigned long long mine = tid < plan.count ? nth(tid) : ~0ull;
-        unsigned long long* from = sh.list + kThreads;
-        from[tid] = mine;
-        __syncthreads();
+    if (!TILES && row.mode == kListed && plan.count > 0) {
+      const auto place = [&](int at) { return place_of(row.seen(get(x + at)), at); };
+      if (plan.count <= kThreads) {  // a wave orders its 64; then each one's number is how many of every 64 lie before it
+        unsigned long long* runs = sh.list + kThreads;
+        const unsigned long long mine = tid < plan.count ? place(listed) : 0xFFFFFFFF00000000ull | tid;  // (behind all)
         int before = 0;
-        for (int i = 0; i < plan.count; i += 8)  // (behind the last: none is lower)
 #pragma unroll
-          for (int e = 0; e < 8; ++e) before += from[i + e] < mine;
-        if (tid < plan.count) sh.list[before] = mine;
+        for (int l = 0; l < kWave; ++l) {
+          const uint32_t hi = __builtin_amdgcn_readlane(static_cast<uint32_t>(mine >> 32), l);
+          const uint32_t lo = __builtin_amdgcn_readlane(static_cast<uint32_t>(mine), l);
+          before += (static_cast<unsigned long long>(hi) << 32 | lo) < mine;
+        }
+        runs[w * kWave + before] = mine;
+        const auto search = [&](auto n) {
+          constexpr int N = decltype(n)::value;
+          int at[N] = {};
+#pragma unroll
+          for (int d = kWave / 2; d > 0; d /= 2)
+#pragma unroll
+            for (int q = 0; q < N; ++q) at[q] += runs[q * kWave + at[q] + d - 1] < mine ? d : 0;
+          before = 0;
+#pragma unroll
+          for (int q = 0; q < N; ++q) before += at[q] + (runs[q * kWave + at[q]] < mine);
+        };
+        __syncthreads();
+        if (w * kWave < plan.count) {
+          if (plan.count > 4 * kWave) search(std::integral_constant<int, 8>{});
+          else if (plan.count > 2 * kWave) search(std::integral_constant<int, 4>{});
+          else if (plan.count > kWave) search(std::integral_constant<int, 2>{});
+          if (tid < plan.count) sh.list[before] = mine;
+        }
       } else {
         int size = 2 * kThreads;
         while (size < plan.count) size *= 2;
-        for (int i = tid; i < size; i += kThreads) sh.list[i] = i < plan.count ? nth(i) : ~0ull;
+        for (int i = tid; i < size; i += kThreads) sh.list[i] = i < plan.count ? place(c.w.list[static_cast<int64_t>(r) * kList + i]) : ~0ull;
         // exchanges between partners at falling distances, in runs of rising length
         for (int run = 2; run <= size; run *= 2)
           for (int d = run / 2; d > 0; d /= 2) {
@@ -925,7 +962,8 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
       }
       if (tid == 0) sh.at = 0;
       __syncthreads();
-      if (last >= 0) atomicMax(&sh.at, static_cast<uint32_t>(last));
+      const uint32_t most = wave_max(static_cast<uint32_t>(last + 1));
+      if (lane == 0 && most) atomicMax(&sh.at, most - 1);
       __syncthreads();
       end = sh.list[sh.at];
     }
