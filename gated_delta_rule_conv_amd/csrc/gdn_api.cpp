@@ -293,7 +293,7 @@ gdn_status linear_args(const gdn_dims* d, const char* fn, const void* q, int64_t
     return fail(GDN_ERR_ALIGN, "%s: q, k, v must be 16-byte aligned with strides a multiple of 16 bytes", fn);
   *a = gdn::LinearArgs{q, qs, k, ks, v, vs, g, gs, o, state_ptrs, d->num_k_heads, d->num_v_heads, d->head_dim,
                        d->num_v_heads / d->num_k_heads, d->scale, d->in_dtype == GDN_BF16, d->out_dtype == GDN_BF16,
-                       resolve_mma(d), d->prefill_form};
+                       d->prefill_form};
   return GDN_OK;
 }
 

@@ -221,7 +221,6 @@ struct LinearArgs {
   float scale;
   int32_t bf16;  // q, k and v
   int32_t o_bf16;
-  int32_t mma;  // 1 = fp32, 2 = bf16x3's place: exact bf16 thirds (resolved)
   int32_t form;  // gdn_prefill_form
 };
 

@@ -7,6 +7,8 @@
 #include "launch.h"
 #include "mma.h"
 
+#include "../../include/gdn.h"
+
 namespace gdn {
 namespace {
 
@@ -39,13 +41,14 @@ __device__ __forceinline__ int xcd_block() {
 }
 
 // Bound by HBM: a state is read and written once, rows in any order, since
-// o_r = scale (e^g S_r . q + v_r (k . q)) needs row r alone. A wave takes P passes of 1024 / D rows
-// (4 KiB each); D / 16 lanes share a row, lane c holding the columns [4 c + D / 4 e, + 4), e < 4, and
-// every load is issued before any arithmetic. Dots over a row's lanes are a fixed butterfly, so a
-// slot's bits depend on nothing else in the call.
-template <int D, int P, typename T>
+// o_r = scale (e^g S_r . q + v_r (k . q)) needs row r alone. A wave takes 1024 / D rows (4 KiB); D / 16
+// lanes share a row, lane c holding the columns [4 c + D / 4 e, + 4), e < 4, and every load is issued before any arithmetic.
+// Dots over a row's lanes are a fixed butterfly, so a slot's bits depend on nothing else in the call. Twice the rows
+// a wave: slower everywhere (32 heads, d = 128: 1 slot 4.8 us against 4.2, 64 slots 48.5 against 46.7, 256 slots 186 against
+// 176, 6.1 TB/s).
+template <int D, typename T>
 __global__ __launch_bounds__(kDecodeWaves* kWave) void linear_decode_kernel(LinearArgs a) {
-  constexpr int LPR = D / 16, RPP = kWave / LPR, PARTS = D / (RPP * P);
+  constexpr int LPR = D / 16, ROWS = kWave / LPR, PARTS = D / ROWS;
   const int lane = threadIdx.x & (kWave - 1);
   const int w = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int unit = xcd_block() * kDecodeWaves + w;
@@ -53,14 +56,11 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void linear_decode_kernel(Line
   const int j = unit / PARTS, i = blockIdx.y;
   const uint64_t sp = ((cu64*)a.state_ptrs)[i];
   if (sp == 0) return;
-  const int h = j / a.group, c = lane % LPR, row0 = unit % PARTS * (RPP * P) + lane / LPR;
-  gf32x4* S = (gf32x4*)(reinterpret_cast<float*>(sp) + static_cast<int64_t>(j) * D * D);
-  f32x4 s[P][4];
+  const int h = j / a.group, c = lane % LPR, row = unit % PARTS * ROWS + lane / LPR;
+  gf32x4* S = (gf32x4*)(reinterpret_cast<float*>(sp) + (static_cast<int64_t>(j) * D + row) * D);
+  f32x4 s[4];
 #pragma unroll
-  for (int p = 0; p < P; ++p)
-#pragma unroll
-    for (int e = 0; e < 4; ++e)
-      s[p][e] = __builtin_nontemporal_load(S + static_cast<int64_t>(row0 + p * RPP) * (D / 4) + c + LPR * e);
+  for (int e = 0; e < 4; ++e) s[e] = __builtin_nontemporal_load(S + c + LPR * e);
   const T* kp = static_cast<const T*>(a.k) + i * a.k_stride + h * D;
   const T* qp = static_cast<const T*>(a.q) + i * a.q_stride + h * D;
   typename Vec4<T>::Raw kr[4], qr[4];
@@ -69,51 +69,40 @@ __global__ __launch_bounds__(kDecodeWaves* kWave) void linear_decode_kernel(Line
     kr[e] = Vec4<T>::load_raw(kp + 4 * (c + LPR * e));
     qr[e] = Vec4<T>::load_raw(qp + 4 * (c + LPR * e));
   }
-  const T* vp = static_cast<const T*>(a.v) + i * a.v_stride + static_cast<int64_t>(j) * D;
-  float vr[P];
-#pragma unroll
-  for (int p = 0; p < P; ++p) vr[p] = value(vp + row0 + p * RPP);
+  const float v = value(static_cast<const T*>(a.v) + i * a.v_stride + static_cast<int64_t>(j) * D + row);
   const float decay = expf(((cfloat*)a.g)[i * a.g_stride + j]);
-  float kq = 0.f;
+  float kq = 0.f, sq = 0.f;
 #pragma unroll
-  for (int e = 0; e < 4; ++e)
+  for (int e = 0; e < 4; ++e) {
+    f32x4 n;
 #pragma unroll
-    for (int t = 0; t < 4; ++t) kq = fmaf(Vec4<T>::elem(kr[e], t), Vec4<T>::elem(qr[e], t), kq);
-  kq = group_sum<LPR>(kq);
-#pragma unroll
-  for (int p = 0; p < P; ++p) {
-    float sq = 0.f;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      f32x4 n;
-#pragma unroll
-      for (int t = 0; t < 4; ++t) {
-        sq = fmaf(s[p][e][t], Vec4<T>::elem(qr[e], t), sq);
-        n[t] = fmaf(vr[p], Vec4<T>::elem(kr[e], t), decay * s[p][e][t]);
-      }
-      __builtin_nontemporal_store(n, S + static_cast<int64_t>(row0 + p * RPP) * (D / 4) + c + LPR * e);
+    for (int t = 0; t < 4; ++t) {
+      const float k = Vec4<T>::elem(kr[e], t), q = Vec4<T>::elem(qr[e], t);
+      kq = fmaf(k, q, kq);
+      sq = fmaf(s[e][t], q, sq);
+      n[t] = fmaf(v, k, decay * s[e][t]);
     }
-    sq = group_sum<LPR>(sq);
-    if (c == 0)
-      put(a.o, a.o_bf16, (static_cast<int64_t>(i) * a.hv + j) * D + row0 + p * RPP, a.scale * fmaf(vr[p], kq, decay * sq));
+    __builtin_nontemporal_store(n, S + c + LPR * e);
   }
+  kq = group_sum<LPR>(kq);
+  sq = group_sum<LPR>(sq);
+  if (c == 0) put(a.o, a.o_bf16, (static_cast<int64_t>(i) * a.hv + j) * D + row, a.scale * fmaf(v, kq, decay * sq));
 }
 
-template <int D, int P, typename T>
-hipError_t decode_units(const LinearArgs& a, int32_t m, hipStream_t s) {
-  constexpr int PARTS = D / (kWave / (D / 16) * P);
+template <int D, typename T>
+hipError_t decode_dt(const LinearArgs& a, int32_t m, hipStream_t s) {
+  constexpr int PARTS = D / (kWave / (D / 16));
   const dim3 grid(static_cast<unsigned>((a.hv * PARTS + kDecodeWaves - 1) / kDecodeWaves), static_cast<unsigned>(m));
-  linear_decode_kernel<D, P, T><<<grid, kDecodeWaves * kWave, 0, s>>>(a);
+  linear_decode_kernel<D, T><<<grid, kDecodeWaves * kWave, 0, s>>>(a);
   return hipGetLastError();
 }
 
 template <typename T>
 hipError_t decode_t(const LinearArgs& a, int32_t m, hipStream_t s) {
-  const bool big = static_cast<int64_t>(m) * a.hv >= 1024;
   switch (a.d) {
-    case 32: return decode_units<32, 1, T>(a, m, s);
-    case 64: return big ? decode_units<64, 1, T>(a, m, s) : decode_units<64, 2, T>(a, m, s);
-    default: return big ? decode_units<128, 1, T>(a, m, s) : decode_units<128, 2, T>(a, m, s);
+    case 32: return decode_dt<32, T>(a, m, s);
+    case 64: return decode_dt<64, T>(a, m, s);
+    default: return decode_dt<128, T>(a, m, s);
   }
 }
 
@@ -124,10 +113,10 @@ hipError_t decode_t(const LinearArgs& a, int32_t m, hipStream_t s) {
 //   o_i = scale (e^G_i S q_i + sum_{j <= i} e^(G_i - G_j) (q_i . k_j) v_j)
 //   S  <- e^G_n S + sum_j e^(G_n - G_j) v_j k_j^T
 // all four products on matrix cores. A workgroup takes a v-head of a tile, a run of a sequence's chunks; each of its
-// waves owns D / 4 columns (D / 2 waves of 16 for D = 32) of S^T [d_k][d_v] in accumulators, where they lie as a product's left operand wants them: lane
-// l of a 16x16 tile's result holds rows 4 h + r (h = l / 16, r < 4) of column l % 16, so a step over 32 contracted values takes its
-// values in the order 32 s + 16 u + 4 h + r (u < 2; fp32: 16 s + 4 h + r) from both operands, and S never passes through LDS.
-// q is stored in LDS in that order, k, v as they came (read by rows for q . k, by columns, transposed on the way, for the
+// waves owns 16 or 32 of the d_v columns of S^T [d_k][d_v] in accumulators, where they lie as a product's left operand wants
+// them: lane l of a 16x16 tile's result holds rows 4 h + r (h = l / 16, r < 4) of column l % 16, so a step over 32 contracted values
+// takes its values in the order 32 s + 16 u + 4 h + r (u < 2; fp32: 16 s + 4 h + r) from both operands, and S never passes through
+// LDS. q is stored in LDS in that order, k, v as they came (read by rows for q . k, by columns, transposed on the way, for the
 // state), the masked scores in that order again.
 //
 // Precision: with bf16 input every product has one operand that is exact in bf16. The other is fp32 and goes as three bf16
@@ -135,10 +124,15 @@ hipError_t decode_t(const LinearArgs& a, int32_t m, hipStream_t s) {
 // goes through fp32 products. Sums of g are kept in base 2 as a multiple of 2^-8, exact up to 2^16, and a rest, so that
 // differences between tokens behind a strongly forgetting one keep their digits.
 //
-// Long sequences are cut into tiles of LinearPlan::tokens so that enough workgroups run: a first pass forms what each tile
-// adds to the state, a scan the state before each tile, and the last pass runs all tiles at once. Tiles begin at a
-// sequence's own first token and their length depends on the layer alone: a sequence has the same bits whatever
-// is packed with it.
+// Sequences are cut into tiles so that enough workgroups run: a first pass forms what each tile adds to the state, a scan the
+// state before each tile, and the last pass runs all tiles at once. Tiles begin at a sequence's own first token.
+//
+// What bounds it (16 k-heads, 32 v-heads, d = 128, bf16): 4096 tokens, tiles of 4 chunks, 26 + 13 + 46 us; the pack of 15717
+// tokens, fp32 outputs, tiles of 16, 62 + 16 + 189 us, where the bytes alone would take 111. No single thing bounds the last
+// pass: per wave and chunk 237 matrix, about 1090 vector and 141 LDS instructions, which a SIMD's two waves issue mostly one at a
+// time (a vector one every 5 cycles of a wave, LDS conflicts in 4 cycles of 10); leaving out stores, scores, loads or the
+// state's update takes off 6 to 18% each. Tried and slower: 8 waves of 16 columns (the pack 196 us against 180, 8-chunk tiles), vector
+// instructions placed between matrix ones by scheduling groups (197 against 180).
 
 constexpr int kChunk = 64;
 constexpr float kForget = -128.0f;  // e^-128 is 0 in fp32
@@ -288,6 +282,13 @@ __device__ __forceinline__ void sequence(const LinearPlan& p, int i, int& lo, in
   hi = max(min(p.cu[i + 1], p.total), lo);
 }
 
+// How many tiles a sequence has: up to 5 chunks are one, whatever a tile's length (a tile of 2 chunks each for 256 tokens of
+// one sequence: 31.5 us against 26.2 in one, 32 heads, d = 128; for 384: 33.8 against 35.5).
+constexpr int kUncut = 5 * kChunk;
+__device__ __forceinline__ int tiles_of(const LinearPlan& p, int len) {
+  return len <= kUncut ? len > 0 : len / p.tokens + (len % p.tokens != 0);
+}
+
 // Tile b, or with SLOTS the tile of room b, by a scan over the sequences, 64 at a time.
 template <bool SLOTS>
 __device__ Place find_place(const LinearPlan& p, int b) {
@@ -296,7 +297,7 @@ __device__ Place find_place(const LinearPlan& p, int b) {
   for (int i0 = 0; i0 < p.n; i0 += kWave) {
     int lo = 0, hi = 0;
     if (i0 + lane < p.n) sequence(p, i0 + lane, lo, hi);
-    const int t = (hi - lo) / p.tokens + ((hi - lo) % p.tokens != 0), r = t > 1 ? t : 0;
+    const int t = tiles_of(p, hi - lo), r = t > 1 ? t : 0;
     int ts = t, rs = r;
 #pragma unroll
     for (int m = 1; m < kWave; m *= 2) {
@@ -340,7 +341,7 @@ __global__ __launch_bounds__(kTableThreads) void linear_table_kernel(LinearPlan 
     const int i = i0 + tid;
     int lo = 0, hi = 0;
     if (i < p.n) sequence(p, i, lo, hi);
-    const int t = (hi - lo) / p.tokens + ((hi - lo) % p.tokens != 0), r = t > 1 ? t : 0;
+    const int t = tiles_of(p, hi - lo), r = t > 1 ? t : 0;
     int ts = t, rs = r;
 #pragma unroll
     for (int m = 1; m < kWave; m *= 2) {
@@ -422,9 +423,9 @@ __global__ __launch_bounds__((LinearCfg<D, T, OUT>::THREADS), (sizeof(T) == 2 ? 
   sequence(p, at.seq, lo, hi);
   lo = __builtin_amdgcn_readfirstlane(lo);
   hi = __builtin_amdgcn_readfirstlane(hi);
-  const bool last = hi - lo <= (at.part + 1) * static_cast<int64_t>(p.tokens);
+  const bool last = at.slot < 0 || hi - lo <= (at.part + 1) * static_cast<int64_t>(p.tokens);
   if (!OUT && last) return;  // (no tile follows)
-  const int start = lo + at.part * p.tokens, end = last ? hi : start + p.tokens;
+  const int start = at.slot < 0 ? lo : lo + at.part * p.tokens, end = last ? hi : start + p.tokens;
   const int kh = j / a.group;
   const int64_t head = static_cast<int64_t>(j) * D * D;
   float* own = reinterpret_cast<float*>(sp) + head;
@@ -791,50 +792,83 @@ __global__ __launch_bounds__(kScanThreads) void linear_scan_kernel(LinearArgs a,
   if (sp == 0) return;
   int lo, hi;
   sequence(p, at.seq, lo, hi);
-  const int n = (hi - lo) / p.tokens + ((hi - lo) % p.tokens != 0);
+  const int n = tiles_of(p, hi - lo);
   const int64_t e = static_cast<int64_t>(j) * (D * D / 4) + b % BLOCKS * kScanThreads + threadIdx.x;
   const int64_t up = static_cast<int64_t>(a.hv) * (D * D / 4);
   f32x4 z = reinterpret_cast<const f32x4*>(sp)[e];
   f32x4* to = reinterpret_cast<f32x4*>(p.states) + at.slot * up + e;
   const float* kept = p.kept + static_cast<int64_t>(at.slot) * a.hv + j;
-  for (int i = 0; i < n; ++i) {
-    const bool more = i + 1 < n;  // (the last tile added nothing)
-    const f32x4 added = more ? to[i * up] : f32x4{0.f, 0.f, 0.f, 0.f};
-    const float f = more ? kept[static_cast<int64_t>(i) * a.hv] : 0.f;
-    to[i * up] = z;
-    z = z * f + added;
+  // Two tiles at a time, the next two on their way (the last tile added nothing). One at a time: 8 heads, d = 64, 64 tiles of
+  // 256 tokens 25.6 us against 16.0, 32 heads, d = 128, 16 of 1024 23.1 against 24.0; four at a time: the latter 26.5.
+  constexpr int A = 2;
+  f32x4 added[A], next[A];
+  float f[A], next_f[A];
+  const auto load = [&](int i) {
+#pragma unroll
+    for (int x = 0; x < A; ++x) {
+      next[x] = to[min(i + x, n - 2) * up];
+      next_f[x] = kept[static_cast<int64_t>(min(i + x, n - 2)) * a.hv];
+    }
+  };
+  load(0);
+  for (int i = 0; i < n; i += A) {
+#pragma unroll
+    for (int x = 0; x < A; ++x) {
+      added[x] = next[x];
+      f[x] = next_f[x];
+    }
+    if (i + A < n) load(i + A);
+#pragma unroll
+    for (int x = 0; x < A; ++x) {
+      if (i + x >= n) return;
+      to[(i + x) * up] = z;
+      z = z * f[x] + added[x];
+    }
   }
 }
 
 struct LinearSizes {
   int32_t tokens;  // a tile's
-  int64_t tiles, slots;
-  bool cut;  // sequences may have several tiles
-  size_t table, kept, states, bytes;  // offsets, and all of it
+  int64_t tiles, slots;  // to launch, and there is room for as many as no smaller call has more of:
+  int64_t most_tiles, most_slots;
+  size_t kept, states, bytes;  // offsets, and all of it
 };
 
-// A tile's length depends on the layer alone.
-int32_t tile_tokens(int32_t hv, int32_t d) {
-  const int32_t chunks = hv * d / 512;
-  return kChunk * (chunks < 2 ? 2 : chunks > 8 ? 8 : chunks);
-}
-
+// A tile's length. Under GDN_PREFILL_SEGMENTS it depends on the layer alone. Else the call's tokens set it: 2 chunks
+// (the adding pass, whose work a longer tile would not lessen, then has the most workgroups), doubled until one head's work for a
+// workgroup of 4 waves comes to about two workgroups a CU, where more would wait for a place; and until the scan's
+// steps, one a tile, are few beside a tile's own. Calls, us, against the layer's own 8 chunks and whole sequences (32 heads,
+// d = 128, bf16): 1024 tokens 41 (69, 83), 4096 86 (86, 309), the pack of 15717 tokens 229 (251, 629), 16 sequences of 1024 166
+// (225, 147), 64 of them 599 (855, 573). Half the tiles of the last rule (32 heads): 64 sequences 592, one of 16384
+// among 31 of 256 354 (407); 8 heads, d = 64, one of 16384 tokens without the scan's rule 60 (49).
 LinearSizes sizes(int32_t hv, int32_t d, int32_t n, int32_t total, int32_t form) {
   LinearSizes z{};
-  z.tokens = tile_tokens(hv, d);
-  z.cut = form != 1 && total > z.tokens;
-  if (!z.cut) z.tokens = INT32_MAX;
   const int64_t seqs = n < total ? n : total;
-  z.tiles = seqs + (z.cut ? total / z.tokens : 0);
+  int64_t whole = 0, most = 0;  // tiles' lengths that all tokens hold
+  z.tokens = INT32_MAX;
+  if (form != GDN_PREFILL_WHOLE) {
+    const bool fixed = form == GDN_PREFILL_SEGMENTS;
+    const int32_t chunks = fixed ? hv * d / 512 : 2, shortest = kChunk * (chunks < 2 ? 2 : chunks > 8 ? 8 : chunks);
+    const int64_t cap = fixed ? INT32_MAX : 1 + 512 * 128 / (hv * d);
+    int64_t tokens = shortest;
+    const auto scan_heavy = [&] { return 16 * (tokens / kChunk) * (tokens / kChunk) < total / kChunk; };
+    while (tokens * cap < total || (!fixed && scan_heavy())) tokens *= 2;
+    if (total > kUncut && total > tokens) {
+      z.tokens = static_cast<int32_t>(tokens);
+      whole = total / tokens;
+    }
+    most = total / shortest < cap ? total / shortest : cap;
+  }
   // a sequence of several tiles is longer than one: at most twice the whole tiles of all tokens
-  z.slots = z.cut ? 2 * static_cast<int64_t>(total / z.tokens) : 0;
-  const int64_t by_seq = z.slots / 2 + seqs;
-  if (z.cut && by_seq < z.slots) z.slots = by_seq;
+  const auto rooms = [&](int64_t w) { return w < seqs ? 2 * w : w + seqs; };
+  z.tiles = seqs + whole;
+  z.slots = rooms(whole);
+  z.most_tiles = seqs + most;
+  z.most_slots = rooms(most);
   const auto up = [](size_t x) { return (x + 255) & ~static_cast<size_t>(255); };
-  z.table = 0;
-  z.kept = n > kWave ? up((z.tiles + z.slots) * sizeof(Place)) : 0;
-  z.states = z.kept + up(z.slots * hv * sizeof(float));
-  z.bytes = z.states + z.slots * hv * static_cast<size_t>(d) * d * sizeof(float);
+  z.kept = n > kWave ? up((z.most_tiles + z.most_slots) * sizeof(Place)) : 0;
+  z.states = z.kept + up(z.most_slots * hv * sizeof(float));
+  z.bytes = z.states + z.most_slots * hv * static_cast<size_t>(d) * d * sizeof(float);
   return z;
 }
 

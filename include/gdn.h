@@ -35,7 +35,8 @@
  *  - Strides are in ELEMENTS of the pointed-to type.
  *  - Unchecked preconditions (undefined behaviour when violated): device pointers
  *    are valid for the stated extents; per-slot pointers within one call are
- *    distinct; outputs alias no input; g <= 0 and finite; beta in [0, 1];
+ *    distinct; outputs alias no input; g <= 0 and finite (for the linear
+ *    attention calls minus infinity too); beta in [0, 1];
  *    cu_seqlens is non-decreasing from 0 to total_tokens.
  */
 #ifndef GDN_H_
@@ -58,7 +59,7 @@ typedef enum gdn_status {
                               precision policy, prefill form, or a 0/1 switch) */
   GDN_ERR_ALIGN = 4,       /* a pointer or stride breaks the 16-byte alignment rule */
   GDN_ERR_WORKSPACE = 5,   /* workspace NULL or smaller than gdn_prefill_workspace_size */
-  GDN_ERR_UNSUPPORTED = 6, /* valid but not built: head dim, chunk size, conv width or tree size */
+  GDN_ERR_UNSUPPORTED = 6, /* valid but not built: head dim, chunk size, conv width, tree size, row width or stride */
   GDN_ERR_HIP = 7          /* the HIP runtime failed the launch */
 } gdn_status;
 
@@ -491,8 +492,9 @@ gdn_status gdn_group_norm(const gdn_norm_dims* dims, const void* x, int64_t x_st
  * their pointer arrays, copies and snapshots serve both kinds of layer):
  *   S_t = exp(g_t) S_{t-1} + v_t k_t^T,   o_t = scale S_t q_t.
  * dims: num_k_heads, num_v_heads (v-head j reads k-head j / (Hv / Hk)), head_dim, in_dtype (of q, k, v), out_dtype,
- * scale, mma and prefill_form. q and k are used as given: qk_l2norm_off must be 1 (else GDN_ERR_UNSUPPORTED), so
- * that dims of the layer core are not taken by mistake. No conv state is touched.
+ * scale and prefill_form; mma is checked and changes nothing (the products lose no more than fp32's do, under every policy).
+ * q and k are used as given: qk_l2norm_off must be 1 (else GDN_ERR_UNSUPPORTED), so that dims of the layer core are not
+ * taken by mistake. No conv state is touched.
  *
  *  q, k       [rows][Hk*d], v [rows][Hv*d] in dims->in_dtype, row strides in elements.
  *  g          [rows][Hv] fp32, row stride g_stride (>= Hv); g_stride 0: one row of Hv decays for all tokens.
@@ -505,10 +507,14 @@ gdn_status gdn_group_norm(const gdn_norm_dims* dims, const void* x, int64_t x_st
  *  Errors: GDN_ERR_UNSUPPORTED where rows of a prefill's q, k, v or g lie 2^24 bytes or more apart.
  *
  * gdn_linear_prefill: packed ragged sequences, cu_seqlens device int32 [num_seqs+1] as for gdn_prefill_chunked;
- * zero-length sequences keep their state; rows outside [0, total_tokens) are not touched. A token's o depends on no
- * later token, whatever that holds (an infinity or a NaN among its values included).
+ * zero-length sequences keep their state; rows that are no sequence's are not touched. A token's o depends on no
+ * later token, whatever that holds (an infinity or a NaN among its values included); behind such a value o and the
+ * state may hold a NaN where the formula gives an infinity.
+ * prefill_form: WHOLE takes a sequence in one piece, SEGMENTS in pieces of a length that num_v_heads and head_dim set, AUTO
+ * in pieces that grow with the call's tokens. Under the first two a sequence's bits do not depend on the rest of the call; all
+ * three agree to rounding.
  *  workspace  gdn_linear_workspace_size(dims, num_seqs, total_tokens) bytes, 256-byte aligned, contents ignored;
- *             may be NULL where that is 0.
+ *             may be NULL where that is 0. Enough for every call of fewer sequences and tokens.
  * gdn_linear_decode: one token for each of m slots; a slot's bits do not depend on the rest of the call.
  */
 gdn_status gdn_linear_workspace_size(const gdn_dims* dims, int32_t num_seqs, int32_t total_tokens, size_t* bytes);

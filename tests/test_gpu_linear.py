@@ -133,14 +133,15 @@ def test_decays_that_keep_nothing(dtype):
     check(c, c.prefill)
 
 
-def test_no_token_before_a_broken_one_is_touched():
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_no_token_before_a_broken_one_is_touched(dtype):
     """Infinities and NaN in q, k, v and g reach no earlier token and no other sequence or head."""
     import torch
 
     for what in ("q", "k", "v", "g"):
         for bad in (float("nan"), float("inf")):
-            announce(f"linear prefill {what} = {bad}")
-            clean, c = (Case([90, 100], Hk=2, Hv=4, d=64, seed=4) for _ in range(2))
+            announce(f"linear prefill {what} = {bad} {dtype}")
+            clean, c = (Case([90, 100], Hk=2, Hv=4, d=64, dtype=dtype, seed=4) for _ in range(2))
             t, row, head = 30, 30 + 90, 1  # token 30 of the second sequence
             if what == "g":
                 c.g[row, head] = bad if bad != bad else -bad
@@ -201,14 +202,15 @@ def test_rows_and_slots_that_are_not_the_calls():
 
 
 @pytest.mark.parametrize("dtype,d", [(BF16, 128), (F32, 32), (BF16, 64)])
-def test_a_sequence_has_the_same_bits_alone_and_packed(dtype, d):
+@pytest.mark.parametrize("form", [1, 2])
+def test_a_sequence_has_the_same_bits_alone_and_packed(dtype, d, form):
     import torch
 
     import gated_delta_rule_conv_amd as gdn
 
-    announce(f"linear prefill packed = solo {dtype} d={d}")
-    lens = [5, 600, 64, 129, 1]
-    c = Case(lens, d=d, dtype=dtype, seed=2)
+    announce(f"linear prefill packed = solo {dtype} d={d} form {form}")
+    lens = [5, 600, 64, 129, 1, 320, 321]
+    c = Case(lens, d=d, dtype=dtype, seed=2, form=form)
     first = c.state.clone()
     c.prefill()
     whole, end = bits_of(c.o), bits_of(c.state)
@@ -226,6 +228,17 @@ def test_many_short_sequences():
     announce("linear prefill of 1100 short sequences")
     r = np.random.default_rng(0)
     c = Case([int(x) for x in r.integers(0, 7, 1100)], Hk=1, Hv=1, d=32, seed=1)
+    check(c, c.prefill)
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("many", [False, True])
+def test_longer_tiles_in_larger_calls(dtype, many):
+    """Calls whose tokens make the tiles of a long sequence longer, with few sequences and with more than 64."""
+    announce(f"linear prefill of 9000 tokens {dtype} {many}")
+    r = np.random.default_rng(4)
+    short = [int(x) for x in r.integers(0, 60, 70)] if many else [257]
+    c = Case(short[:-1] + [5000, 0, 321, 9000 - 5321 - sum(short[:-1])] + short[-1:], Hk=8, Hv=40, d=32, dtype=dtype, seed=17)
     check(c, c.prefill)
 
 
