@@ -219,3 +219,64 @@ def test_sampled_drafts_are_what_decoding_gives():
         assert int(acc[i]) == (int(path[i][steps - 1]) if steps else -1)
         assert normwise_err(pool.state[i].cpu().numpy(), states[steps][i].cpu().numpy()) < 1e-5
         assert torch.equal(pool.conv_state[i], convs[steps][i])
+
+
+def test_one_step_on_another_stream_and_in_a_graph():
+    """Norm, decode, output norm, norm, sampling and following with every operand fixed: on the current stream, on a stream that
+    is given, and captured and replayed with eager work between; the same bits each time."""
+    import torch
+
+    import gated_delta_rule_conv_amd as gdn
+
+    announce("hybrid step: streams and graphs")
+    m, g = 5, torch.Generator().manual_seed(6)
+    rand = lambda *s: torch.randn(*s, generator=g).cuda()  # noqa: E731
+    gpu, r, g_t = OnGpu(Model(9), m), rand(m, W), -torch.rand(m, HV, generator=g).cuda()
+    qkv, head, logits, u = rand(m, (2 * HK + HV) * D), rand(m, W), rand(m, 5000), torch.rand(m, generator=g).cuda()
+    start = rand(m, HV, D, D)
+    ptrs, _ = gpu.pool.pointers(torch.arange(m, dtype=torch.int32, device="cuda"))
+    p = torch.full((m,), 0.9, device="cuda")
+    drafted = torch.randint(0, 3, (4 * m,), dtype=torch.int32, generator=g).cuda()
+    sampled = torch.randint(0, 3, (4 * m,), dtype=torch.int32, generator=g).cuda()
+    cu = (4 * torch.arange(m + 1, dtype=torch.int32)).cuda()
+    out = dict(h=torch.empty(m, W, device="cuda"), y=torch.empty(m, W, device="cuda"), o=torch.empty(m, HV, D, device="cuda"),
+               n=torch.empty(m, W, device="cuda"), y2=torch.empty(m, W, device="cuda"),
+               **{k: torch.empty(m, dtype=torch.int32, device="cuda") for k in ("tokens", "acc", "next")})
+    work, pending = gdn.sample_workspace(m, 5000), torch.zeros(m, dtype=torch.int32, device="cuda")
+
+    def step(stream=None):
+        gdn.block_norm(gpu.first, head, r, out["y"], residual_out=out["h"], pre_weight=gpu.t["pre"], stream=stream)
+        gdn.linear_decode(gpu.dims, qkv[:, :HK * D], qkv[:, HK * D:2 * HK * D], qkv[:, 2 * HK * D:], g_t, out["o"], ptrs, stream=stream)
+        gdn.group_norm(gpu.heads, out["o"], gpu.t["head"], out["n"], gate=out["y"], stream=stream)
+        gdn.block_norm(gpu.second, out["n"], out["h"], out["y2"], gate=gpu.t["ls"], post_weight=gpu.t["post"], stream=stream)
+        gdn.sample(logits, u, out["tokens"], work, top_p=p, stream=stream)
+        gdn.tree_follow(drafted, sampled, pending, None, cu, 4, out["acc"], out["next"], stream=stream)
+
+    def clear():
+        gpu.pool.state.copy_(start)
+        for t in out.values():
+            t.fill_(7)
+
+    def bits():
+        torch.cuda.synchronize()
+        return [t.cpu().numpy().tobytes() for t in (*out.values(), gpu.pool.state)]
+
+    clear()
+    step()
+    want = bits()
+    side = torch.cuda.Stream()
+    clear()
+    side.wait_stream(torch.cuda.current_stream())
+    step(side)  # (not the current stream)
+    assert bits() == want
+    graph = torch.cuda.CUDAGraph()
+    clear()
+    with torch.cuda.graph(graph):
+        step()
+    for _ in range(4):
+        clear()
+        graph.replay()
+        assert bits() == want
+        clear()
+        step()
+        assert bits() == want
