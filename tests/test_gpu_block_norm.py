@@ -133,7 +133,7 @@ OPTIONS = [
 
 @pytest.mark.parametrize("o", OPTIONS, ids=lambda o: "-".join(f"{k}={v}" for k, v in o.items()) or "plain")
 @pytest.mark.parametrize("rows,width", [(1, 1), (3, 7), (5, 512), (5, 513), (9, 1024), (3, 1031), (4, 2048), (3, 4096), (2, 4099), (2, 8192),
-                                        (2, 10000), (1, 16384), (1, 32768), (1, 32765)])
+                                        (2, 10000), (1, 16384), (1, 32768), (1, 32765), (5, 520), (2, 7001), (2, 12001)])
 def test_formula(o, rows, width):
     announce(f"block norm {rows} x {width} {o}")
     check(o, rows, width, seed=width)
