@@ -19,6 +19,12 @@
 // A kept token is one whose (value, index), as one number that falls with the value and rises with the index, is not
 // above the last kept one's. A list that would be longer than 4096 (thousands of equal values at a border) is not made:
 // choose then looks the borders up in the row itself, 11 bits of the key at a time.
+//
+// What bounds it: without filters the vector units (25 instructions a token, 10 of them in 64 bits: 1024 rows of 131072 bf16
+// 116 us, where reading them takes 44 to 54; 64-bit exponentials by a longer series and a table of 8: 165). With filters, 64
+// rows of 99991 fp32, 6 + 13 + 14 + 8 us: each pass's beginning (the row's ends, the bins' sums) and the weights; one row of 131072 3 + 5
+// + 6 + 6 us: dependent launches. Weights of bins only up to the border that a workgroup's own counts give top_k (13.7
+// against 12.8 us for weigh) cost more than they saved.
 
 #include <type_traits>
 
@@ -868,7 +874,8 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
     }
     if (!TILES && row.mode == kListed && plan.count > 0) {
       const auto place = [&](int at) { return place_of(row.seen(get(x + at)), at); };
-      if (plan.count <= kThreads) {  // a wave orders its 64; then each one's number is how many of every 64 lie before it
+      if (plan.count <= kThreads) {  // a wave orders its 64; then each one's number is how many of every 64 lie
+        // before it (286 entries 1.7 us; each against all others 6 to 8)
         unsigned long long* runs = sh.list + kThreads;
         const unsigned long long mine = tid < plan.count ? place(listed) : 0xFFFFFFFF00000000ull | tid;  // (behind all)
         int before = 0;
@@ -1075,8 +1082,8 @@ hipError_t launch_sample(const SampleArgs& a, hipStream_t s) {
   int bits = 0;
   while ((1 << bits) < a.vocab) ++bits;
   c.shift = 62 - bits < 51 ? 62 - bits : 51;
-  // about three workgroups a CU in the passes over all tokens (64 rows of 99991 with filters: 256 workgroups 54.5 us, 768 49,
-  // 2048 61)
+  // about three workgroups a CU in the passes over all tokens (64 rows of 99991 with filters, the kernels' sum: 576 workgroups
+  // 43.4 us, 768 40.1, 832 42.2, 1600 48.5)
   const int blocks = (z.tiles + kWaves - 1) / kWaves;
   const int want = (768 + a.rows - 1) / a.rows;
   c.groups = want < blocks ? want : blocks;

