@@ -238,3 +238,31 @@ def test_captured_and_on_another_stream():
 def test_no_rows():
     announce("block norm of no rows")
     call({}, make({}, 0, 64))
+
+
+def test_more_rows_than_a_launch_holds():
+    """2^21 + 5 rows go in two launches: every row as in calls of fewer rows, in place and with one gate for all."""
+    import torch
+
+    import gated_delta_rule_conv_amd as gdn
+
+    announce("block norm of 2^21 + 5 rows")
+    rows, width = (1 << 21) + 5, 3
+    g = torch.Generator().manual_seed(1)
+    x, r = (torch.randn(rows, width, generator=g).cuda() for _ in range(2))
+    gate, w = torch.randn(width, generator=g).cuda(), torch.randn(width, generator=g).cuda()
+    f32 = dict(in_dtype=gdn.GDN_F32, residual_dtype=gdn.GDN_F32, gate_dtype=gdn.GDN_F32, param_dtype=gdn.GDN_F32, out_dtype=gdn.GDN_F32)
+    dims = gdn.make_block_norm_dims(width, post_norm=True, scale=0.5, **f32)
+
+    def run(a, b):
+        h, y = r[a:b].clone(), torch.full((b - a, width), 7.0, device="cuda")
+        gdn.block_norm(dims, x[a:b], h, y, residual_out=h, gate=gate, pre_weight=w)
+        return h, y
+
+    whole = run(0, rows)
+    parts = [run(a, min(a + (1 << 20), rows)) for a in range(0, rows, 1 << 20)]
+    torch.cuda.synchronize()
+    for i in (0, 1):
+        assert torch.equal(whole[i], torch.cat([p[i] for p in parts]))
+    a = x.double() / torch.sqrt((x.double() ** 2).mean(1, keepdim=True) + 1e-6)
+    assert float((whole[0] - (r.double() + 0.5 * gate.double() * a)).abs().max()) < 1e-5
