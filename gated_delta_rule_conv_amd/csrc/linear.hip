@@ -120,7 +120,8 @@ hipError_t decode_t(const LinearArgs& a, int32_t m, hipStream_t s) {
 // state), the masked scores in that order again.
 //
 // Precision: with bf16 input every product has one operand that is exact in bf16. The other is fp32 and goes as three bf16
-// thirds, x = a + b + c exactly (8 bits each, cut, not rounded): three products, no rounding but those of fp32 sums. fp32 input
+// thirds, x = a + b + c exactly (8 bits each, cut, not rounded): three products, no rounding but those of fp32 sums. (Two thirds
+// alone, cut to 2^-15 of a term, would show where terms cancel, in bf16 outputs too.) fp32 input
 // goes through fp32 products. Sums of g are kept in base 2 as a multiple of 2^-8, exact up to 2^16, and a rest, so that
 // differences between tokens behind a strongly forgetting one keep their digits.
 //
@@ -213,9 +214,9 @@ struct Prod<uint16_t> {
     for (int e = 0; e < 4; ++e) o |= (y[e] & 0x7F807F80u) + 0x00800080u;
     return (o & 0x80008000u) != 0;
   }
-  __device__ __forceinline__ static Full load(const uint16_t* p, int plane, int skip) {
+  __device__ __forceinline__ static Full load(const uint16_t* p, int plane) {
     return Full{*reinterpret_cast<const bf16x8*>(p), *reinterpret_cast<const bf16x8*>(p + plane),
-                *reinterpret_cast<const bf16x8*>(p + (skip ? 1 : 2) * plane)};
+                *reinterpret_cast<const bf16x8*>(p + 2 * plane)};
   }
   __device__ __forceinline__ static f32x4 exact(const Exact& a, const Exact& b, const f32x4& acc) {
     return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, acc, 0, 0, 0);
@@ -243,7 +244,7 @@ struct Prod<float> {
     return !(fmaxf(fmaxf(fabsf(x[0]), fabsf(x[1])), fmaxf(fabsf(x[2]), fabsf(x[3]))) < __builtin_inff()) || x[0] != x[0] ||
            x[1] != x[1] || x[2] != x[2] || x[3] != x[3];
   }
-  __device__ __forceinline__ static Full load(const float* p, int, int) { return *reinterpret_cast<const f32x4*>(p); }
+  __device__ __forceinline__ static Full load(const float* p, int) { return *reinterpret_cast<const f32x4*>(p); }
   __device__ __forceinline__ static f32x4 exact(const Exact& a, const Exact& b, f32x4 acc) {
 #pragma unroll
     for (int e = 0; e < 4; ++e) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(a[e], b[e], acc, 0, 0, 0);
@@ -402,9 +403,7 @@ __global__ __launch_bounds__((LinearCfg<D, T, OUT>::THREADS), (sizeof(T) == 2 ? 
   using Exact = typename P::Exact;
   using Full = typename P::Full;
   constexpr int PITCH = C::PITCH, PROWS = C::PROWS;
-  // Outputs in bf16 (half a step: 2^-8) leave out the third parts, 2^-16 of a value, of what they alone are formed from.
-  constexpr int SKIP = sizeof(T) == 2 && sizeof(O) == 2 ? 1 : 0;
-  constexpr int PLANES = sizeof(T) == 2 ? 3 - SKIP : 1;
+  constexpr int PLANES = sizeof(T) == 2 ? 3 : 1;  // of the scores
   __shared__ __attribute__((aligned(16))) T kl[kChunk * PITCH];
   __shared__ __attribute__((aligned(16))) T vl[kChunk * PITCH];
   __shared__ __attribute__((aligned(16))) T ql[OUT ? kChunk * PITCH : 16];
@@ -658,7 +657,7 @@ __global__ __launch_bounds__((LinearCfg<D, T, OUT>::THREADS), (sizeof(T) == 2 ? 
           sf[t] = P::full(x);
         }
 #pragma unroll
-        for (int part = SKIP; part < P::PARTS; ++part)
+        for (int part = 0; part < P::PARTS; ++part)
 #pragma unroll
           for (int i = 0; i < 4; ++i)
 #pragma unroll
@@ -699,9 +698,9 @@ __global__ __launch_bounds__((LinearCfg<D, T, OUT>::THREADS), (sizeof(T) == 2 ? 
         }
 #pragma unroll
         for (int i = st * (C::STEP / 16); i < 4; ++i) {
-          const Full sc = P::load(pl + (16 * i + l16) * PROWS + (sizeof(T) == 2 ? 32 * st + 2 * h4 : 16 * st + h4), kChunk * PROWS, SKIP);
+          const Full sc = P::load(pl + (16 * i + l16) * PROWS + (sizeof(T) == 2 ? 32 * st + 2 * h4 : 16 * st + h4), kChunk * PROWS);
 #pragma unroll
-          for (int part = SKIP; part < P::PARTS; ++part)
+          for (int part = 0; part < P::PARTS; ++part)
 #pragma unroll
             for (int t = 0; t < C::VT; ++t) o[i][t] = P::right(v[t], sc, o[i][t], part);
         }
