@@ -1003,7 +1003,8 @@ __global__ __launch_bounds__(kThreads) void sample_choose_kernel(Call c) {
   if (i < vocab && c.a.prob) chance = row.weight(row.seen(own_v)) / static_cast<double>(total);
   if constexpr (TILES) {  // in the tile's own weights
     const double own = static_cast<double>(c.w.sums[static_cast<int64_t>(r) * c.tiles + tile]);
-    goal = fmin((goal - static_cast<double>(before)) * (own / static_cast<double>(tiles[tile])), own - 1.0);
+    // (below own, whatever the product is rounded to: own can be 2^60, where own - 1 is own)
+    goal = fmin((goal - static_cast<double>(before)) * (own / static_cast<double>(tiles[tile])), own * (1.0 - 0x1p-53));
     before = 0;
     row.against(value_of(c.w.ends[static_cast<int64_t>(r) * c.tiles + tile].x));
   }
