@@ -1,9 +1,10 @@
 // One token a row of logits from a given random number, gfx950 (include/gdn.h, gdn_sample).
 //
-// Weights are whole numbers: w = round(2^S e^((x - m) / T)), the exponential in 64 bits to 2^-39, S = 62 minus
+// Weights are whole numbers: w = round(2^S e^((x - m) / T)), the exponential in 64 bits to 2^-51 of the largest, S = 62 minus
 // the bits of the vocabulary's size, at most 51 (44 for 2^18 tokens). Their sums are then exact in any order, atomic or
 // not, so a row's token depends on nothing but the row, and a border (top_p's, or the random number's) is met within
-// 2^-S of the largest weight a token. Tokens whose weight is 0 do not count at all: they come last in the order.
+// 2^-S of the largest weight a token and a rounding of the sum to 64 bits. Tokens whose weight is 0 do not count at all: they
+// come last in the order.
 //
 // A row is cut into tiles of 512 tokens, a wave each. Without filters two launches over all rows:
 //   tiles     the largest value of every tile, and the tile's weight against it: logits are read once
@@ -130,16 +131,19 @@ struct Row {
     }
   }
   // 2^S e^((x - most) / T): t = 32 log2 of the exponential, its nearest whole number n and the rest f, |f| <= 1/2;
-  // 2^(t / 32) = 2^(n / 32) e^(f ln 2 / 32), the series good to 2^-39. (A NaN, also from minus infinity at an infinite T,
-  // is dropped by the largest of it and `low`.)
+  // 2^(t / 32) = 2^(n / 32) e^z, z = f ln 2 / 32, by the series to z^5 with z^6 / 720 taken into z^2 and z^4 (economised: on |z| <= a it
+  // is a^4 (3/2 (z/a)^2 - 9/16) z^2 / 720 to a^6 / 11520). Good to 2^-51.8, and a weight, with what t loses, to 2^-51 of the largest.
+  // (A NaN, also from minus infinity at an infinite T, is dropped by the largest of it and `low`.)
   __device__ __forceinline__ double weight(float x) const {
-    constexpr double c = 0.693147180559945309417 / kSteps;
+    constexpr double c = 0.693147180559945309417 / kSteps, a = c / 2;
+    constexpr double c2 = 1.0 / 2.0 - 9.0 / 16.0 * a * a * a * a / 720.0, c4 = 1.0 / 24.0 + 3.0 / 2.0 * a * a / 720.0;
     const double t = __builtin_fmax((static_cast<double>(x) - base) * per, low);
     const double whole = t + 0x1.8p52;
     const int n = static_cast<int>(__double_as_longlong(whole));
     const double f = t - (whole - 0x1.8p52);
-    double s = fma(f, c * c * c * c / 24.0, c * c * c / 6.0);
-    s = fma(s, f, c * c / 2.0);
+    double s = fma(f, c * c * c * c * c / 120.0, c4 * c * c * c * c);
+    s = fma(s, f, c * c * c / 6.0);
+    s = fma(s, f, c2 * c * c);
     s = fma(s, f, c);
     s = fma(s, f, 1.0);
     const double step = steps[n & (kSteps - 1)];

@@ -577,7 +577,9 @@ gdn_status gdn_block_norm(const gdn_block_norm_dims* dims, const void* x, int64_
  * T <= 0 (or NaN): the lowest index that has m, prob 1. A NaN logit counts as minus infinity; a row with nothing above
  * minus infinity gives token -1, prob 0. Beside an x of plus infinity only others like it weigh anything.
  * Weights are whole multiples of 2^-S (with temperature alone: of 2^-S of the largest among 512 neighbours) with
- * S = min(51, 62 - ceil(log2 vocab)): smaller ones are 0, and a row's token depends on nothing else in the call.
+ * S = min(51, 62 - ceil(log2 vocab)), from an exponential good to 2^-51 of the largest weight: smaller ones are 0, and a row's
+ * token depends on nothing else in the call. A border that a filter or u falls on is met to that and to a 64-bit
+ * rounding of the sum.
  *
  *  logits     [rows][vocab] in dtype (a gdn_dtype), row stride in elements, any alignment of the type.
  *  temperature, top_p, min_p  device fp32 [rows], top_k device int32 [rows]; NULL, or an entry that filters nothing
