@@ -254,9 +254,11 @@ hipError_t launch_v(const BlockNormArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Waves a row, and groups of 8 values a lane: the fewest idle lanes, then the most waves (64 Mi bf16 values of x, residual, gate,
+// Waves a row, and groups of 8 values a lane: of these shapes the one with the fewest idle lanes, then the most waves (64 Mi bf16 values of x, residual, gate,
 // h and y, TB/s: width 1024 with 4 waves 4.9, one wave with two groups 5.6; 2048 with 4 waves 5.7, with two groups 5.4;
-// 4104 with 16 waves 4.5, 8 with two groups 4.8; 16384 with two groups 4.8, four 3.9).
+// 4104 with 16 waves 4.5, 8 with two groups 4.8; 16384 with two groups 4.8, four 3.9). With four groups 16 waves have 128 registers
+// each, which suffices where 8 divides the width for bf16 throughout, and for one of x and residual in fp32 without a gate; the rest spills
+// (16 to 276 bytes a lane): 32768 wide 5.0 TB/s in bf16, 4.0 in fp32, 32767 wide 2.7 and 3.5.
 template <typename TX, typename TR, typename TZ, bool EIGHTS>
 hipError_t launch_w(const BlockNormArgs& a, hipStream_t s) {
   if (a.width <= 512) return launch_v<TX, TR, TZ, 1, 1, EIGHTS>(a, s);

@@ -128,11 +128,13 @@ hipError_t decode_t(const LinearArgs& a, int32_t m, hipStream_t s) {
 // Sequences are cut into tiles so that enough workgroups run: a first pass forms what each tile adds to the state, a scan the
 // state before each tile, and the last pass runs all tiles at once. Tiles begin at a sequence's own first token.
 //
-// What bounds it (16 k-heads, 32 v-heads, d = 128, bf16): 4096 tokens, tiles of 4 chunks, 26 + 13 + 46 us; the pack of 15717
-// tokens, fp32 outputs, tiles of 16, 62 + 16 + 189 us, where the bytes alone would take 111. No single thing bounds the last
-// pass: per wave and chunk 237 matrix, about 1090 vector and 141 LDS instructions, which a SIMD's two waves issue mostly one at a
+// What bounds it (16 k-heads, 32 v-heads, d = 128, bf16): 4096 tokens, tiles of 4 chunks, 24 + 13 + 48 us; the pack of 15717
+// tokens, fp32 outputs, tiles of 16, 54 + 15 + 164 us, where the bytes alone would take 111. No single thing bounds the last
+// pass: per wave and chunk 240 matrix, 1300 to 1400 vector and 143 LDS instructions, which a SIMD's two waves issue mostly one at a
 // time (a vector one every 5 cycles of a wave, LDS conflicts in 4 cycles of 10); leaving out stores, scores, loads or the
-// state's update takes off 6 to 18% each. Tried and slower: 8 waves of 16 columns (the pack 196 us against 180, 8-chunk tiles), vector
+// state's update takes off 6 to 18% each. All 512 workgroups of the 4096 tokens run at once, two a CU (7.1 waves of 8 on
+// average), a chunk of both in 20000 cycles. fp32 input: 4096 tokens 189 us, the pack 663, beside 56 and 214 for fp32 products of
+// S q and v k^T alone; at d = 128 one workgroup a CU (320 registers, 117 KiB of LDS). Tried and slower: 8 waves of 16 columns (the pack 196 us against 180, 8-chunk tiles), vector
 // instructions placed between matrix ones by scheduling groups (197 against 180).
 
 constexpr int kChunk = 64;
@@ -837,8 +839,9 @@ struct LinearSizes {
 // (the adding pass, whose work a longer tile would not lessen, then has the most workgroups), doubled until one head's work for a
 // workgroup of 4 waves comes to about two workgroups a CU, where more would wait for a place; and until the scan's
 // steps, one a tile, are few beside a tile's own. Calls, us, against the layer's own 8 chunks and whole sequences (32 heads,
-// d = 128, bf16): 1024 tokens 41 (69, 83), 4096 86 (86, 309), the pack of 15717 tokens 229 (251, 629), 16 sequences of 1024 166
-// (225, 147), 64 of them 599 (855, 573). Half the tiles of the last rule (32 heads): 64 sequences 592, one of 16384
+// d = 128, bf16): 1024 tokens 41 (74, 93), 4096 87 (83, 347), the pack of 15717 tokens 233 (250, 696), 16 sequences of 1024 181
+// (238, 161), 64 of them 636 (905, 623), one of 16384 among 31 of 256 417 (369, 1423). The rule knows the sum of the lengths alone:
+// where many sequences of one length fill the card by themselves, WHOLE is the better choice by 2 to 13%. Half the tiles of the last rule (32 heads): 64 sequences 592, one of 16384
 // among 31 of 256 354 (407); 8 heads, d = 64, one of 16384 tokens without the scan's rule 60 (49).
 LinearSizes sizes(int32_t hv, int32_t d, int32_t n, int32_t total, int32_t form) {
   LinearSizes z{};

@@ -21,10 +21,13 @@
 // above the last kept one's. A list that would be longer than 4096 (thousands of equal values at a border) is not made:
 // choose then looks the borders up in the row itself, 11 bits of the key at a time.
 //
-// What bounds it: without filters the vector units (25 instructions a token, 10 of them in 64 bits: 1024 rows of 131072 bf16
-// 116 us, where reading them takes 44 to 54; 64-bit exponentials by a longer series and a table of 8: 165). With filters, 64
+// What bounds it: without filters the vector units (26 instructions a token, 11 of them in 64 bits: 1024 rows of 131072 bf16
+// 120 us, where reading them takes 44 to 54; 64-bit exponentials by a longer series and a table of 8: 165). With filters, 64
 // rows of 99991 fp32, 6 + 13 + 14 + 8 us: each pass's beginning (the row's ends, the bins' sums) and the weights; one row of 131072 3 + 5
-// + 6 + 6 us: dependent launches. Weights of bins only up to the border that a workgroup's own counts give top_k (13.7
+// + 6 + 6 us: dependent launches. Bins are as wide as the row: a mask of large negative numbers in place of minus infinity makes them
+// wider and the list longer (131072 tokens, top_p alone: 34 us against 23). Rows without a list are one workgroup's, which reads them
+// up to nine times: 131072 equal values 0.80 ms with top_p, 0.37 with top_k, 2^20 of them 6.2 and 2.8 ms, whatever the
+// number of rows up to one a CU. Weights of bins only up to the border that a workgroup's own counts give top_k (13.7
 // against 12.8 us for weigh) cost more than they saved.
 
 #include <type_traits>

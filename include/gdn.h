@@ -499,7 +499,8 @@ gdn_status gdn_group_norm(const gdn_norm_dims* dims, const void* x, int64_t x_st
  *  q, k       [rows][Hk*d], v [rows][Hv*d] in dims->in_dtype, row strides in elements.
  *  g          [rows][Hv] fp32, row stride g_stride (>= Hv); g_stride 0: one row of Hv decays for all tokens.
  *             exp(g) is the share of the state that a token keeps: g <= 0, minus infinity included (nothing is
- *             kept: a new document inside a sequence). In the prefill a g below -128 counts as -128, which is 0 too.
+ *             kept: a new document inside a sequence). In the prefill a g below -128 counts as -128, which is 0 too, and a
+ *             decay over several tokens below 2^-126 may count as 0.
  *  o          [rows][Hv][d] contiguous in dims->out_dtype.
  *  state_ptrs device u64, fp32 [Hv][d_v][d_k] states, 16-byte aligned, updated in place. An entry of 0 marks an
  *             inactive slot (nothing read or written for it, its o rows untouched). Distinct slots.
@@ -534,7 +535,8 @@ gdn_status gdn_linear_decode(const gdn_dims* dims, const void* q, int64_t q_stri
  *   y = N(h) pre_weight + pre_bias
  * with N(x) = x / sqrt(mean(x^2) + eps), or, centered, (x - mean(x)) / sqrt(var(x) + eps), over the whole row. h is
  * rounded to residual_dtype where it is stored; y is the norm of h before that. Sums are fp32, under a power of two
- * where the squares leave its range (any finite x and h will do). A row of zeros with eps = 0 is 0 / 0: NaN.
+ * where the squares leave its range (any finite x and h will do; act(gate) a is formed before scale, and has to be a finite
+ * fp32 number too). A row of zeros with eps = 0 is 0 / 0: NaN.
  */
 typedef struct gdn_block_norm_dims {
   int32_t struct_size;    /* sizeof(gdn_block_norm_dims) as compiled by the caller */
@@ -588,7 +590,7 @@ gdn_status gdn_block_norm(const gdn_block_norm_dims* dims, const void* x, int64_
  *  uniform    device fp32 [rows] in [0, 1); others count as the nearest number there, NaN as 0.
  *  tokens     device int32 [rows].   prob: device fp32 [rows], or NULL.
  *  vocab      1 .. 2^20.   workspace: gdn_sample_workspace_size(rows, vocab) bytes, 256-byte aligned, contents ignored;
- *             may be NULL where that is 0.
+ *             may be NULL where that is 0. (28 KiB a row of it are for top_k and top_p.)
  */
 gdn_status gdn_sample_workspace_size(int32_t rows, int32_t vocab, size_t* bytes);
 gdn_status gdn_sample(const void* logits, int64_t stride, int32_t dtype, int32_t rows, int32_t vocab,
